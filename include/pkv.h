@@ -515,6 +515,126 @@ int pkv_swap_in(const pkv_bf16 *host_k, const pkv_bf16 *host_v, const int32_t *b
                 int head_dim, int32_t *d_status, void *stream);
 
 /* ------------------------------------------------------------------------
+ * The cache in 8 bits: a quantising write, its read-back, and the single-token
+ * decode over it.
+ *
+ * The pages have no counterpart (their caches are bf16); a decode is bound by
+ * the bytes of the cache (x321.org "The serving bottleneck is not just FLOPs",
+ * "Continuous batching is the other half of the story": the decode side is
+ * memory-bound), and 8 bits hold twice the tokens of 16.
+ *
+ * Format.  Every row (the head_dim keys, or values, of one token and KV head)
+ * is stored as head_dim e4m3 codes (1 sign, 4 exponent, 3 mantissa bits, no
+ * infinities, NaN = 0x7F or 0xFF, largest value 448) and one exponent byte b:
+ * code c stands for c * 2^(b - 127).  For a row x with a = max |x_i| over its
+ * finite values, b - 127 = e is the smallest integer with a <= 448 * 2^e,
+ * clamped to [-31, 31] (a = 0: -31), and code_i is x_i * 2^-e rounded to
+ * nearest even, held at +-448 (values above 448 * 2^31 = 9.6e11 saturate, those
+ * at or below 2^-41 become zero).  NaN and infinities become NaN.  The scale
+ * being a power of two, it costs no rounding of its own: a stored value is
+ * within 2^-4 of x_i relatively (or half a step of 2^-9 * 2^e, for values more
+ * than 2^13 below the row's largest), and every stored value is a bf16 number.
+ *   k_codes, v_codes  [num_blocks][num_kv_heads][block_size][head_dim] uint8
+ *   k_exps,  v_exps   [num_blocks][num_kv_heads][block_size] uint8
+ * Block ids, slots, tables and the allocator are those of the bf16 cache.  A
+ * copy-on-write or a swap moves whole blocks of bytes: pkv_block_copy and
+ * pkv_swap_out / _in take the code arrays as bf16 caches of head_dim / 2
+ * (head_dim a multiple of 16) and, for blocks of num_kv_heads * block_size a
+ * multiple of 16 exponent bytes, the exponent arrays as bf16 caches of one
+ * head, num_kv_heads * block_size / 16 rows and head_dim 8.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * pkv_write_quant -- quantise the keys and values of new tokens into their
+ * cache slots.
+ *
+ * For every token t < num_tokens with s = slot_mapping[t] >= 0 and every KV
+ * head h the rows k[t][h][:] and v[t][h][:] go, in the format above, to block
+ * s / block_size, head h, offset s % block_size.
+ *   k, v          device bf16, 16-byte aligned (read): token t's rows
+ *                 [num_kv_heads][head_dim] start t * k_stride (v_stride)
+ *                 elements after the first token's, so that both can be views
+ *                 of one projection's output; strides are multiples of 8 and
+ *                 at least num_kv_heads * head_dim
+ *   slot_mapping  device, [num_tokens] int64 (read)
+ *   the four cache arrays as above (written; code arrays 16-byte aligned)
+ * Slots >= num_blocks * block_size set PKV_STATUS_BAD_SLOT and are skipped.
+ * The non-negative slots of one call must be distinct: a slot that two tokens
+ * name holds undefined codes and exponents (other slots are not affected).
+ * Supported: head_dim a multiple of 16 up to 512, any block_size >= 1; other
+ * sizes return PKV_ERR_UNSUPPORTED.  num_tokens == 0 is a no-op.
+ */
+int pkv_write_quant(const pkv_bf16 *k, const pkv_bf16 *v, int64_t k_stride, int64_t v_stride,
+                    const int64_t *slot_mapping, int num_tokens, uint8_t *k_codes, uint8_t *v_codes,
+                    uint8_t *k_exps, uint8_t *v_exps, int num_blocks, int block_size, int num_kv_heads,
+                    int head_dim, int32_t *d_status, void *stream);
+
+/*
+ * pkv_read_quant -- read the rows of listed slots back into bf16: the inverse
+ * of pkv_write_quant (for instance a cached context, so that a prompt chunk's
+ * attention can run over a bf16 cache).
+ *
+ * For every t < num_tokens with s = slot_mapping[t] >= 0 and every KV head h:
+ * k[t][h][:] and v[t][h][:] = the values stored at slot s, exactly.  A slot may
+ * be listed any number of times.  Rows of negative slots are not written;
+ * slots >= num_blocks * block_size set PKV_STATUS_BAD_SLOT and their rows are
+ * not written.
+ *   k, v          device, [num_tokens][num_kv_heads][head_dim] bf16 (written)
+ * Exponent bytes outside [96, 158] (a slot that was never written) count as the
+ * nearer bound.  Sizes as pkv_write_quant.
+ */
+int pkv_read_quant(const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t *k_exps,
+                   const uint8_t *v_exps, const int64_t *slot_mapping, int num_tokens, pkv_bf16 *k,
+                   pkv_bf16 *v, int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                   int32_t *d_status, void *stream);
+
+/*
+ * Bytes of device workspace paged_attention_decode_quant needs for these sizes
+ * (0: none; also for invalid sizes, so check the decode call's return code).
+ * It depends on the sequences' number and longest length only through how many
+ * CTAs they can keep busy.  The library asks the current device for its number
+ * of SMs.
+ */
+size_t paged_attention_decode_quant_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                                   int head_dim, int max_seq_len);
+
+/*
+ * paged_attention_decode_quant -- attention of each sequence's newest token over
+ * its 8-bit cache: paged_attention_decode with q_len = 1 whose keys and values
+ * are the stored values.
+ *
+ * For sequence i with L = seq_lens[i] and query head g, KV head
+ * h = g / (num_q_heads / num_kv_heads):
+ *   out[i][0][g][:] = sum_{t < L} softmax_t(scale * q[i][0][g] . k_t) v_t,
+ * rounded to bf16 (nearest even); L = 0 gives zeros.  The newest token's rows
+ * are in the cache already (pkv_write_quant before this call).
+ *   q, out        device, [num_seqs][1][num_q_heads][head_dim] bf16
+ *   block_tables, max_blocks_per_seq, seq_lens, max_seq_len, d_status: as
+ *                 paged_attention_decode (table entries past a sequence's
+ *                 blocks may hold anything)
+ *   workspace     device scratch, 16-byte aligned, at least
+ *                 paged_attention_decode_quant_workspace_size(...) bytes (may
+ *                 be NULL when that is 0); its contents need not be
+ *                 initialised and are not preserved.  Calls that may overlap
+ *                 on the GPU need a workspace each.
+ * Slots past a sequence's end never contribute, whatever bytes they hold.  A
+ * NaN stored at a visible key or value makes the outputs that use it NaN.
+ * Block ids outside [0, num_blocks) set PKV_STATUS_BAD_BLOCK; the block's keys
+ * and values read as zeros.  Exponent bytes outside [96, 158] (which
+ * pkv_write_quant never stores) count as the nearer bound.
+ * Supported: head_dim in {64, 128}; block_size in {16, 32, 64, 128};
+ *   num_q_heads / num_kv_heads <= 16; num_seqs and num_kv_heads <= 65535.
+ *   Other sizes return PKV_ERR_UNSUPPORTED.
+ */
+int paged_attention_decode_quant(const pkv_bf16 *q, const uint8_t *k_codes, const uint8_t *v_codes,
+                                 const uint8_t *k_exps, const uint8_t *v_exps,
+                                 const int32_t *block_tables, int max_blocks_per_seq,
+                                 const int32_t *seq_lens, int num_seqs, int max_seq_len, int num_q_heads,
+                                 int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                 float scale, pkv_bf16 *out, void *workspace, size_t workspace_bytes,
+                                 int32_t *d_status, void *stream);
+
+/* ------------------------------------------------------------------------
  * Host block allocator: pool, block tables, refcounts, copy-on-write.
  *
  * Pages: a request grows by allocating more free blocks and returns them to

@@ -7,7 +7,11 @@ from .native import (  # noqa: F401
     BlockAllocator,
     PkvError,
     paged_attention_decode,
+    paged_attention_decode_quant,
+    paged_attention_decode_quant_workspace_size,
     paged_attention_workspace_size,
     pkv_block_copy,
+    pkv_read_quant,
     pkv_write,
+    pkv_write_quant,
 )

@@ -1,0 +1,292 @@
+// Quantising slot write (pkv_write_quant) and read-back (pkv_read_quant) of the
+// 8-bit cache.
+//
+// Both are data movement with a little arithmetic, bound by HBM: per row of d
+// values a write reads 2 d bytes and stores d + 1, a read-back the reverse.  A
+// group of lanes takes one (token, KV head): its key row and its value row, 16
+// values (32 bytes of bf16, 16 bytes of codes) per lane, so the row's maximum
+// is a few shuffles and a row is read once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "internal.h"
+#include "pkv.h"
+#include "ptx.cuh"
+#include "quant.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxHeadDim = 512;  // 32 lanes x 16 values
+
+struct RowParams {
+  const int64_t *slots;
+  int64_t num_slots;  // num_blocks * block_size
+  int64_t rows;       // num_tokens * num_kv_heads
+  int64_t k_stride, v_stride;  // elements between tokens (write)
+  int32_t *status;
+  int num_kv_heads, block_size, chunks;  // chunks: head_dim / 16
+  int narrow;  // rows and num_slots fit 32 bits: divide in 32 bits
+};
+
+struct CachePtrs {
+  uint4 *k_codes, *v_codes;
+  uint8_t *k_exps, *v_exps;
+};
+
+// The bf16 pair's magnitudes, non-finite ones replaced by 0.
+__device__ __forceinline__ uint32_t finite_magnitudes(uint32_t v) {
+  const uint32_t m = v & 0x7FFF7FFFu;
+  return ((m & 0xFFFFu) >= 0x7F80u ? 0u : m & 0xFFFFu) | ((m >> 16) >= 0x7F80u ? 0u : m & 0xFFFF0000u);
+}
+
+// This row's token and head, and its slot; false: nothing to do.
+__device__ __forceinline__ bool locate(const RowParams &p, int64_t row, bool report, int64_t *token, int *head,
+                                       int64_t *cache_row) {
+  int64_t t;
+  if (p.narrow) t = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.num_kv_heads);
+  else t = row / p.num_kv_heads;
+  const int h = static_cast<int>(row - t * p.num_kv_heads);
+  const int64_t slot = p.slots[t];
+  if (slot < 0) return false;
+  if (slot >= p.num_slots) {
+    if (report && h == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_SLOT);
+    return false;
+  }
+  int64_t blk;
+  if (p.narrow) blk = static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.block_size);
+  else blk = slot / p.block_size;
+  *token = t;
+  *head = h;
+  *cache_row = (blk * p.num_kv_heads + h) * p.block_size + (slot - blk * p.block_size);
+  return true;
+}
+
+// 16 bf16 of a row (two 16-byte loads) -> 16 codes, given the row's exponent.
+__device__ __forceinline__ uint4 encode(const uint4 &a, const uint4 &b, float inv) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t half[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t v = w[2 * i + j];
+      half[j] = quant::to_e4m3x2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xFFFF0000u) * inv);
+    }
+    c[i] = half[0] | (half[1] << 16);
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// The largest magnitude of a lane's 16 values, as bf16 bits in either half.
+__device__ __forceinline__ uint32_t magnitude_max(const uint4 &a, const uint4 &b) {
+  constexpr uint32_t M = 0x7FFF7FFFu;
+  uint32_t m = __vmaxu2(__vmaxu2(a.x & M, a.y & M), __vmaxu2(a.z & M, a.w & M));
+  return __vmaxu2(m, __vmaxu2(__vmaxu2(b.x & M, b.y & M), __vmaxu2(b.z & M, b.w & M)));
+}
+
+template <int W>
+__device__ __forceinline__ uint32_t group_max(uint32_t m) {
+#pragma unroll
+  for (int off = W / 2; off; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// Infinities become NaN (a row that holds any is rare: only then).
+__device__ __forceinline__ uint32_t infinities_to_nan(uint32_t v) {
+  const uint32_t m = v & 0x7FFF7FFFu;
+  return v | ((m & 0xFFFFu) == 0x7F80u ? 0x40u : 0u) | ((m >> 16) == 0x7F80u ? 0x400000u : 0u);
+}
+__device__ __forceinline__ uint4 infinities_to_nan(const uint4 &a) {
+  return make_uint4(infinities_to_nan(a.x), infinities_to_nan(a.y), infinities_to_nan(a.z), infinities_to_nan(a.w));
+}
+__device__ __forceinline__ uint4 finite_magnitudes(const uint4 &a) {
+  return make_uint4(finite_magnitudes(a.x), finite_magnitudes(a.y), finite_magnitudes(a.z), finite_magnitudes(a.w));
+}
+
+// One row's 16 values per lane -> codes and exponent byte, W lanes together.
+template <int W>
+__device__ __forceinline__ uint4 quantise(uint4 a, uint4 b, uint8_t *exp_byte) {
+  uint32_t top = group_max<W>(magnitude_max(a, b));
+  if (__any_sync(0xffffffffu, top >= 0x7F80u)) {  // a NaN or infinity somewhere in the warp's rows
+    top = group_max<W>(magnitude_max(finite_magnitudes(a), finite_magnitudes(b)));
+    a = infinities_to_nan(a);
+    b = infinities_to_nan(b);
+  }
+  const int e = quant::row_exponent(top);
+  *exp_byte = static_cast<uint8_t>(e + quant::kExpBias);
+  return encode(a, b, quant::pow2i(-e));
+}
+
+// W lanes per (token, KV head) row pair: lane c of the group holds values
+// 16 c .. 16 c + 15 of the key row and of the value row.
+template <int W>
+__global__ void __launch_bounds__(kThreads) write_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
+                                                         const RowParams p, const CachePtrs out) {
+  // the grid queued behind this one may become resident now (it waits for this
+  // grid's writes before it reads the cache)
+  grid_launch_dependents();
+  const int c = threadIdx.x % W;
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kThreads / W);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W;
+  // every lane of a warp runs the same number of rounds (the shuffles below)
+  const int64_t rounds = (p.rows + groups - 1) / groups;
+  for (int64_t i = 0; i < rounds; ++i) {
+    const int64_t row = first + i * groups;
+    int64_t t = 0, dst = 0;
+    int h = 0;
+    const bool live = row < p.rows && locate(p, row, c == 0, &t, &h, &dst);
+    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a, d = a, e = a;
+    if (live && c < p.chunks) {
+      const uint4 *ks = k + (t * p.k_stride) / 8 + (static_cast<int64_t>(h) * p.chunks + c) * 2;
+      const uint4 *vs = v + (t * p.v_stride) / 8 + (static_cast<int64_t>(h) * p.chunks + c) * 2;
+      a = ks[0];
+      b = ks[1];
+      d = vs[0];
+      e = vs[1];
+    }
+    uint8_t ke, ve;
+    const uint4 kc = quantise<W>(a, b, &ke), vc = quantise<W>(d, e, &ve);
+    if (live && c < p.chunks) {
+      out.k_codes[dst * p.chunks + c] = kc;
+      out.v_codes[dst * p.chunks + c] = vc;
+      if (c == 0) {
+        out.k_exps[dst] = ke;
+        out.v_exps[dst] = ve;
+      }
+    }
+  }
+}
+
+// 4 codes -> 4 bf16 (two words), times the row's power of two: exact.
+__device__ __forceinline__ uint2 decode4(uint32_t codes, float scale) {
+  const uint32_t lo = quant::e4m3x2_to_f16x2(codes), hi = quant::e4m3x2_hi_to_f16x2(codes);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+  return make_uint2(pack_bf16x2(a.x * scale, a.y * scale), pack_bf16x2(b.x * scale, b.y * scale));
+}
+
+__device__ __forceinline__ void decode16(const uint4 &codes, float scale, uint4 *dst) {
+  const uint2 a = decode4(codes.x, scale), b = decode4(codes.y, scale);
+  const uint2 c = decode4(codes.z, scale), d = decode4(codes.w, scale);
+  dst[0] = make_uint4(a.x, a.y, b.x, b.y);
+  dst[1] = make_uint4(c.x, c.y, d.x, d.y);
+}
+
+// W lanes per (token, KV head) row pair, as in write_kernel.
+template <int W>
+__global__ void __launch_bounds__(kThreads) read_kernel(uint4 *__restrict__ k, uint4 *__restrict__ v,
+                                                        const RowParams p, const CachePtrs in) {
+  grid_launch_dependents();
+  const int c = threadIdx.x % W;
+  if (c >= p.chunks) return;
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kThreads / W);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W; row < p.rows;
+       row += groups) {
+    int64_t t, src;
+    int h;
+    if (!locate(p, row, c == 0, &t, &h, &src)) continue;
+    const uint4 kc = in.k_codes[src * p.chunks + c], vc = in.v_codes[src * p.chunks + c];
+    const float ks = quant::pow2i(quant::clamp_exp(in.k_exps[src]));
+    const float vs = quant::pow2i(quant::clamp_exp(in.v_exps[src]));
+    decode16(kc, ks, k + (row * p.chunks + c) * 2);
+    decode16(vc, vs, v + (row * p.chunks + c) * 2);
+  }
+}
+
+int check_rows(const void *k, const void *v, const int64_t *slots, int num_tokens, const void *k_codes,
+               const void *v_codes, const void *k_exps, const void *v_exps, int num_blocks, int block_size,
+               int num_kv_heads, int head_dim) {
+  if (num_tokens < 0 || num_blocks < 0 || block_size < 1 || num_kv_heads < 1 || head_dim < 1) return PKV_ERR_ARG;
+  if (head_dim % 16 != 0 || head_dim > kMaxHeadDim) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PKV_OK;
+  if (!k || !v || !slots || !k_codes || !v_codes || !k_exps || !v_exps) return PKV_ERR_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(v_codes) ||
+      (reinterpret_cast<uintptr_t>(slots) & 7u))
+    return PKV_ERR_ARG;
+  return PKV_OK;
+}
+
+RowParams row_params(const int64_t *slots, int num_tokens, int num_blocks, int block_size, int num_kv_heads,
+                     int head_dim, int32_t *status) {
+  RowParams p{};
+  p.slots = slots;
+  p.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+  p.rows = static_cast<int64_t>(num_tokens) * num_kv_heads;
+  p.status = status;
+  p.num_kv_heads = num_kv_heads;
+  p.block_size = block_size;
+  p.chunks = head_dim / 16;
+  p.narrow = p.rows <= 0xffffffffll && p.num_slots <= 0xffffffffll;
+  return p;
+}
+
+int row_grid(int64_t rows, int lanes) {
+  const int64_t per = kThreads / lanes;
+  const int64_t blocks = (rows + per - 1) / per, cap = static_cast<int64_t>(num_sms()) * 8;
+  return static_cast<int>(blocks < cap ? blocks : cap);
+}
+
+// lanes per row: the power of two that covers head_dim / 16
+template <typename F>
+void by_lanes(int chunks, F &&f) {
+  if (chunks <= 1) f(std::integral_constant<int, 1>());
+  else if (chunks <= 2) f(std::integral_constant<int, 2>());
+  else if (chunks <= 4) f(std::integral_constant<int, 4>());
+  else if (chunks <= 8) f(std::integral_constant<int, 8>());
+  else if (chunks <= 16) f(std::integral_constant<int, 16>());
+  else f(std::integral_constant<int, 32>());
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+int pkv_write_quant(const pkv_bf16 *k, const pkv_bf16 *v, int64_t k_stride, int64_t v_stride,
+                    const int64_t *slot_mapping, int num_tokens, uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_exps,
+                    uint8_t *v_exps, int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                    int32_t *d_status, void *stream) {
+  const int rc = pkv::check_rows(k, v, slot_mapping, num_tokens, k_codes, v_codes, k_exps, v_exps, num_blocks,
+                                 block_size, num_kv_heads, head_dim);
+  if (rc != PKV_OK) return rc;
+  const int64_t width = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (k_stride < width || v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0) return PKV_ERR_ARG;
+  if (num_tokens == 0) return PKV_OK;
+  pkv::RowParams p = pkv::row_params(slot_mapping, num_tokens, num_blocks, block_size, num_kv_heads, head_dim, d_status);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  const pkv::CachePtrs out{reinterpret_cast<uint4 *>(k_codes), reinterpret_cast<uint4 *>(v_codes), k_exps, v_exps};
+  pkv::by_lanes(p.chunks, [&](auto w) {
+    constexpr int W = decltype(w)::value;
+    pkv::write_kernel<W><<<pkv::row_grid(p.rows, W), pkv::kThreads, 0, pkv::as_stream(stream)>>>(
+        reinterpret_cast<const uint4 *>(k), reinterpret_cast<const uint4 *>(v), p, out);
+  });
+  return pkv::check_launch();
+}
+
+int pkv_read_quant(const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t *k_exps, const uint8_t *v_exps,
+                   const int64_t *slot_mapping, int num_tokens, pkv_bf16 *k, pkv_bf16 *v, int num_blocks,
+                   int block_size, int num_kv_heads, int head_dim, int32_t *d_status, void *stream) {
+  const int rc = pkv::check_rows(k, v, slot_mapping, num_tokens, k_codes, v_codes, k_exps, v_exps, num_blocks,
+                                 block_size, num_kv_heads, head_dim);
+  if (rc != PKV_OK || num_tokens == 0) return rc;
+  const pkv::RowParams p =
+      pkv::row_params(slot_mapping, num_tokens, num_blocks, block_size, num_kv_heads, head_dim, d_status);
+  const pkv::CachePtrs in{reinterpret_cast<uint4 *>(const_cast<uint8_t *>(k_codes)),
+                          reinterpret_cast<uint4 *>(const_cast<uint8_t *>(v_codes)), const_cast<uint8_t *>(k_exps),
+                          const_cast<uint8_t *>(v_exps)};
+  pkv::by_lanes(p.chunks, [&](auto w) {
+    constexpr int W = decltype(w)::value;
+    pkv::read_kernel<W><<<pkv::row_grid(p.rows, W), pkv::kThreads, 0, pkv::as_stream(stream)>>>(
+        reinterpret_cast<uint4 *>(k), reinterpret_cast<uint4 *>(v), p, in);
+  });
+  return pkv::check_launch();
+}
+
+}  // extern "C"

@@ -8,6 +8,7 @@ if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -106,6 +107,14 @@ SIGNATURES = {
                               _c_ptr, _c_ptr]),
     "pkv_swap_in": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_int, _c_int, _c_int, _c_int,
                              _c_ptr, _c_ptr]),
+    "pkv_write_quant": (_c_int, [_c_ptr, _c_ptr, _c_i64, _c_i64, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                 _c_int, _c_int, _c_int, _c_int, _c_ptr, _c_ptr]),
+    "pkv_read_quant": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_int, _c_int,
+                                _c_int, _c_int, _c_ptr, _c_ptr]),
+    "paged_attention_decode_quant_workspace_size": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "paged_attention_decode_quant": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_int,
+                                              _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_ptr,
+                                              _c_ptr, _c_size, _c_ptr, _c_ptr]),
     "pkv_seq_append_batch": (_c_int, [_c_ptr, _c_ptr, _c_int, _c_int, _c_ptr]),
     "pkv_seq_append_tokens": (_c_int, [_c_ptr, ctypes.c_int64, _c_ptr, _c_int, _c_ptr, ctypes.POINTER(_c_int)]),
     "pkv_prefix_cache_stats": (_c_int, [_c_ptr, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64)]),
@@ -505,6 +514,121 @@ def paged_attention_decode_static_scratch(q, k_cache, v_cache, block_tables, seq
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B,
         int(max_seq_len), q_len, Hq, Hkv, d, bs, NB, float(scale), int(partition_size), _ptr(out),
         _ptr(d_status), _stream(stream, dev)), "paged_attention_decode_static_scratch")
+
+
+# ------------------------------------------------------- the cache in 8 bits
+def _quant_cache(k_codes, v_codes, k_exps, v_exps):
+    """The cache's shape (NB, Hkv, bs, d) and device, its four tensors checked."""
+    dev = k_codes.device
+    for t, n in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+        _need(t, torch.float8_e4m3fn, n, dev)
+    for t, n in ((k_exps, "k_exps"), (v_exps, "v_exps")):
+        _need(t, torch.uint8, n, dev)
+    if k_codes.dim() != 4 or v_codes.shape != k_codes.shape or k_exps.shape != k_codes.shape[:3] \
+            or v_exps.shape != k_exps.shape:
+        raise ValueError("shape mismatch: codes [NB, Hkv, bs, d] and exponents [NB, Hkv, bs] expected")
+    return k_codes.shape, dev
+
+
+def _status(d_status, dev):
+    if d_status is not None:
+        _need(d_status, torch.int32, "d_status", dev)
+        if d_status.numel() < 1:
+            raise ValueError("d_status: one int32 expected")
+    return _ptr(d_status)
+
+
+def _on(dev):
+    """Context that makes ``dev`` current (its kernels are launched from there); nothing to do when it is."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _need_cuda(dev):
+    if dev.type != "cuda":
+        raise ValueError(f"the cache must be on a CUDA device, got {dev}")
+
+
+def _token_rows(t, name, shape, dev):
+    """The stride in elements between tokens of [T, Hkv, d] rows whose own values are dense."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    T, Hkv, d = shape
+    if T <= 1 and t.is_contiguous():
+        return Hkv * d
+    s = t.stride()
+    if T > 0 and (s[2] != 1 and d > 1 or s[1] != d and Hkv > 1 or s[0] < Hkv * d or s[0] % 8):
+        raise ValueError(f"{name}: each token's [Hkv, d] rows must be dense, tokens a multiple of 8 elements apart")
+    return s[0] if T > 1 else Hkv * d
+
+
+def pkv_write_quant(k, v, slot_mapping, k_codes, v_codes, k_exps, v_exps, d_status=None, stream=None):
+    """Quantise new tokens into an 8-bit cache.  k, v: [T, Hkv, d] bf16, each token's rows dense (views of a
+    fused projection's output are fine); slot_mapping: [T] int64, negative: skip; codes [NB, Hkv, bs, d]
+    float8_e4m3fn, exponents [NB, Hkv, bs] uint8 (device).  d: a multiple of 16."""
+    (NB, Hkv, bs, d), dev = _quant_cache(k_codes, v_codes, k_exps, v_exps)
+    _need(slot_mapping, torch.int64, "slot_mapping", dev)
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping: [T] expected")
+    T = slot_mapping.shape[0]
+    ks, vs = _token_rows(k, "k", (T, Hkv, d), dev), _token_rows(v, "v", (T, Hkv, d), dev)
+    _need_cuda(dev)
+    with _on(dev):
+        _check(lib().pkv_write_quant(_ptr(k), _ptr(v), ks, vs, _ptr(slot_mapping), T, _ptr(k_codes), _ptr(v_codes),
+                                     _ptr(k_exps), _ptr(v_exps), NB, bs, Hkv, d, _status(d_status, dev),
+                                     _stream(stream, dev)), "pkv_write_quant")
+
+
+def pkv_read_quant(k_codes, v_codes, k_exps, v_exps, slot_mapping, k, v, d_status=None, stream=None):
+    """Rows of listed slots of an 8-bit cache, exactly, into k, v [T, Hkv, d] bf16 (rows of negative slots stay
+    as they are); the cache as in ``pkv_write_quant``."""
+    (NB, Hkv, bs, d), dev = _quant_cache(k_codes, v_codes, k_exps, v_exps)
+    _need(slot_mapping, torch.int64, "slot_mapping", dev)
+    _need(k, torch.bfloat16, "k", dev)
+    _need(v, torch.bfloat16, "v", dev)
+    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+    if k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
+        raise ValueError("shape mismatch between k/v, slot_mapping [T] and the cache")
+    _need_cuda(dev)
+    with _on(dev):
+        _check(lib().pkv_read_quant(_ptr(k_codes), _ptr(v_codes), _ptr(k_exps), _ptr(v_exps), _ptr(slot_mapping), T,
+                                    _ptr(k), _ptr(v), NB, bs, Hkv, d, _status(d_status, dev), _stream(stream, dev)),
+               "pkv_read_quant")
+
+
+def paged_attention_decode_quant_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len):
+    return int(lib().paged_attention_decode_quant_workspace_size(int(num_seqs), int(num_q_heads), int(num_kv_heads),
+                                                                 int(head_dim), int(max_seq_len)))
+
+
+def paged_attention_decode_quant(q, k_codes, v_codes, k_exps, v_exps, block_tables, seq_lens, max_seq_len, scale, out,
+                                 workspace=None, d_status=None, stream=None):
+    """Single-token decode over an 8-bit cache: q, out [B, 1, Hq, d] bf16; the cache as in ``pkv_write_quant``;
+    tables [B, max_blocks] int32; lens [B] int32; workspace: a device buffer of
+    ``paged_attention_decode_quant_workspace_size`` bytes (one per call that may overlap)."""
+    (NB, Hkv, bs, d), dev = _quant_cache(k_codes, v_codes, k_exps, v_exps)
+    _need(q, torch.bfloat16, "q", dev)
+    _need(out, torch.bfloat16, "out", dev)
+    _need(block_tables, torch.int32, "block_tables", dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
+    if q.dim() != 4 or q.shape[1] != 1 or q.shape[3] != d or out.shape != q.shape or block_tables.dim() != 2 \
+            or block_tables.shape[0] != q.shape[0] or seq_lens.shape != q.shape[:1]:
+        raise ValueError("shape mismatch")
+    ws_bytes = 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {dev}")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _need_cuda(dev)
+    with _on(dev):
+        _check(lib().paged_attention_decode_quant(
+            _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_exps), _ptr(v_exps), _ptr(block_tables),
+            block_tables.shape[1], _ptr(seq_lens), q.shape[0], int(max_seq_len), q.shape[2], Hkv, d, bs, NB,
+            float(scale), _ptr(out), _ptr(workspace), ws_bytes, _status(d_status, dev), _stream(stream, dev)),
+            "paged_attention_decode_quant")
 
 
 # ------------------------------------------------------------- allocator
