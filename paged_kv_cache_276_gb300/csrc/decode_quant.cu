@@ -2,14 +2,39 @@
 //
 // Math: with key codes kc_t, value codes vc_t (e4m3) and the rows' powers of two
 // 2^ke_t, 2^ve_t:  s_t = scale 2^ke_t (q . kc_t),  out = sum_t softmax_t(s) 2^ve_t vc_t.
+// In log2 units x_t = log2(e) s_t + ve_t, with any reference R:
+//   w_t = 2^(x_t - R)  (the weight with the value row's scale folded in),
+//   O = sum_t w_t vc_t,  l = sum_t w_t 2^-ve_t,  out = O / l,
+// so codes enter the products as they are stored and a scale costs one FMA per
+// score.  e4m3 values are exact in fp16, so both products run on fp16 MMA with
+// fp32 accumulators; the queries are scaled by a power of two per head to use
+// fp16's range (bf16 has fewer significant bits: exact but for values 2^-31
+// and more below the head's largest).  The weights' rounding to fp16 (2^-11)
+// enters O only; l sums them unrounded, since a key whose value row is tiny can
+// hold most of the softmax at a negligible w.
 //
-// One CTA per (KV head, sequence): four warps take the tokens in turn, each with
-// a running maximum and sum, and are joined in shared memory at the end.
+// Work: the cache is read once, so the kernel is bound by HBM; it has to keep
+// every SM streaming however the lengths are spread.  All (sequence, KV head)
+// runs are cut into units of kUnitBytes of keys (32 tokens at head_dim 128, 64
+// at 64) and laid end to end; every warp of a grid of one CTA per SM takes an
+// equal, contiguous range of units.  The lengths' prefix sums are taken by every
+// CTA at its start, so there is no host-built list and a captured graph follows
+// its lengths.  A warp streams its units through a ring of its own (TMA with the
+// 128-byte swizzle for the codes, cp.async for the exponents, one mbarrier per
+// stage) and refills a stage right after it has used it: no barrier between
+// warps until the end.  A run that a warp holds whole is written at once; pieces
+// of a run are joined in shared memory at the CTA's end, and runs that span
+// CTAs through the workspace by a second kernel.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <cstdint>
+#include <utility>
 
 #include "internal.h"
 #include "pkv.h"
@@ -19,94 +44,769 @@
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kMaxGroup = 16;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kUnitBytes = 4096;  // key codes of one unit; the value codes take as many
+// A weight is 2^(x - R): R is set 7 below the largest x when it moves, and moves
+// when an x exceeds it by more than 15, so weights stay below 2^15 (fp16 holds
+// 65504) and most units skip the rescale.
+constexpr float kHeadroom = 7.f, kSlack = 15.f;
 
 struct Params {
   const __nv_bfloat16 *q;
-  const uint8_t *k_codes, *v_codes, *k_exps, *v_exps;
+  const uint8_t *k_exps, *v_exps;
   const int32_t *block_tables, *seq_lens;
   __nv_bfloat16 *out;
+  float *ws;      // [grid][2] pieces of runs that span CTAs, then [grid] descriptors
+  int4 *ws_desc;  // {sequence, KV head, last CTA of the run, 1} of the run that leaves CTA c, or .w = 0
   int32_t *status;
-  int max_blocks, max_len, num_q_heads, num_kv_heads, group, num_blocks, block_size;
+  int num_seqs, max_blocks, max_len, num_q_heads, num_kv_heads, group, num_blocks;
   float scale_log2;
 };
 
-__device__ __forceinline__ float code_value(uint8_t c) {
-  const uint32_t h = quant::e4m3x2_to_f16x2(c);
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
+template <int D, int NT>
+struct Shape {
+  static constexpr int kTokens = kUnitBytes / D;  // tokens of a unit
+  static constexpr int kStages = 2;
+  static constexpr int kTileFloats = NT * 8 * D;  // O of one piece, in accumulator order
+  static constexpr int kPieceFloats = kTileFloats + 2 * NT * 8;  // ..., m[cols], l[cols]
+  static constexpr int kRingBytes = kStages * 2 * kUnitBytes;
+  static constexpr int kExpBytes = kStages * 2 * kTokens;
+  static constexpr int kMetaBytes = kStages * (16 + 8);  // an int4 and a barrier per stage
+  static constexpr int kWarpBytes = kRingBytes + kExpBytes + kMetaBytes + kPieceFloats * 4;
+  // as many warps as shared memory (227 KB a CTA) holds rings for
+  static constexpr int kWarps = D == 128 ? (NT == 1 ? 11 : 9) : (NT == 1 ? 12 : 10);
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kSmemBytes = 1024 + kWarps * kWarpBytes;
+  static_assert(kPieceFloats * 4 <= kRingBytes, "a warp's last piece goes over its ring");
+  static_assert(kSmemBytes + kThreads * 8 + kWarps * 24 + 64 <= 227 * 1024, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) decode_simple(const Params p) {
-  constexpr int PER = D / 32;
-  __shared__ float so[kWarps][D], sm[kWarps], sl[kWarps];
-  const int h = blockIdx.x, seq = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_launch_dependents();
-  grid_dependency_wait();
-  int L = p.seq_lens[seq];
-  const long long cap_tbl = static_cast<long long>(p.max_blocks) * p.block_size;
-  const int cap = static_cast<int>(cap_tbl < p.max_len ? cap_tbl : p.max_len);
-  if (L < 0 || L > cap) {
-    if (h == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_LEN);
-    L = L < 0 ? 0 : cap;
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ int lds_u8(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+  return static_cast<int>(r);
+}
+
+// 16 bytes global -> shared by this thread, asynchronously.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on `bar` once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Shared-memory address of byte `off` of a unit staged with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz(uint32_t base, uint32_t off) { return base + (off ^ ((off >> 3) & 0x70u)); }
+
+__device__ __forceinline__ int capped_len(const Params &p, int bs) {
+  const long long cap = static_cast<long long>(p.max_blocks) * bs;
+  return static_cast<int>(cap < p.max_len ? cap : p.max_len);
+}
+
+// The running softmax of one warp's piece: its columns are the query heads.
+template <int D, int NT>
+struct Acc {
+  float r[NT][2];  // reference R per column (the thread's two columns of each 8)
+  float l[NT][2];  // this thread's part of the sum
+  float o[D / 16][NT][4];
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      r[nt][0] = r[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int md = 0; md < D / 16; ++md) o[md][nt][0] = o[md][nt][1] = o[md][nt][2] = o[md][nt][3] = 0.f;
+    }
   }
-  for (int g = 0; g < p.group; ++g) {
-    const size_t row = (static_cast<size_t>(seq) * p.num_q_heads + h * p.group + g) * D;
-    float q[PER], o[PER], m = -INFINITY, l = 0.f;
-    for (int i = 0; i < PER; ++i) q[i] = __bfloat162float(p.q[row + lane * PER + i]), o[i] = 0.f;
-    for (int t = warp; t < L; t += kWarps) {
-      const int b = p.block_tables[static_cast<size_t>(seq) * p.max_blocks + t / p.block_size];
-      float s = 0.f, v[PER];
-      for (int i = 0; i < PER; ++i) v[i] = 0.f;
-      if (b >= 0 && b < p.num_blocks) {
-        const size_t r = (static_cast<size_t>(b) * p.num_kv_heads + h) * p.block_size + t % p.block_size;
-        const float kf = quant::pow2i(quant::clamp_exp(p.k_exps[r])), vf = quant::pow2i(quant::clamp_exp(p.v_exps[r]));
-        for (int i = 0; i < PER; ++i) {
-          s += q[i] * code_value(p.k_codes[r * D + lane * PER + i]);
-          v[i] = code_value(p.v_codes[r * D + lane * PER + i]) * vf;
+};
+
+// The group's queries as B fragments.  The product over head_dim takes its
+// terms in the order a key row's bytes are read in: lane t of a quad holds
+// values [t D/4, (t + 1) D/4) of each row, four to a k-step.  cf: per column of
+// the accumulators, the factor that undoes the queries' power of two and
+// applies the scale (in log2 units).
+template <int D, int NT>
+__device__ __forceinline__ void load_queries(const Params &p, int seq, int h, uint32_t (&qf)[NT][D / 16][2],
+                                             float (&cf)[NT][2], int lane) {
+  const int g4 = lane >> 2, c4 = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int col = nt * 8 + g4;
+    const bool real = col < p.group;
+    const uint4 *src = reinterpret_cast<const uint4 *>(
+        p.q + (static_cast<size_t>(seq) * p.num_q_heads + static_cast<size_t>(h) * p.group + (real ? col : 0)) * D +
+        c4 * (D / 4));
+    uint32_t w[D / 8];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 x = real ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+      w[4 * i] = x.x;
+      w[4 * i + 1] = x.y;
+      w[4 * i + 2] = x.z;
+      w[4 * i + 3] = x.w;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // largest magnitude to [2^14, 2^15); queries below 2^-86 keep a smaller one
+    const int shift = min(100, 14 + 127 - static_cast<int>(top >> 7));
+    const float up = quant::pow2i(shift);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t v = w[ks * 2 + b];
+        qf[nt][ks][b] = pack_f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+      }
+    const float f = p.scale_log2 * quant::pow2i(-shift);
+    cf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c4);
+    cf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * c4 + 4);
+  }
+}
+
+// One staged unit: scores, running softmax, product with the values.
+//   valid: tokens of the unit before the sequence's end (1 .. kTokens); staged
+//          bytes behind them may be anything.
+template <int D, int NT>
+__device__ __forceinline__ void attend_unit(Acc<D, NT> &acc, const uint32_t (&qf)[NT][D / 16][2],
+                                            const float (&cf)[NT][2], uint32_t kb, uint32_t vb, uint32_t keb,
+                                            uint32_t veb, int valid, int lane) {
+  constexpr int MT = Shape<D, NT>::kTokens / 16;
+  constexpr int W = D / 64;  // 16-byte chunks of a key row per lane
+  const int g4 = lane >> 2, c4 = lane & 3;
+
+  // S^T[token][head]: A rows are tokens, read 16 bytes at a time as they lie
+  float s[MT][NT][4], s2[MT][NT][4];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[mt][nt][i] = s2[mt][nt][i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const uint32_t off = (mt * 16 + g4) * D + (c4 * W + j) * 16;
+      const uint4 lo = lds128(swz(kb, off)), hi = lds128(swz(kb, off + 8 * D));
+      const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = quant::e4m3x2_to_f16x2(a[i]), a2 = quant::e4m3x2_hi_to_f16x2(a[i]);
+        const uint32_t a1 = quant::e4m3x2_to_f16x2(b[i]), a3 = quant::e4m3x2_hi_to_f16x2(b[i]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {  // two chains of products, so that they overlap
+          const int ks = j * 4 + i;
+          if (i & 1) mma_f16_16816(s2[mt][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+          else mma_f16_16816(s[mt][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
         }
-        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= kf * p.scale_log2;
-      } else if (lane == 0 && p.status) {
-        atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
       }
-      const float mn = fmaxf(m, s), a = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(s - mn);
-      l = l * a + w;
-      for (int i = 0; i < PER; ++i) o[i] = o[i] * a + w * v[i];
-      m = mn;
     }
-    for (int i = 0; i < PER; ++i) so[warp][lane * PER + i] = o[i];
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-    __syncthreads();
-    for (int i = threadIdx.x; i < D; i += kWarps * 32) {
-      float M = -INFINITY, lt = 0.f, ot = 0.f;
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = sl[w] == 0.f ? 0.f : exp2f(sm[w] - M);
-        lt += sl[w] * f;
-        ot += so[w][i] * f;
-      }
-      p.out[row + i] = __float2bfloat16_rn(L > 0 ? ot / lt : 0.f);
-    }
-    __syncthreads();
   }
+
+  // x = log2(e) s + ve, masked; the columns' largest
+  float top[NT][2], inv[MT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int tok = mt * 16 + g4 + 8 * hf;
+      const bool seen = tok < valid;
+      const int ke = quant::clamp_exp(lds_u8(keb + tok));
+      const int ve = quant::clamp_exp(lds_u8(veb + tok));
+      const float kf = quant::pow2i(ke), vf = static_cast<float>(ve);
+      inv[mt][hf] = quant::pow2i(-ve);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = 2 * hf + e;
+          const float x = seen ? fmaf((s[mt][nt][i] + s2[mt][nt][i]) * kf, cf[nt][e], vf) : -INFINITY;
+          s[mt][nt][i] = x;
+          top[nt][e] = fmaxf(top[nt][e], x);
+        }
+    }
+  float sub[NT][2], alpha[NT][2];
+  bool moved = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float t = top[nt][e];
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+      const float r = acc.r[nt][e];
+      alpha[nt][e] = 1.f;
+      if (t > r + kSlack) {  // also while r is -inf and t is not
+        const float n = t - kHeadroom;
+        alpha[nt][e] = fast_exp2(r - n);
+        acc.r[nt][e] = n;
+        moved = true;
+      }
+      sub[nt][e] = acc.r[nt][e] == -INFINITY ? 0.f : acc.r[nt][e];
+    }
+  if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        acc.l[nt][e] *= alpha[nt][e];
+#pragma unroll
+        for (int md = 0; md < D / 16; ++md) {
+          acc.o[md][nt][e] *= alpha[nt][e];
+          acc.o[md][nt][e + 2] *= alpha[nt][e];
+        }
+      }
+  }
+
+  // weights -> fp16 -> B fragments of P^T (movmatrix turns the accumulator layout)
+  uint32_t pb[MT][NT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float w0 = fast_exp2(s[mt][nt][2 * hf] - sub[nt][0]);
+        const float w1 = fast_exp2(s[mt][nt][2 * hf + 1] - sub[nt][1]);
+        acc.l[nt][0] = fmaf(w0, inv[mt][hf], acc.l[nt][0]);
+        acc.l[nt][1] = fmaf(w1, inv[mt][hf], acc.l[nt][1]);
+        pb[mt][nt][hf] = movmatrix_trans(pack_f16x2(w0, w1));
+      }
+
+  // O^T[value][head] += V^T P^T.  A rows are values: accumulator rows g and
+  // g + 8 of step md stand for values g D/8 + 2 md and + 2 md + 1, so a lane
+  // reads D/8 consecutive bytes of each of its four tokens; a byte permute pairs
+  // two tokens' codes of the same value.
+#pragma unroll
+  for (int kt = 0; kt < MT; ++kt) {
+    uint32_t v[4][D / 32];
+    const int t0 = kt * 16 + 2 * c4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = t0 + (i & 1) + 8 * (i >> 1);
+      const uint32_t a = swz(vb, tok * D + g4 * (D / 8));
+      if constexpr (D == 128) {
+        const uint4 x = lds128(a);
+        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+      } else {
+        const uint2 x = lds64(a);
+        v[i][0] = x.x, v[i][1] = x.y;
+      }
+    }
+    if (valid < (kt + 1) * 16) {  // warp-uniform; a NaN code behind the end must not meet its zero weight
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + (i & 1) + 8 * (i >> 1) >= valid)
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) v[i][c] = 0u;
+    }
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t sel = half ? 0x7362u : 0x5140u;
+        const uint32_t lo = __byte_perm(v[0][c], v[1][c], sel), hi = __byte_perm(v[2][c], v[3][c], sel);
+        const uint32_t a0 = quant::e4m3x2_to_f16x2(lo), a1 = quant::e4m3x2_hi_to_f16x2(lo);
+        const uint32_t a2 = quant::e4m3x2_to_f16x2(hi), a3 = quant::e4m3x2_hi_to_f16x2(hi);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16_16816(acc.o[c * 2 + half][nt], a0, a1, a2, a3, pb[kt][nt][0], pb[kt][nt][1]);
+      }
+  }
+}
+
+// Where a warp's producer stands: run (seq, h) of n units, its next unit j.
+struct Cursor {
+  int seq, h, j, n, len;
+  int wbase, window;  // 32 table entries from wbase on, one per lane
+  bool from0;         // the current piece began at its run's first unit
+};
+
+template <int D, int BS, int NT>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
+    decode_quant_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                        const Params p) {
+  using Sh = Shape<D, NT>;
+  constexpr int UT = Sh::kTokens, S = Sh::kStages, NW = Sh::kWarps, COLS = NT * 8;
+  constexpr int BR = BS < UT ? BS : UT;   // tokens of one copy
+  constexpr int BOXES = UT / BR;          // copies per unit and tensor
+  constexpr int BOX_BYTES = BR * D;
+  constexpr int EXP_LANES = 2 * UT / 16;  // 16 exponent bytes each
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long warp_sum[NW], chunk_base[Sh::kThreads];
+  __shared__ uint2 pieces[2 * NW];  // {seq | KV head << 16, flags} of each warp's first and last incomplete piece
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  uint8_t *ring_ptr = smem + warp * Sh::kRingBytes;
+  uint8_t *rest = smem + NW * Sh::kRingBytes;
+  float *piece_ptr = reinterpret_cast<float *>(rest) + warp * Sh::kPieceFloats;
+  uint8_t *exp_ptr = rest + NW * Sh::kPieceFloats * 4 + warp * Sh::kExpBytes;
+  uint8_t *meta_ptr = rest + NW * (Sh::kPieceFloats * 4 + Sh::kExpBytes) + warp * (S * 16);
+  uint8_t *bar_ptr = rest + NW * (Sh::kPieceFloats * 4 + Sh::kExpBytes + S * 16) + warp * (S * 8);
+  const uint32_t ring = smem_u32(ring_ptr), exps = smem_u32(exp_ptr), full = smem_u32(bar_ptr);
+  int4 *meta = reinterpret_cast<int4 *>(meta_ptr);
+
+  grid_launch_dependents();
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(full + 8 * s, 1 + EXP_LANES);
+    mbar_init_fence();
+  }
+  if (tid < 2 * NW) pieces[tid] = make_uint2(0u, 0u);
+  if (tid == 0) {
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
+  }
+  grid_dependency_wait();  // the inputs may come from the kernel launched just before
+
+  // ---- prefix sums of the runs' units: thread i holds sequences [i CH, (i + 1) CH)
+  const int cap = capped_len(p, BS);
+  const int CH = (p.num_seqs + Sh::kThreads - 1) / Sh::kThreads;
+  auto length = [&](int seq) {
+    const int L = p.seq_lens[seq];
+    return L < 0 ? 0 : min(L, cap);
+  };
+  auto units = [&](int L) { return static_cast<int>((static_cast<unsigned>(L) + UT - 1) / UT); };
+  long long mine = 0;
+  for (int k = 0; k < CH; ++k) {
+    const int seq = tid * CH + k;
+    if (seq >= p.num_seqs) break;
+    const int L = p.seq_lens[seq];
+    if ((L < 0 || L > cap) && blockIdx.x == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_LEN);
+    mine += units(L < 0 ? 0 : min(L, cap));
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += t;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  chunk_base[tid] = before + incl - mine;
+  __syncthreads();
+  const long long U = total * p.num_kv_heads;
+  // as many CTAs as give every warp a unit; the others have none
+  const long long nc = max(1ll, min(static_cast<long long>(gridDim.x), (U + NW - 1) / NW));
+  const long long W = nc * NW;
+  auto range_start = [&](long long i) { return min(i, W) * U / W; };
+  const long long wi = static_cast<long long>(blockIdx.x) * NW + warp;
+  const long long u0 = range_start(wi), u1 = range_start(wi + 1);
+
+  bool ok = true;
+  if (u0 < u1) {
+    // ---- the run that unit u0 belongs to
+    Cursor c;
+    {
+      const long long key = u0 / p.num_kv_heads;  // units of whole sequences before it, per head
+      int lo = 0, hi = Sh::kThreads - 1;           // last chunk whose base is <= key
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (chunk_base[mid] <= key) lo = mid;
+        else hi = mid - 1;
+      }
+      long long base = chunk_base[lo];
+      int seq = lo * CH;
+      for (;;) {  // warp-wide walk of the chunk, 32 sequences at a time
+        const int s = seq + lane;
+        const int L = s < p.num_seqs ? length(s) : 0;
+        const int n = units(L);
+        long long pre = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const long long t = __shfl_up_sync(0xffffffffu, pre, off);
+          if (lane >= off) pre += t;
+        }
+        const unsigned in = __ballot_sync(0xffffffffu, key < base + pre);
+        if (in || seq + 32 >= p.num_seqs) {
+          const int src = in ? __ffs(in) - 1 : 31;
+          c.seq = seq + src;
+          c.n = max(1, __shfl_sync(0xffffffffu, n, src));
+          c.len = __shfl_sync(0xffffffffu, L, src);
+          base += __shfl_sync(0xffffffffu, pre, src) - c.n;
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, pre, 31);
+        seq += 32;
+      }
+      const long long r = u0 - base * p.num_kv_heads;
+      c.h = static_cast<int>(r / c.n);
+      c.j = static_cast<int>(r - static_cast<long long>(c.h) * c.n);
+      c.wbase = -32;
+      c.window = -1;
+      c.from0 = c.j == 0;
+    }
+
+    const uint64_t pol = l2_policy_evict_first();
+    long long next = u0;  // next unit to issue
+    // Issue the cursor's unit into stage s and move the cursor on (whole warp).
+    auto issue = [&](int s) {
+      const int valid = min(UT, c.len - c.j * UT);
+      const bool ends = c.j + 1 == c.n;
+      const int first_entry = BS <= UT ? c.j * BOXES : c.j / (BS / UT);
+      const int piece_row = BS <= UT ? 0 : (c.j % (BS / UT)) * UT;  // token of the block where the unit starts
+      if ((first_entry & ~31) != c.wbase) {
+        c.wbase = first_entry & ~31;
+        const int e = c.wbase + lane;
+        c.window = static_cast<long long>(e) * BS < c.len ? p.block_tables[static_cast<size_t>(c.seq) * p.max_blocks + e] : -1;
+      }
+      const int nbox = BS <= UT ? (valid + BR - 1) / BR : 1;
+      const uint32_t bar = full + 8 * s, kdst = ring + s * 2 * kUnitBytes, vdst = kdst + kUnitBytes;
+      if (lane == 0) {
+        meta[s] = make_int4(c.seq, c.h,
+                            valid | (next == u0 || c.j == 0 ? 1 << 16 : 0) | (ends || next + 1 == u1 ? 1 << 17 : 0) |
+                                (c.from0 ? 1 << 18 : 0) | (ends ? 1 << 19 : 0),
+                            0);
+        mbar_arrive_expect_tx(bar, 2 * nbox * BOX_BYTES);
+      }
+      int erow = -1;  // this lane's 16 exponents: their first row, or none
+#pragma unroll
+      for (int k = 0; k < BOXES; ++k) {
+        if (k < nbox) {
+          const int b = __shfl_sync(0xffffffffu, c.window, (first_entry + k) & 31);
+          const bool good = b >= 0 && b < p.num_blocks;
+          if (!good && lane == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
+          const int row = good ? (b * p.num_kv_heads + c.h) * BS + piece_row : 0;
+          if (lane == 0) {  // a bad block: a box wholly outside the tensor reads zeros
+            const int y = good ? static_cast<int>(static_cast<long long>(row) * D / 128) : 0x7fffff00;
+            tma_load_2d(kdst + k * BOX_BYTES, &tmk, 0, y, bar, pol);
+            tma_load_2d(vdst + k * BOX_BYTES, &tmv, 0, y, bar, pol);
+          }
+          const int chunk = lane % (UT / 16);
+          if (lane < EXP_LANES && chunk / (BR / 16) == k) erow = row + (chunk % (BR / 16)) * 16;
+        }
+      }
+      if (lane < EXP_LANES) {
+        const bool value = lane >= UT / 16;
+        if (erow >= 0)
+          cp_async16(exps + (s * 2 + value) * UT + (lane % (UT / 16)) * 16, (value ? p.v_exps : p.k_exps) + erow);
+        cp_async_arrive(bar);
+      }
+      ++next;
+      if (!ends) {
+        ++c.j;
+        return;
+      }
+      c.j = 0;
+      c.from0 = true;
+      if (next >= u1) return;
+      if (++c.h < p.num_kv_heads) {
+        // the same table: the window stands unless it has moved on
+        return;
+      }
+      c.h = 0;
+      do {
+        c.len = c.seq + 1 < p.num_seqs ? length(++c.seq) : 1;  // (the range ends before the last sequence does)
+      } while (c.len == 0);
+      c.n = units(c.len);
+      c.wbase = -32;
+    };
+
+    const long long count = u1 - u0;
+    for (int s = 0; s < S && s < count; ++s) issue(s);
+
+    Acc<D, NT> acc;
+    uint32_t qf[NT][D / 16][2];
+    float cf[NT][2];
+    const int g4 = lane >> 2, c4 = lane & 3;
+    long long i = 0;
+    for (; i < count; ++i) {
+      const int s = static_cast<int>(i % S);
+      if (!mbar_wait(full + 8 * s, static_cast<uint32_t>(i / S) & 1)) ok = false;
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0 && p.status) atomicOr(p.status, PKV_STATUS_TIMEOUT);
+        ok = false;
+        break;
+      }
+      const int4 m = meta[s];
+      if (m.z & (1 << 16)) {
+        load_queries<D, NT>(p, m.x, m.y, qf, cf, lane);
+        acc.reset();
+      }
+      const uint32_t kb = ring + s * 2 * kUnitBytes, eb = exps + s * 2 * UT;
+      attend_unit<D, NT>(acc, qf, cf, kb, kb + kUnitBytes, eb, eb + UT, m.z & 0xFFFF, lane);
+      __syncwarp();
+      if (next < u1) issue(s);
+      if (m.z & (1 << 17)) {  // the piece ends here
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float l = acc.l[nt][e];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            acc.l[nt][e] = l;
+          }
+        const bool from0 = m.z & (1 << 18), ends = m.z & (1 << 19);
+        if (from0 && ends) {
+          // the whole run: values g D/8 .. of this lane's two heads per tile
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int col = nt * 8 + 2 * c4 + e;
+              if (col >= p.group) continue;
+              const float l = acc.l[nt][e], inv = l == 0.f ? 0.f : 1.f / l;
+              uint32_t w[D / 16];
+#pragma unroll
+              for (int md = 0; md < D / 16; ++md)
+                w[md] = pack_bf16x2(acc.o[md][nt][e] * inv, acc.o[md][nt][e + 2] * inv);
+              uint4 *dst = reinterpret_cast<uint4 *>(
+                  p.out + (static_cast<size_t>(m.x) * p.num_q_heads + static_cast<size_t>(m.y) * p.group + col) * D +
+                  g4 * (D / 8));
+#pragma unroll
+              for (int k = 0; k < D / 64; ++k)
+                dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            }
+        } else {
+          // a first piece goes to its own place, a last one (from a run's start) over the drained ring
+          float *dst = from0 ? reinterpret_cast<float *>(ring_ptr) : piece_ptr;
+          float4 *o4 = reinterpret_cast<float4 *>(dst) + lane;
+#pragma unroll
+          for (int md = 0; md < D / 16; ++md)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              o4[(md * NT + nt) * 32] =
+                  make_float4(acc.o[md][nt][0], acc.o[md][nt][1], acc.o[md][nt][2], acc.o[md][nt][3]);
+          if (g4 == 0)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                dst[Sh::kTileFloats + nt * 8 + 2 * c4 + e] = acc.r[nt][e];
+                dst[Sh::kTileFloats + COLS + nt * 8 + 2 * c4 + e] = acc.l[nt][e];
+              }
+          if (lane == 0)
+            pieces[2 * warp + (from0 ? 1 : 0)] = make_uint2(
+                static_cast<uint32_t>(m.x) | (static_cast<uint32_t>(m.y) << 16), 1u | (from0 ? 2u : 0u) | (ends ? 4u : 0u));
+        }
+      }
+    }
+    // after a timeout: leave no copy in flight into this CTA's shared memory
+    if (!ok)
+      for (long long k = i + 1; k < next - u0; ++k) mbar_wait(full + 8 * static_cast<int>(k % S), (k / S) & 1);
+  }
+  const bool failed = __syncthreads_or(!ok);
+
+  // ---- join the pieces of each run; warp w takes every NW-th (value step, tile)
+  int4 desc = make_int4(0, 0, 0, 0);
+  if (!failed) {
+    const int c4 = lane & 3, g4 = lane >> 2;
+    auto place = [&](int k) -> const float * {
+      return (k & 1) ? reinterpret_cast<const float *>(smem + (k >> 1) * Sh::kRingBytes)
+                     : reinterpret_cast<const float *>(rest) + (k >> 1) * Sh::kPieceFloats;
+    };
+    for (int a = 0; a < 2 * NW;) {
+      const uint2 first = pieces[a];
+      if (!(first.y & 1u)) {
+        ++a;
+        continue;
+      }
+      int b = a;
+      uint32_t last_flags = first.y;
+      int k = a + 1;
+      for (; k < 2 * NW; ++k) {
+        const uint2 x = pieces[k];
+        if (!(x.y & 1u)) continue;
+        if (x.x != first.x || (x.y & 2u)) break;
+        b = k;
+        last_flags = x.y;
+      }
+      const int seq = first.x & 0xFFFF, h = first.x >> 16;
+      const bool from0 = first.y & 2u, ends = last_flags & 4u;
+      float *dst = from0 && ends ? nullptr
+                                 : p.ws + (static_cast<size_t>(blockIdx.x) * 2 + (from0 ? 1 : 0)) * Sh::kPieceFloats;
+      for (int t = warp; t < (D / 16) * NT; t += NW) {
+        const int md = t / NT, nt = t - md * NT, col = nt * 8 + 2 * c4;
+        float R[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int q = a; q <= b; ++q) {
+          if (!(pieces[q].y & 1u)) continue;
+          const float *x = place(q) + Sh::kTileFloats + col;
+          R[0] = fmaxf(R[0], x[0]);
+          R[1] = fmaxf(R[1], x[1]);
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = a; q <= b; ++q) {
+          if (!(pieces[q].y & 1u)) continue;
+          const float *x = place(q);
+          const float r0 = x[Sh::kTileFloats + col], r1 = x[Sh::kTileFloats + col + 1];
+          const float f0 = r0 == -INFINITY ? 1.f : fast_exp2(r0 - R[0]), f1 = r1 == -INFINITY ? 1.f : fast_exp2(r1 - R[1]);
+          l[0] += x[Sh::kTileFloats + COLS + col] * f0;
+          l[1] += x[Sh::kTileFloats + COLS + col + 1] * f1;
+          const float4 v = reinterpret_cast<const float4 *>(x)[t * 32 + lane];
+          o.x += v.x * f0;
+          o.y += v.y * f1;
+          o.z += v.z * f0;
+          o.w += v.w * f1;
+        }
+        if (dst) {
+          reinterpret_cast<float4 *>(dst)[t * 32 + lane] = o;
+          if (md == 0 && g4 == 0) {
+            dst[Sh::kTileFloats + col] = R[0];
+            dst[Sh::kTileFloats + col + 1] = R[1];
+            dst[Sh::kTileFloats + COLS + col] = l[0];
+            dst[Sh::kTileFloats + COLS + col + 1] = l[1];
+          }
+        } else {
+          uint32_t *row = reinterpret_cast<uint32_t *>(
+              p.out + (static_cast<size_t>(seq) * p.num_q_heads + static_cast<size_t>(h) * p.group + col) * D +
+              g4 * (D / 8) + 2 * md);
+          const float i0 = l[0] == 0.f ? 0.f : 1.f / l[0], i1 = l[1] == 0.f ? 0.f : 1.f / l[1];
+          if (col < p.group) row[0] = pack_bf16x2(o.x * i0, o.z * i0);
+          if (col + 1 < p.group) row[D / 2] = pack_bf16x2(o.y * i1, o.w * i1);
+        }
+      }
+      if (from0 && !ends) {  // leaves this CTA: the CTA that holds the run's last unit
+        long long end = 0;
+        // units up to the run's end: the CTA's last warp's cursor is gone, so count them again
+        const int n = units(length(seq));
+        // sequences before seq
+        const int ch = seq / CH;
+        long long base = chunk_base[ch];
+        for (int s = ch * CH; s < seq; ++s) base += units(length(s));
+        end = base * p.num_kv_heads + (static_cast<long long>(h) + 1) * n;  // one past its last unit
+        // owner warp of unit end - 1: the largest i with range_start(i) <= end - 1
+        const long long i = ((end - 1) * W + W - 1) / U;
+        long long o = min(i, W - 1);
+        while (o > 0 && range_start(o) > end - 1) --o;
+        while (o + 1 < W && range_start(o + 1) <= end - 1) ++o;
+        desc = make_int4(seq, h, static_cast<int>(o / NW), 1);
+      }
+      a = k;
+    }
+  }
+  if (tid == 0 && p.ws_desc) p.ws_desc[blockIdx.x] = desc;
+
+  // ---- sequences without keys: zeros
+  for (long long s = blockIdx.x + static_cast<long long>(gridDim.x) * warp; s < p.num_seqs;
+       s += static_cast<long long>(gridDim.x) * NW) {
+    if (length(static_cast<int>(s)) != 0) continue;
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(s) * p.num_q_heads * D);
+    for (int k = lane; k < p.num_q_heads * D / 8; k += 32) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// The run that starts in CTA c and spans more (blockIdx.x = c): the exact merge
+// of its pieces, one accumulator quad per thread.
+template <int D, int NT>
+__global__ void __launch_bounds__(D * NT * 2) join_kernel(const Params p) {
+  using Sh = Shape<D, NT>;
+  constexpr int COLS = NT * 8;
+  grid_launch_dependents();
+  grid_dependency_wait();  // the pieces come from the grid launched just before
+  const int4 desc = p.ws_desc[blockIdx.x];
+  if (desc.w == 0) return;
+  const int c0 = blockIdx.x, c1 = desc.z;
+  const int t = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane & 3, g4 = lane >> 2;
+  const int md = t / NT, nt = t - md * NT, col = nt * 8 + 2 * c4;
+  auto piece = [&](int c) { return p.ws + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * Sh::kPieceFloats; };
+  float R0 = -INFINITY, R1 = -INFINITY;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float2 r = *reinterpret_cast<const float2 *>(piece(c) + Sh::kTileFloats + col);
+    R0 = fmaxf(R0, r.x);
+    R1 = fmaxf(R1, r.y);
+  }
+  float l0 = 0.f, l1 = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float *x = piece(c);
+    const float2 r = *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col);
+    const float2 l = *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + COLS + col);
+    const float4 v = reinterpret_cast<const float4 *>(x)[t * 32 + lane];
+    const float f0 = r.x == -INFINITY ? 1.f : fast_exp2(r.x - R0), f1 = r.y == -INFINITY ? 1.f : fast_exp2(r.y - R1);
+    l0 += l.x * f0;
+    l1 += l.y * f1;
+    o.x += v.x * f0;
+    o.y += v.y * f1;
+    o.z += v.z * f0;
+    o.w += v.w * f1;
+  }
+  const float i0 = l0 == 0.f ? 0.f : 1.f / l0, i1 = l1 == 0.f ? 0.f : 1.f / l1;
+  uint32_t *row = reinterpret_cast<uint32_t *>(
+      p.out + (static_cast<size_t>(desc.x) * p.num_q_heads + static_cast<size_t>(desc.y) * p.group + col) * D +
+      g4 * (D / 8) + 2 * md);
+  if (col < p.group) row[0] = pack_bf16x2(o.x * i0, o.z * i0);
+  if (col + 1 < p.group) row[D / 2] = pack_bf16x2(o.y * i1, o.w * i1);
+}
+
+// ------------------------------------------------------------------------ host
+struct Plan {
+  int grid = 1;
+  size_t piece_bytes = 0;
+  size_t ws_bytes() const { return grid > 1 ? grid * (2 * piece_bytes + sizeof(int4)) : 0; }
+};
+
+// The grid: one CTA per SM, fewer when the longest possible batch has fewer
+// than a unit per warp.  One CTA needs no workspace and no second kernel.
+Plan make_plan(int num_seqs, int num_kv_heads, int group, int head_dim, int max_seq_len) {
+  const int nt = group > 8 ? 2 : 1, tokens = kUnitBytes / head_dim;
+  const int warps = head_dim == 128 ? (nt == 1 ? Shape<128, 1>::kWarps : Shape<128, 2>::kWarps)
+                                    : (nt == 1 ? Shape<64, 1>::kWarps : Shape<64, 2>::kWarps);
+  const double units = static_cast<double>(num_seqs) * num_kv_heads * ((max_seq_len + (tokens - 1ll)) / tokens);
+  Plan plan;
+  plan.grid = static_cast<int>(std::max(1.0, std::min<double>(num_sms(), std::ceil(units / warps))));
+  plan.piece_bytes = (static_cast<size_t>(nt) * 8 * head_dim + 2 * nt * 8) * sizeof(float);
+  return plan;
+}
+
+bool sizes_valid(int num_seqs, int max_seq_len, int num_q_heads, int num_kv_heads) {
+  return num_seqs >= 0 && max_seq_len >= 0 && num_q_heads >= 1 && num_kv_heads >= 1 && num_q_heads % num_kv_heads == 0;
+}
+
+bool sizes_supported(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim) {
+  return (head_dim == 64 || head_dim == 128) && num_q_heads / num_kv_heads <= kMaxGroup && num_seqs <= 65535 &&
+         num_kv_heads <= 65535;
 }
 
 int check_decode(const void *q, const void *k_codes, const void *v_codes, const void *k_exps, const void *v_exps,
                  const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens, int num_seqs,
                  int max_seq_len, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
                  float scale, const void *out) {
-  if (num_seqs < 0 || max_blocks_per_seq < 0 || max_seq_len < 0 || num_q_heads < 1 || num_kv_heads < 1 ||
-      num_blocks < 0 || !std::isfinite(scale))
+  if (!sizes_valid(num_seqs, max_seq_len, num_q_heads, num_kv_heads) || max_blocks_per_seq < 0 || num_blocks < 0 ||
+      !std::isfinite(scale))
     return PKV_ERR_ARG;
-  if (num_q_heads % num_kv_heads != 0) return PKV_ERR_ARG;
-  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (!sizes_supported(num_seqs, num_q_heads, num_kv_heads, head_dim)) return PKV_ERR_UNSUPPORTED;
   if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128) return PKV_ERR_UNSUPPORTED;
-  if (num_q_heads / num_kv_heads > kMaxGroup) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
-  if (num_seqs > 65535 || num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
   if (!q || !k_codes || !v_codes || !k_exps || !v_exps || !block_tables || !seq_lens || !out || num_blocks == 0)
     return PKV_ERR_ARG;
   if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_exps) || !aligned16(v_exps) ||
@@ -114,8 +814,47 @@ int check_decode(const void *q, const void *k_codes, const void *v_codes, const 
       (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
     return PKV_ERR_ARG;
   const long long rows = static_cast<long long>(num_blocks) * num_kv_heads * block_size;
-  if (rows + block_size >= (1ll << 31)) return PKV_ERR_UNSUPPORTED;
+  if (rows + block_size >= 0x7fffff00ll) return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
+}
+
+// Launch with programmatic stream serialisation: the grid may start while the
+// previous kernel in the stream drains; it waits before it reads anything.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), int grid, int block, size_t smem, cudaStream_t stream,
+                       Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <int D, int BS, int NT>
+cudaError_t launch(const CUtensorMap &tmk, const CUtensorMap &tmv, const Params &p, int grid, cudaStream_t stream) {
+  using Sh = Shape<D, NT>;
+  auto k = decode_quant_kernel<D, BS, NT>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmemBytes);
+  if (e == cudaSuccess) e = launch_pdl(k, grid, Sh::kThreads, Sh::kSmemBytes, stream, tmk, tmv, p);
+  if (e == cudaSuccess && grid > 1) e = launch_pdl(join_kernel<D, NT>, grid, D * NT * 2, 0, stream, p);
+  return e;
+}
+
+template <int D, int NT>
+cudaError_t by_block(const CUtensorMap &tmk, const CUtensorMap &tmv, const Params &p, int grid, int block_size,
+                     cudaStream_t stream) {
+  switch (block_size) {
+    case 16: return launch<D, 16, NT>(tmk, tmv, p, grid, stream);
+    case 32: return launch<D, 32, NT>(tmk, tmv, p, grid, stream);
+    case 64: return launch<D, 64, NT>(tmk, tmv, p, grid, stream);
+    default: return launch<D, 128, NT>(tmk, tmv, p, grid, stream);
+  }
 }
 
 }  // namespace
@@ -125,7 +864,10 @@ extern "C" {
 
 size_t paged_attention_decode_quant_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                                    int max_seq_len) {
-  return 0;
+  if (!pkv::sizes_valid(num_seqs, max_seq_len, num_q_heads, num_kv_heads) ||
+      !pkv::sizes_supported(num_seqs, num_q_heads, num_kv_heads, head_dim) || num_seqs == 0)
+    return 0;
+  return pkv::make_plan(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, head_dim, max_seq_len).ws_bytes();
 }
 
 int paged_attention_decode_quant(const pkv_bf16 *q, const uint8_t *k_codes, const uint8_t *v_codes,
@@ -138,28 +880,47 @@ int paged_attention_decode_quant(const pkv_bf16 *q, const uint8_t *k_codes, cons
                                    num_seqs, max_seq_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
                                    scale, out);
   if (rc != PKV_OK || num_seqs == 0) return rc;
+  const int group = num_q_heads / num_kv_heads;
+  const pkv::Plan plan = pkv::make_plan(num_seqs, num_kv_heads, group, head_dim, max_seq_len);
+  if (plan.ws_bytes() > 0 && (!workspace || workspace_bytes < plan.ws_bytes() || !pkv::aligned16(workspace)))
+    return PKV_ERR_WORKSPACE;
+
+  // the code arrays as rows of 128 bytes, copied a block (or a unit's part of one) at a time
+  const int unit_tokens = pkv::kUnitBytes / head_dim, box_tokens = std::min(block_size, unit_tokens);
+  const long long rows = static_cast<long long>(num_blocks) * num_kv_heads * block_size * head_dim / 128;
+  CUtensorMap tmk, tmv;
+  if (!pkv::make_tensor_map_bytes(&tmk, k_codes, rows, box_tokens * head_dim / 128) ||
+      !pkv::make_tensor_map_bytes(&tmv, v_codes, rows, box_tokens * head_dim / 128))
+    return PKV_ERR_CUDA;
+
   pkv::Params p{};
   p.q = reinterpret_cast<const __nv_bfloat16 *>(q);
-  p.k_codes = k_codes;
-  p.v_codes = v_codes;
   p.k_exps = k_exps;
   p.v_exps = v_exps;
   p.block_tables = block_tables;
   p.seq_lens = seq_lens;
   p.out = reinterpret_cast<__nv_bfloat16 *>(out);
+  if (plan.grid > 1) {
+    p.ws = static_cast<float *>(workspace);
+    p.ws_desc = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + plan.grid * 2 * plan.piece_bytes);
+  }
   p.status = d_status;
+  p.num_seqs = num_seqs;
   p.max_blocks = max_blocks_per_seq;
   p.max_len = max_seq_len;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = num_kv_heads;
-  p.group = num_q_heads / num_kv_heads;
+  p.group = group;
   p.num_blocks = num_blocks;
-  p.block_size = block_size;
   p.scale_log2 = scale * pkv::kLog2e;
-  const dim3 grid(num_kv_heads, num_seqs);
-  if (head_dim == 128) pkv::decode_simple<128><<<grid, pkv::kWarps * 32, 0, pkv::as_stream(stream)>>>(p);
-  else pkv::decode_simple<64><<<grid, pkv::kWarps * 32, 0, pkv::as_stream(stream)>>>(p);
-  return pkv::check_launch();
+  cudaStream_t st = pkv::as_stream(stream);
+  const cudaError_t e =
+      head_dim == 128 ? (group > 8 ? pkv::by_block<128, 2>(tmk, tmv, p, plan.grid, block_size, st)
+                                   : pkv::by_block<128, 1>(tmk, tmv, p, plan.grid, block_size, st))
+                      : (group > 8 ? pkv::by_block<64, 2>(tmk, tmv, p, plan.grid, block_size, st)
+                                   : pkv::by_block<64, 1>(tmk, tmv, p, plan.grid, block_size, st));
+  if (e != cudaSuccess) return pkv::set_cuda_error(e), PKV_ERR_CUDA;
+  return PKV_OK;
 }
 
 }  // extern "C"

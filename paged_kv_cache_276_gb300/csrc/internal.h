@@ -17,6 +17,9 @@ bool make_tensor_map_2d(void *map, const void *base, int dim0, long long dim1, i
 bool make_tensor_map_3d(void *map, const void *base, int dim0, int dim1, long long dim2, int box0, int box1,
                         int box2);
 
+// Bytes as rows of 128, read box_rows at a time with the 128-byte swizzle (decode.cu).
+bool make_tensor_map_bytes(void *map, const void *base, long long rows, int box_rows);
+
 // Chunked causal query on tcgen05 (chunk_tc.cu): q_len 16, 8 query heads per
 // KV head, head_dim 128, block 16 or 32, partitions a multiple of 64 tokens.
 struct ChunkTcArgs {
