@@ -623,7 +623,9 @@ size_t paged_attention_decode_quant_workspace_size(int num_seqs, int num_q_heads
  * and values read as zeros.  Exponent bytes outside [96, 158] (which
  * pkv_write_quant never stores) count as the nearer bound.
  * Supported: head_dim in {64, 128}; block_size in {16, 32, 64, 128};
- *   num_q_heads / num_kv_heads <= 16; num_seqs and num_kv_heads <= 65535.
+ *   num_q_heads / num_kv_heads <= 16; num_seqs and num_kv_heads <= 65535;
+ *   num_seqs * num_kv_heads * head_dim * (the longest sequence that max_seq_len
+ *   and the tables allow) below 2^43.
  *   Other sizes return PKV_ERR_UNSUPPORTED.
  */
 int paged_attention_decode_quant(const pkv_bf16 *q, const uint8_t *k_codes, const uint8_t *v_codes,

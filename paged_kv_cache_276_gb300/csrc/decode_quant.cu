@@ -68,6 +68,8 @@ template <int D, int NT>
 struct Shape {
   static constexpr int kTokens = kUnitBytes / D;  // tokens of a unit
   static constexpr int kStages = 2;
+  // tokens of one softmax step: the whole unit where registers allow (12 warps: 168 a thread)
+  static constexpr int kStep = NT == 1 ? kTokens : kTokens / 2;
   static constexpr int kTileFloats = NT * 8 * D;  // O of one piece, in accumulator order
   static constexpr int kPieceFloats = kTileFloats + 2 * NT * 8;  // ..., m[cols], l[cols]
   static constexpr int kRingBytes = kStages * 2 * kUnitBytes;
@@ -75,11 +77,11 @@ struct Shape {
   static constexpr int kMetaBytes = kStages * (16 + 8);  // an int4 and a barrier per stage
   static constexpr int kWarpBytes = kRingBytes + kExpBytes + kMetaBytes + kPieceFloats * 4;
   // as many warps as shared memory (227 KB a CTA) holds rings for
-  static constexpr int kWarps = D == 128 ? (NT == 1 ? 11 : 9) : (NT == 1 ? 12 : 10);
+  static constexpr int kWarps = D == 128 ? (NT == 1 ? 11 : 8) : (NT == 1 ? 12 : 10);
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kSmemBytes = 1024 + kWarps * kWarpBytes;
   static_assert(kPieceFloats * 4 <= kRingBytes, "a warp's last piece goes over its ring");
-  static_assert(kSmemBytes + kThreads * 8 + kWarps * 24 + 64 <= 227 * 1024, "shared memory of one CTA");
+  static_assert(kSmemBytes + kThreads * 8 + kWarps * 40 + 64 <= 227 * 1024, "shared memory of one CTA");
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -193,25 +195,25 @@ __device__ __forceinline__ void load_queries(const Params &p, int seq, int h, ui
   }
 }
 
-// One staged unit: scores, running softmax, product with the values.
-//   valid: tokens of the unit before the sequence's end (1 .. kTokens); staged
-//          bytes behind them may be anything.
-template <int D, int NT>
-__device__ __forceinline__ void attend_unit(Acc<D, NT> &acc, const uint32_t (&qf)[NT][D / 16][2],
+// 16 MT staged tokens: scores, running softmax, product with the values.
+//   valid: those of them before the sequence's end (at least 1); staged bytes
+//          behind them may be anything.
+template <int D, int NT, int MT>
+__device__ __forceinline__ void attend_tokens(Acc<D, NT> &acc, const uint32_t (&qf)[NT][D / 16][2],
                                             const float (&cf)[NT][2], uint32_t kb, uint32_t vb, uint32_t keb,
                                             uint32_t veb, int valid, int lane) {
-  constexpr int MT = Shape<D, NT>::kTokens / 16;
   constexpr int W = D / 64;  // 16-byte chunks of a key row per lane
   const int g4 = lane >> 2, c4 = lane & 3;
 
   // S^T[token][head]: A rows are tokens, read 16 bytes at a time as they lie
-  float s[MT][NT][4], s2[MT][NT][4];
+  float s[MT][NT][4];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
+    float s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[mt][nt][i] = s2[mt][nt][i] = 0.f;
+      for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       const uint32_t off = (mt * 16 + g4) * D + (c4 * W + j) * 16;
@@ -224,11 +226,14 @@ __device__ __forceinline__ void attend_unit(Acc<D, NT> &acc, const uint32_t (&qf
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {  // two chains of products, so that they overlap
           const int ks = j * 4 + i;
-          if (i & 1) mma_f16_16816(s2[mt][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+          if (NT == 1 && (i & 1)) mma_f16_16816(s2, a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
           else mma_f16_16816(s[mt][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
         }
       }
     }
+    if (NT == 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[mt][0][i] += s2[i];
   }
 
   // x = log2(e) s + ve, masked; the columns' largest
@@ -250,7 +255,7 @@ __device__ __forceinline__ void attend_unit(Acc<D, NT> &acc, const uint32_t (&qf
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = 2 * hf + e;
-          const float x = seen ? fmaf((s[mt][nt][i] + s2[mt][nt][i]) * kf, cf[nt][e], vf) : -INFINITY;
+          const float x = seen ? fmaf(s[mt][nt][i] * kf, cf[nt][e], vf) : -INFINITY;
           s[mt][nt][i] = x;
           top[nt][e] = fmaxf(top[nt][e], x);
         }
@@ -346,6 +351,18 @@ __device__ __forceinline__ void attend_unit(Acc<D, NT> &acc, const uint32_t (&qf
   }
 }
 
+// One quad of joined accumulators: values g D/8 + 2 md and + 1 of heads col and col + 1.
+template <int D>
+__device__ __forceinline__ void store_quad(const Params &p, int seq, int h, int col, int g4, int md, const float4 &o,
+                                           float l0, float l1) {
+  uint32_t *row = reinterpret_cast<uint32_t *>(
+      p.out + (static_cast<size_t>(seq) * p.num_q_heads + static_cast<size_t>(h) * p.group + col) * D + g4 * (D / 8) +
+      2 * md);
+  const float i0 = l0 == 0.f ? 0.f : 1.f / l0, i1 = l1 == 0.f ? 0.f : 1.f / l1;
+  if (col < p.group) row[0] = pack_bf16x2(o.x * i0, o.z * i0);
+  if (col + 1 < p.group) row[D / 2] = pack_bf16x2(o.y * i1, o.w * i1);
+}
+
 // Where a warp's producer stands: run (seq, h) of n units, its next unit j.
 struct Cursor {
   int seq, h, j, n, len;
@@ -358,14 +375,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     decode_quant_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                         const Params p) {
   using Sh = Shape<D, NT>;
-  constexpr int UT = Sh::kTokens, S = Sh::kStages, NW = Sh::kWarps, COLS = NT * 8;
+  constexpr int UT = Sh::kTokens, S = Sh::kStages, NW = Sh::kWarps, COLS = NT * 8, TH = Sh::kThreads;
   constexpr int BR = BS < UT ? BS : UT;   // tokens of one copy
   constexpr int BOXES = UT / BR;          // copies per unit and tensor
   constexpr int BOX_BYTES = BR * D;
   constexpr int EXP_LANES = 2 * UT / 16;  // 16 exponent bytes each
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long warp_sum[NW], chunk_base[Sh::kThreads];
-  __shared__ uint2 pieces[2 * NW];  // {seq | KV head << 16, flags} of each warp's first and last incomplete piece
+  __shared__ uint32_t warp_sum[NW];
+  __shared__ uint32_t chunk_start[TH];  // first unit of each thread's sequences
+  __shared__ int chunk_len[TH];         // their length, where a thread has one sequence
+  __shared__ uint4 pieces[2 * NW];      // each warp's first and last incomplete piece (see flush)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -383,7 +402,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     for (int s = 0; s < S; ++s) mbar_init(full + 8 * s, 1 + EXP_LANES);
     mbar_init_fence();
   }
-  if (tid < 2 * NW) pieces[tid] = make_uint2(0u, 0u);
+  if (tid < 2 * NW) pieces[tid] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) {
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
@@ -392,90 +411,101 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 
   // ---- prefix sums of the runs' units: thread i holds sequences [i CH, (i + 1) CH)
   const int cap = capped_len(p, BS);
-  const int CH = (p.num_seqs + Sh::kThreads - 1) / Sh::kThreads;
+  const int CH = (p.num_seqs + TH - 1) / TH;
   auto length = [&](int seq) {
     const int L = p.seq_lens[seq];
     return L < 0 ? 0 : min(L, cap);
   };
-  auto units = [&](int L) { return static_cast<int>((static_cast<unsigned>(L) + UT - 1) / UT); };
-  long long mine = 0;
+  auto units = [&](int L) { return (static_cast<uint32_t>(L) + UT - 1) / UT; };
+  uint32_t mine = 0;
+  int any_empty = 0;
   for (int k = 0; k < CH; ++k) {
     const int seq = tid * CH + k;
     if (seq >= p.num_seqs) break;
-    const int L = p.seq_lens[seq];
-    if ((L < 0 || L > cap) && blockIdx.x == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_LEN);
-    mine += units(L < 0 ? 0 : min(L, cap));
+    int L = p.seq_lens[seq];
+    if (L < 0 || L > cap) {
+      if (blockIdx.x == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_LEN);
+      L = L < 0 ? 0 : cap;
+    }
+    mine += units(L);
+    any_empty |= L == 0;
+    if (k == 0) chunk_len[tid] = L;
   }
-  long long incl = mine;
+  uint32_t incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, incl, off);
+    const uint32_t t = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += t;
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  long long before = 0, total = 0;
+  uint32_t before = 0, total = 0;
+#pragma unroll
   for (int w = 0; w < NW; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
+    const uint32_t x = warp_sum[w];
+    if (w < warp) before += x;
+    total += x;
   }
-  chunk_base[tid] = before + incl - mine;
-  __syncthreads();
-  const long long U = total * p.num_kv_heads;
-  // as many CTAs as give every warp a unit; the others have none
-  const long long nc = max(1ll, min(static_cast<long long>(gridDim.x), (U + NW - 1) / NW));
-  const long long W = nc * NW;
-  auto range_start = [&](long long i) { return min(i, W) * U / W; };
-  const long long wi = static_cast<long long>(blockIdx.x) * NW + warp;
-  const long long u0 = range_start(wi), u1 = range_start(wi + 1);
+  chunk_start[tid] = (before + incl - mine) * p.num_kv_heads;
+  any_empty = __syncthreads_or(any_empty);
+  const uint32_t U = total * p.num_kv_heads;  // below 2^31 (checked on the host)
+  // as many CTAs as give every warp a unit; the others have none.  CTA c's
+  // range, then the warp's part of it: equal to within a unit.
+  const uint32_t nc = max(1u, min(gridDim.x, (U + NW - 1) / NW));
+  const uint32_t cq = U / nc, crem = U - cq * nc;
+  uint32_t u0 = 0, u1 = 0;
+  if (blockIdx.x < nc) {
+    const uint32_t cs = blockIdx.x * cq + min(blockIdx.x, crem), size = cq + (blockIdx.x < crem ? 1 : 0);
+    const uint32_t wq = size / NW, wrem = size - wq * NW, w = warp;
+    u0 = cs + w * wq + min(w, wrem);
+    u1 = u0 + wq + (w < wrem ? 1 : 0);
+  }
 
   bool ok = true;
   if (u0 < u1) {
-    // ---- the run that unit u0 belongs to
+    // ---- the run that unit u0 belongs to: the last chunk that starts at or before it
     Cursor c;
     {
-      const long long key = u0 / p.num_kv_heads;  // units of whole sequences before it, per head
-      int lo = 0, hi = Sh::kThreads - 1;           // last chunk whose base is <= key
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (chunk_base[mid] <= key) lo = mid;
-        else hi = mid - 1;
-      }
-      long long base = chunk_base[lo];
-      int seq = lo * CH;
-      for (;;) {  // warp-wide walk of the chunk, 32 sequences at a time
-        const int s = seq + lane;
-        const int L = s < p.num_seqs ? length(s) : 0;
-        const int n = units(L);
-        long long pre = n;
+      int at = 0;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const long long t = __shfl_up_sync(0xffffffffu, pre, off);
-          if (lane >= off) pre += t;
+      for (int k = 0; k < NW; ++k) at += chunk_start[k * 32 + lane] <= u0 ? 1 : 0;
+      at = __reduce_add_sync(0xffffffffu, at) - 1;
+      uint32_t base = chunk_start[at];
+      c.seq = at;
+      c.len = chunk_len[at];
+      if (CH > 1) {  // walk the chunk, 32 sequences at a time
+        for (int seq = at * CH;; seq += 32) {
+          const int s = seq + lane, L = s < p.num_seqs ? length(s) : 0;
+          uint32_t pre = units(L) * p.num_kv_heads;
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t t = __shfl_up_sync(0xffffffffu, pre, off);
+            if (lane >= off) pre += t;
+          }
+          const unsigned in = __ballot_sync(0xffffffffu, u0 < base + pre);
+          if (in || seq + 32 >= p.num_seqs) {
+            const int src = in ? __ffs(in) - 1 : 31;
+            c.seq = min(seq + src, p.num_seqs - 1);
+            c.len = __shfl_sync(0xffffffffu, L, src);
+            base += src > 0 ? __shfl_sync(0xffffffffu, pre, src - 1) : 0;
+            break;
+          }
+          base += __shfl_sync(0xffffffffu, pre, 31);
         }
-        const unsigned in = __ballot_sync(0xffffffffu, key < base + pre);
-        if (in || seq + 32 >= p.num_seqs) {
-          const int src = in ? __ffs(in) - 1 : 31;
-          c.seq = seq + src;
-          c.n = max(1, __shfl_sync(0xffffffffu, n, src));
-          c.len = __shfl_sync(0xffffffffu, L, src);
-          base += __shfl_sync(0xffffffffu, pre, src) - c.n;
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, pre, 31);
-        seq += 32;
       }
-      const long long r = u0 - base * p.num_kv_heads;
-      c.h = static_cast<int>(r / c.n);
-      c.j = static_cast<int>(r - static_cast<long long>(c.h) * c.n);
+      c.n = max(1, static_cast<int>(units(c.len)));
+      c.h = static_cast<int>((u0 - base) / static_cast<uint32_t>(c.n));
+      c.j = static_cast<int>(u0 - base) - c.h * c.n;
       c.wbase = -32;
       c.window = -1;
       c.from0 = c.j == 0;
     }
 
     const uint64_t pol = l2_policy_evict_first();
-    long long next = u0;  // next unit to issue
+    uint32_t next = u0;  // next unit to issue
     // Issue the cursor's unit into stage s and move the cursor on (whole warp).
+    // meta[s]: {sequence, KV head, valid tokens | flags, units of the run behind this one};
+    // flags: 16 first unit of a piece, 17 last of a piece, 18 the piece began at its run's start, 19 it ends the run
     auto issue = [&](int s) {
       const int valid = min(UT, c.len - c.j * UT);
       const bool ends = c.j + 1 == c.n;
@@ -484,7 +514,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       if ((first_entry & ~31) != c.wbase) {
         c.wbase = first_entry & ~31;
         const int e = c.wbase + lane;
-        c.window = static_cast<long long>(e) * BS < c.len ? p.block_tables[static_cast<size_t>(c.seq) * p.max_blocks + e] : -1;
+        c.window =
+            static_cast<long long>(e) * BS < c.len ? p.block_tables[static_cast<size_t>(c.seq) * p.max_blocks + e] : -1;
       }
       const int nbox = BS <= UT ? (valid + BR - 1) / BR : 1;
       const uint32_t bar = full + 8 * s, kdst = ring + s * 2 * kUnitBytes, vdst = kdst + kUnitBytes;
@@ -492,7 +523,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         meta[s] = make_int4(c.seq, c.h,
                             valid | (next == u0 || c.j == 0 ? 1 << 16 : 0) | (ends || next + 1 == u1 ? 1 << 17 : 0) |
                                 (c.from0 ? 1 << 18 : 0) | (ends ? 1 << 19 : 0),
-                            0);
+                            c.n - 1 - c.j);
         mbar_arrive_expect_tx(bar, 2 * nbox * BOX_BYTES);
       }
       int erow = -1;  // this lane's 16 exponents: their first row, or none
@@ -518,6 +549,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
           cp_async16(exps + (s * 2 + value) * UT + (lane % (UT / 16)) * 16, (value ? p.v_exps : p.k_exps) + erow);
         cp_async_arrive(bar);
       }
+      if (c.j == 0 && lane * 64 < p.group * D)  // the run's queries, 128 bytes a lane
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            p.q + (static_cast<size_t>(c.seq) * p.num_q_heads + static_cast<size_t>(c.h) * p.group) * D + lane * 64));
+      __syncwarp();  // meta[s] is there for every lane
       ++next;
       if (!ends) {
         ++c.j;
@@ -525,42 +560,46 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       }
       c.j = 0;
       c.from0 = true;
-      if (next >= u1) return;
-      if (++c.h < p.num_kv_heads) {
-        // the same table: the window stands unless it has moved on
-        return;
-      }
+      if (next >= u1 || ++c.h < p.num_kv_heads) return;
       c.h = 0;
       do {
         c.len = c.seq + 1 < p.num_seqs ? length(++c.seq) : 1;  // (the range ends before the last sequence does)
       } while (c.len == 0);
-      c.n = units(c.len);
+      c.n = static_cast<int>(units(c.len));
       c.wbase = -32;
     };
 
-    const long long count = u1 - u0;
+    const int count = static_cast<int>(u1 - u0);
     for (int s = 0; s < S && s < count; ++s) issue(s);
 
     Acc<D, NT> acc;
     uint32_t qf[NT][D / 16][2];
     float cf[NT][2];
     const int g4 = lane >> 2, c4 = lane & 3;
-    long long i = 0;
+    int i = 0;
     for (; i < count; ++i) {
-      const int s = static_cast<int>(i % S);
+      const int s = i % S;
+      const int4 m = meta[s];
+      if (m.z & (1 << 16)) {  // while the unit is on its way
+        load_queries<D, NT>(p, m.x, m.y, qf, cf, lane);
+        acc.reset();
+      }
       if (!mbar_wait(full + 8 * s, static_cast<uint32_t>(i / S) & 1)) ok = false;
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0 && p.status) atomicOr(p.status, PKV_STATUS_TIMEOUT);
         ok = false;
         break;
       }
-      const int4 m = meta[s];
-      if (m.z & (1 << 16)) {
-        load_queries<D, NT>(p, m.x, m.y, qf, cf, lane);
-        acc.reset();
-      }
       const uint32_t kb = ring + s * 2 * kUnitBytes, eb = exps + s * 2 * UT;
-      attend_unit<D, NT>(acc, qf, cf, kb, kb + kUnitBytes, eb, eb + UT, m.z & 0xFFFF, lane);
+      const int valid = m.z & 0xFFFF;
+      if constexpr (Sh::kStep == UT) {
+        attend_tokens<D, NT, UT / 16>(acc, qf, cf, kb, kb + kUnitBytes, eb, eb + UT, valid, lane);
+      } else {
+#pragma unroll 1
+        for (int t = 0; t < valid; t += Sh::kStep)
+          attend_tokens<D, NT, Sh::kStep / 16>(acc, qf, cf, kb + t * D, kb + kUnitBytes + t * D, eb + t, eb + UT + t,
+                                               valid - t, lane);
+      }
       __syncwarp();
       if (next < u1) issue(s);
       if (m.z & (1 << 17)) {  // the piece ends here
@@ -613,64 +652,62 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                 dst[Sh::kTileFloats + nt * 8 + 2 * c4 + e] = acc.r[nt][e];
                 dst[Sh::kTileFloats + COLS + nt * 8 + 2 * c4 + e] = acc.l[nt][e];
               }
+          // {sequence | KV head << 16, 1 | began at the run's start << 1 | ends it << 2, the run's last unit}
           if (lane == 0)
-            pieces[2 * warp + (from0 ? 1 : 0)] = make_uint2(
-                static_cast<uint32_t>(m.x) | (static_cast<uint32_t>(m.y) << 16), 1u | (from0 ? 2u : 0u) | (ends ? 4u : 0u));
+            pieces[2 * warp + (from0 ? 1 : 0)] =
+                make_uint4(static_cast<uint32_t>(m.x) | (static_cast<uint32_t>(m.y) << 16),
+                           1u | (from0 ? 2u : 0u) | (ends ? 4u : 0u), u0 + i + m.w, 0u);
         }
       }
     }
     // after a timeout: leave no copy in flight into this CTA's shared memory
     if (!ok)
-      for (long long k = i + 1; k < next - u0; ++k) mbar_wait(full + 8 * static_cast<int>(k % S), (k / S) & 1);
+      for (int k = i + 1; k < static_cast<int>(next - u0); ++k) mbar_wait(full + 8 * (k % S), (k / S) & 1);
   }
   const bool failed = __syncthreads_or(!ok);
 
-  // ---- join the pieces of each run; warp w takes every NW-th (value step, tile)
+  // ---- join the pieces of each run: (run, value step, tile) triples go round the warps
   int4 desc = make_int4(0, 0, 0, 0);
   if (!failed) {
     const int c4 = lane & 3, g4 = lane >> 2;
-    auto place = [&](int k) -> const float * {
-      return (k & 1) ? reinterpret_cast<const float *>(smem + (k >> 1) * Sh::kRingBytes)
-                     : reinterpret_cast<const float *>(rest) + (k >> 1) * Sh::kPieceFloats;
-    };
-    for (int a = 0; a < 2 * NW;) {
-      const uint2 first = pieces[a];
-      if (!(first.y & 1u)) {
-        ++a;
-        continue;
-      }
-      int b = a;
-      uint32_t last_flags = first.y;
-      int k = a + 1;
-      for (; k < 2 * NW; ++k) {
-        const uint2 x = pieces[k];
-        if (!(x.y & 1u)) continue;
-        if (x.x != first.x || (x.y & 2u)) break;
-        b = k;
-        last_flags = x.y;
-      }
-      const int seq = first.x & 0xFFFF, h = first.x >> 16;
-      const bool from0 = first.y & 2u, ends = last_flags & 4u;
+    const uint4 info = lane < 2 * NW ? pieces[lane] : make_uint4(0u, 0u, 0u, 0u);
+    unsigned todo = __ballot_sync(0xffffffffu, info.y & 1u);
+    int turn = warp;  // this warp's next triple, counted from the current run's first
+    while (todo) {
+      const int a = __ffs(todo) - 1;
+      const uint32_t run = __shfl_sync(0xffffffffu, info.x, a);
+      const unsigned same = __ballot_sync(0xffffffffu, (info.y & 1u) && info.x == run);
+      const int b = 31 - __clz(same);
+      todo &= ~same;
+      const int seq = run & 0xFFFFu, h = run >> 16;
+      const bool from0 = __shfl_sync(0xffffffffu, info.y, a) & 2u, ends = __shfl_sync(0xffffffffu, info.y, b) & 4u;
+      const uint32_t last = __shfl_sync(0xffffffffu, info.z, a);
       float *dst = from0 && ends ? nullptr
                                  : p.ws + (static_cast<size_t>(blockIdx.x) * 2 + (from0 ? 1 : 0)) * Sh::kPieceFloats;
-      for (int t = warp; t < (D / 16) * NT; t += NW) {
-        const int md = t / NT, nt = t - md * NT, col = nt * 8 + 2 * c4;
-        float R[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        for (int q = a; q <= b; ++q) {
-          if (!(pieces[q].y & 1u)) continue;
-          const float *x = place(q) + Sh::kTileFloats + col;
-          R[0] = fmaxf(R[0], x[0]);
-          R[1] = fmaxf(R[1], x[1]);
+      for (; turn < (D / 16) * NT; turn += NW) {
+        const int t = turn, md = t / NT, nt = t - md * NT, col = nt * 8 + 2 * c4;
+        auto place = [&](int k) {
+          return reinterpret_cast<const float *>((k & 1) ? smem + (k >> 1) * Sh::kRingBytes
+                                                         : rest + (k >> 1) * (Sh::kPieceFloats * 4));
+        };
+        float2 R = make_float2(-INFINITY, -INFINITY);
+        for (unsigned left = same; left; left &= left - 1) {
+          const float2 r = *reinterpret_cast<const float2 *>(place(__ffs(left) - 1) + Sh::kTileFloats + col);
+          R.x = fmaxf(R.x, r.x);
+          R.y = fmaxf(R.y, r.y);
         }
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int q = a; q <= b; ++q) {
-          if (!(pieces[q].y & 1u)) continue;
-          const float *x = place(q);
-          const float r0 = x[Sh::kTileFloats + col], r1 = x[Sh::kTileFloats + col + 1];
-          const float f0 = r0 == -INFINITY ? 1.f : fast_exp2(r0 - R[0]), f1 = r1 == -INFINITY ? 1.f : fast_exp2(r1 - R[1]);
-          l[0] += x[Sh::kTileFloats + COLS + col] * f0;
-          l[1] += x[Sh::kTileFloats + COLS + col + 1] * f1;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll 2
+        for (unsigned left = same; left; left &= left - 1) {
+          const float *x = place(__ffs(left) - 1);
+          const float2 r = *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col);
+          const float2 l = *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + COLS + col);
           const float4 v = reinterpret_cast<const float4 *>(x)[t * 32 + lane];
+          const float f0 = r.x == -INFINITY ? 1.f : fast_exp2(r.x - R.x);
+          const float f1 = r.y == -INFINITY ? 1.f : fast_exp2(r.y - R.y);
+          l0 += l.x * f0;
+          l1 += l.y * f1;
           o.x += v.x * f0;
           o.y += v.y * f1;
           o.z += v.z * f0;
@@ -679,93 +716,80 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         if (dst) {
           reinterpret_cast<float4 *>(dst)[t * 32 + lane] = o;
           if (md == 0 && g4 == 0) {
-            dst[Sh::kTileFloats + col] = R[0];
-            dst[Sh::kTileFloats + col + 1] = R[1];
-            dst[Sh::kTileFloats + COLS + col] = l[0];
-            dst[Sh::kTileFloats + COLS + col + 1] = l[1];
+            *reinterpret_cast<float2 *>(dst + Sh::kTileFloats + col) = R;
+            *reinterpret_cast<float2 *>(dst + Sh::kTileFloats + COLS + col) = make_float2(l0, l1);
           }
         } else {
-          uint32_t *row = reinterpret_cast<uint32_t *>(
-              p.out + (static_cast<size_t>(seq) * p.num_q_heads + static_cast<size_t>(h) * p.group + col) * D +
-              g4 * (D / 8) + 2 * md);
-          const float i0 = l[0] == 0.f ? 0.f : 1.f / l[0], i1 = l[1] == 0.f ? 0.f : 1.f / l[1];
-          if (col < p.group) row[0] = pack_bf16x2(o.x * i0, o.z * i0);
-          if (col + 1 < p.group) row[D / 2] = pack_bf16x2(o.y * i1, o.w * i1);
+          store_quad<D>(p, seq, h, col, g4, md, o, l0, l1);
         }
       }
-      if (from0 && !ends) {  // leaves this CTA: the CTA that holds the run's last unit
-        long long end = 0;
-        // units up to the run's end: the CTA's last warp's cursor is gone, so count them again
-        const int n = units(length(seq));
-        // sequences before seq
-        const int ch = seq / CH;
-        long long base = chunk_base[ch];
-        for (int s = ch * CH; s < seq; ++s) base += units(length(s));
-        end = base * p.num_kv_heads + (static_cast<long long>(h) + 1) * n;  // one past its last unit
-        // owner warp of unit end - 1: the largest i with range_start(i) <= end - 1
-        const long long i = ((end - 1) * W + W - 1) / U;
-        long long o = min(i, W - 1);
-        while (o > 0 && range_start(o) > end - 1) --o;
-        while (o + 1 < W && range_start(o + 1) <= end - 1) ++o;
-        desc = make_int4(seq, h, static_cast<int>(o / NW), 1);
+      turn -= (D / 16) * NT;
+      if (from0 && !ends) {  // leaves this CTA: which one holds the run's last unit
+        const uint32_t big = crem * (cq + 1);
+        desc = make_int4(seq, h, static_cast<int>(last < big ? last / (cq + 1) : crem + (last - big) / cq), 1);
       }
-      a = k;
     }
   }
   if (tid == 0 && p.ws_desc) p.ws_desc[blockIdx.x] = desc;
 
   // ---- sequences without keys: zeros
-  for (long long s = blockIdx.x + static_cast<long long>(gridDim.x) * warp; s < p.num_seqs;
-       s += static_cast<long long>(gridDim.x) * NW) {
-    if (length(static_cast<int>(s)) != 0) continue;
+  if (!any_empty) return;
+  for (int s = blockIdx.x + gridDim.x * warp; s < p.num_seqs; s += gridDim.x * NW) {
+    if (length(s) != 0) continue;
     uint4 *dst = reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(s) * p.num_q_heads * D);
     for (int k = lane; k < p.num_q_heads * D / 8; k += 32) dst[k] = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
 // The run that starts in CTA c and spans more (blockIdx.x = c): the exact merge
-// of its pieces, one accumulator quad per thread.
+// of its pieces, one accumulator quad per thread, eight pieces in flight.
 template <int D, int NT>
 __global__ void __launch_bounds__(D * NT * 2) join_kernel(const Params p) {
   using Sh = Shape<D, NT>;
-  constexpr int COLS = NT * 8;
+  constexpr int COLS = NT * 8, FLY = 8;
   grid_launch_dependents();
-  grid_dependency_wait();  // the pieces come from the grid launched just before
-  const int4 desc = p.ws_desc[blockIdx.x];
-  if (desc.w == 0) return;
-  const int c0 = blockIdx.x, c1 = desc.z;
+  const int c0 = blockIdx.x;
   const int t = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane & 3, g4 = lane >> 2;
   const int md = t / NT, nt = t - md * NT, col = nt * 8 + 2 * c4;
-  auto piece = [&](int c) { return p.ws + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * Sh::kPieceFloats; };
-  float R0 = -INFINITY, R1 = -INFINITY;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float2 r = *reinterpret_cast<const float2 *>(piece(c) + Sh::kTileFloats + col);
-    R0 = fmaxf(R0, r.x);
-    R1 = fmaxf(R1, r.y);
-  }
+  grid_dependency_wait();  // the pieces come from the grid launched just before
+  const int4 desc = p.ws_desc[c0];
+  if (desc.w == 0) return;
+  const float *first = p.ws + (static_cast<size_t>(c0) * 2 + 1) * Sh::kPieceFloats;
+  const int n = desc.z - c0 + 1;  // pieces: CTA c0's last, then the first ones of the CTAs behind it
+  float2 R = make_float2(-INFINITY, -INFINITY);
   float l0 = 0.f, l1 = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float *x = piece(c);
-    const float2 r = *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col);
-    const float2 l = *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + COLS + col);
-    const float4 v = reinterpret_cast<const float4 *>(x)[t * 32 + lane];
-    const float f0 = r.x == -INFINITY ? 1.f : fast_exp2(r.x - R0), f1 = r.y == -INFINITY ? 1.f : fast_exp2(r.y - R1);
-    l0 += l.x * f0;
-    l1 += l.y * f1;
-    o.x += v.x * f0;
-    o.y += v.y * f1;
-    o.z += v.z * f0;
-    o.w += v.w * f1;
+  for (int base = 0; base < n; base += FLY) {
+    float2 r[FLY], l[FLY];
+    float4 v[FLY];
+#pragma unroll
+    for (int k = 0; k < FLY; ++k) {
+      const bool in = base + k < n;
+      const float *x = first + (base + k == 0 ? 0 : (base + k) * 2 - 1) * Sh::kPieceFloats;
+      r[k] = in ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col) : make_float2(-INFINITY, -INFINITY);
+      l[k] = in ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + COLS + col) : make_float2(0.f, 0.f);
+      v[k] = in ? reinterpret_cast<const float4 *>(x)[t * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float2 M = R;
+#pragma unroll
+    for (int k = 0; k < FLY; ++k) M.x = fmaxf(M.x, r[k].x), M.y = fmaxf(M.y, r[k].y);
+    const float a0 = R.x == -INFINITY ? 1.f : fast_exp2(R.x - M.x), a1 = R.y == -INFINITY ? 1.f : fast_exp2(R.y - M.y);
+    l0 *= a0, l1 *= a1, o.x *= a0, o.y *= a1, o.z *= a0, o.w *= a1;
+#pragma unroll
+    for (int k = 0; k < FLY; ++k) {
+      // (a piece without a maximum holds nothing, or NaN)
+      const float f0 = r[k].x == -INFINITY ? 1.f : fast_exp2(r[k].x - M.x);
+      const float f1 = r[k].y == -INFINITY ? 1.f : fast_exp2(r[k].y - M.y);
+      l0 += l[k].x * f0;
+      l1 += l[k].y * f1;
+      o.x += v[k].x * f0;
+      o.y += v[k].y * f1;
+      o.z += v[k].z * f0;
+      o.w += v[k].w * f1;
+    }
+    R = M;
   }
-  const float i0 = l0 == 0.f ? 0.f : 1.f / l0, i1 = l1 == 0.f ? 0.f : 1.f / l1;
-  uint32_t *row = reinterpret_cast<uint32_t *>(
-      p.out + (static_cast<size_t>(desc.x) * p.num_q_heads + static_cast<size_t>(desc.y) * p.group + col) * D +
-      g4 * (D / 8) + 2 * md);
-  if (col < p.group) row[0] = pack_bf16x2(o.x * i0, o.z * i0);
-  if (col + 1 < p.group) row[D / 2] = pack_bf16x2(o.y * i1, o.w * i1);
+  store_quad<D>(p, desc.x, desc.y, col, g4, md, o, l0, l1);
 }
 
 // ------------------------------------------------------------------------ host
@@ -815,6 +839,11 @@ int check_decode(const void *q, const void *k_codes, const void *v_codes, const 
     return PKV_ERR_ARG;
   const long long rows = static_cast<long long>(num_blocks) * num_kv_heads * block_size;
   if (rows + block_size >= 0x7fffff00ll) return PKV_ERR_UNSUPPORTED;
+  // the batch's units are counted in 31 bits
+  const long long len = std::min<long long>(max_seq_len, static_cast<long long>(max_blocks_per_seq) * block_size);
+  const int tokens = kUnitBytes / head_dim;
+  if (static_cast<double>(num_seqs) * num_kv_heads * ((len + tokens - 1) / tokens) >= 2147483648.0)
+    return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
 }
 
