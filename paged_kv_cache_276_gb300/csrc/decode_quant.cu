@@ -58,7 +58,7 @@ struct Params {
   const int32_t *block_tables, *seq_lens;
   __nv_bfloat16 *out;
   float *ws;      // [grid][2] pieces of runs that span CTAs, then [grid] descriptors
-  int4 *ws_desc;  // {sequence, KV head, last CTA of the run, 1} of the run that leaves CTA c, or .w = 0
+  int4 *ws_desc;  // {sequence | KV head << 16, -, last CTA of the run, 1} of the run that leaves CTA c, or .w = 0
   int32_t *status;
   int num_seqs, max_blocks, max_len, num_q_heads, num_kv_heads, group, num_blocks;
   float scale_log2;
@@ -351,16 +351,75 @@ __device__ __forceinline__ void attend_tokens(Acc<D, NT> &acc, const uint32_t (&
   }
 }
 
-// One quad of joined accumulators: values g D/8 + 2 md and + 1 of heads col and col + 1.
+// Values g D/8 + 2 md and + 1 of heads col and col + 1 from their joined accumulators.
 template <int D>
-__device__ __forceinline__ void store_quad(const Params &p, int seq, int h, int col, int g4, int md, const float4 &o,
+__device__ __forceinline__ void store_quad(const Params &p, uint32_t run, int col, int g4, int md, const float4 &o,
                                            float l0, float l1) {
-  uint32_t *row = reinterpret_cast<uint32_t *>(
-      p.out + (static_cast<size_t>(seq) * p.num_q_heads + static_cast<size_t>(h) * p.group + col) * D + g4 * (D / 8) +
-      2 * md);
+  const size_t seq = run & 0xFFFFu, h = run >> 16;
+  uint32_t *row = reinterpret_cast<uint32_t *>(p.out + (seq * p.num_q_heads + h * p.group + col) * D + g4 * (D / 8) +
+                                               2 * md);
   const float i0 = l0 == 0.f ? 0.f : 1.f / l0, i1 = l1 == 0.f ? 0.f : 1.f / l1;
   if (col < p.group) row[0] = pack_bf16x2(o.x * i0, o.z * i0);
   if (col + 1 < p.group) row[D / 2] = pack_bf16x2(o.y * i1, o.w * i1);
+}
+
+// Weight of a piece with reference r in a join to reference R; a piece without
+// a reference (-inf) holds nothing, or NaN: it counts as it is.
+__device__ __forceinline__ float piece_factor(float r, float R) { return r == -INFINITY ? 1.f : fast_exp2(r - R); }
+
+// Join of one run's pieces in shared memory: SPAN value steps from md0 on of
+// tile nt.  The whole run goes to the output, a part of one to the workspace.
+//   g: {bits of the pieces' places, run, 2 began at the run's start | 4 ends it, -}
+template <int D, int NT, int SPAN>
+__device__ __forceinline__ void join_pieces(const Params &p, const uint4 g, int nt, int md0, const uint8_t *smem,
+                                         const uint8_t *rest, int lane) {
+  using Sh = Shape<D, NT>;
+  constexpr int COLS = NT * 8;
+  const int col = nt * 8 + 2 * (lane & 3);
+  auto place = [&](int k) {
+    return reinterpret_cast<const float *>((k & 1) ? smem + (k >> 1) * Sh::kRingBytes
+                                                   : rest + (k >> 1) * (Sh::kPieceFloats * 4));
+  };
+  float2 R = make_float2(-INFINITY, -INFINITY);
+#pragma unroll 1
+  for (unsigned left = g.x; left; left &= left - 1) {
+    const float2 r = *reinterpret_cast<const float2 *>(place(__ffs(left) - 1) + Sh::kTileFloats + col);
+    R.x = fmaxf(R.x, r.x);
+    R.y = fmaxf(R.y, r.y);
+  }
+  float4 o[SPAN];
+#pragma unroll
+  for (int m = 0; m < SPAN; ++m) o[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float2 l = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (unsigned left = g.x; left; left &= left - 1) {
+    const float *x = place(__ffs(left) - 1);
+    const float2 r = *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col);
+    const float2 pl = *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + COLS + col);
+    const float f0 = piece_factor(r.x, R.x), f1 = piece_factor(r.y, R.y);
+    l.x += pl.x * f0;
+    l.y += pl.y * f1;
+#pragma unroll
+    for (int m = 0; m < SPAN; ++m) {
+      const float4 v = reinterpret_cast<const float4 *>(x)[((md0 + m) * NT + nt) * 32 + lane];
+      o[m].x += v.x * f0;
+      o[m].y += v.y * f1;
+      o[m].z += v.z * f0;
+      o[m].w += v.w * f1;
+    }
+  }
+  if ((g.z & 6u) == 6u) {
+#pragma unroll
+    for (int m = 0; m < SPAN; ++m) store_quad<D>(p, g.y, col, lane >> 2, md0 + m, o[m], l.x, l.y);
+    return;
+  }
+  float *dst = p.ws + (static_cast<size_t>(blockIdx.x) * 2 + (g.z & 2u ? 1 : 0)) * Sh::kPieceFloats;
+#pragma unroll
+  for (int m = 0; m < SPAN; ++m) reinterpret_cast<float4 *>(dst)[((md0 + m) * NT + nt) * 32 + lane] = o[m];
+  if (md0 == 0 && lane < 4) {
+    *reinterpret_cast<float2 *>(dst + Sh::kTileFloats + col) = R;
+    *reinterpret_cast<float2 *>(dst + Sh::kTileFloats + COLS + col) = l;
+  }
 }
 
 // Where a warp's producer stands: run (seq, h) of n units, its next unit j.
@@ -382,7 +441,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   constexpr int EXP_LANES = 2 * UT / 16;  // 16 exponent bytes each
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t warp_sum[NW];
-  __shared__ uint32_t chunk_start[TH];  // first unit of each thread's sequences
+  __shared__ __align__(16) uint32_t chunk_start[TH];  // first unit of each thread's sequences
   __shared__ int chunk_len[TH];         // their length, where a thread has one sequence
   __shared__ uint4 pieces[2 * NW];      // each warp's first and last incomplete piece (see flush)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -666,71 +725,45 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   }
   const bool failed = __syncthreads_or(!ok);
 
-  // ---- join the pieces of each run: (run, value step, tile) triples go round the warps
-  int4 desc = make_int4(0, 0, 0, 0);
+  // ---- join the pieces of each run
   if (!failed) {
-    const int c4 = lane & 3, g4 = lane >> 2;
+    // the pieces of one run each: {their places, run, flags, its last unit}
+    uint4 *groups = reinterpret_cast<uint4 *>(chunk_start);
+    static_assert(2 * NW * sizeof(uint4) <= sizeof chunk_start, "the table goes over the prefix sums");
+    const unsigned below = (1u << lane) - 1;
     const uint4 info = lane < 2 * NW ? pieces[lane] : make_uint4(0u, 0u, 0u, 0u);
-    unsigned todo = __ballot_sync(0xffffffffu, info.y & 1u);
-    int turn = warp;  // this warp's next triple, counted from the current run's first
-    while (todo) {
-      const int a = __ffs(todo) - 1;
-      const uint32_t run = __shfl_sync(0xffffffffu, info.x, a);
-      const unsigned same = __ballot_sync(0xffffffffu, (info.y & 1u) && info.x == run);
-      const int b = 31 - __clz(same);
-      todo &= ~same;
-      const int seq = run & 0xFFFFu, h = run >> 16;
-      const bool from0 = __shfl_sync(0xffffffffu, info.y, a) & 2u, ends = __shfl_sync(0xffffffffu, info.y, b) & 4u;
-      const uint32_t last = __shfl_sync(0xffffffffu, info.z, a);
-      float *dst = from0 && ends ? nullptr
-                                 : p.ws + (static_cast<size_t>(blockIdx.x) * 2 + (from0 ? 1 : 0)) * Sh::kPieceFloats;
-      for (; turn < (D / 16) * NT; turn += NW) {
-        const int t = turn, md = t / NT, nt = t - md * NT, col = nt * 8 + 2 * c4;
-        auto place = [&](int k) {
-          return reinterpret_cast<const float *>((k & 1) ? smem + (k >> 1) * Sh::kRingBytes
-                                                         : rest + (k >> 1) * (Sh::kPieceFloats * 4));
-        };
-        float2 R = make_float2(-INFINITY, -INFINITY);
-        for (unsigned left = same; left; left &= left - 1) {
-          const float2 r = *reinterpret_cast<const float2 *>(place(__ffs(left) - 1) + Sh::kTileFloats + col);
-          R.x = fmaxf(R.x, r.x);
-          R.y = fmaxf(R.y, r.y);
-        }
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll 2
-        for (unsigned left = same; left; left &= left - 1) {
-          const float *x = place(__ffs(left) - 1);
-          const float2 r = *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col);
-          const float2 l = *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + COLS + col);
-          const float4 v = reinterpret_cast<const float4 *>(x)[t * 32 + lane];
-          const float f0 = r.x == -INFINITY ? 1.f : fast_exp2(r.x - R.x);
-          const float f1 = r.y == -INFINITY ? 1.f : fast_exp2(r.y - R.y);
-          l0 += l.x * f0;
-          l1 += l.y * f1;
-          o.x += v.x * f0;
-          o.y += v.y * f1;
-          o.z += v.z * f0;
-          o.w += v.w * f1;
-        }
-        if (dst) {
-          reinterpret_cast<float4 *>(dst)[t * 32 + lane] = o;
-          if (md == 0 && g4 == 0) {
-            *reinterpret_cast<float2 *>(dst + Sh::kTileFloats + col) = R;
-            *reinterpret_cast<float2 *>(dst + Sh::kTileFloats + COLS + col) = make_float2(l0, l1);
-          }
-        } else {
-          store_quad<D>(p, seq, h, col, g4, md, o, l0, l1);
-        }
-      }
-      turn -= (D / 16) * NT;
-      if (from0 && !ends) {  // leaves this CTA: which one holds the run's last unit
-        const uint32_t big = crem * (cq + 1);
-        desc = make_int4(seq, h, static_cast<int>(last < big ? last / (cq + 1) : crem + (last - big) / cq), 1);
-      }
+    const unsigned all = __ballot_sync(0xffffffffu, info.y & 1u);
+    // a piece opens a group where the one before it is another run's
+    const uint32_t before_it = __shfl_sync(0xffffffffu, info.x, 31 - __clz(all & below | 1u));
+    const bool opens = (info.y & 1u) && (!(all & below) || before_it != info.x);
+    const unsigned starts = __ballot_sync(0xffffffffu, opens);
+    const unsigned later = starts & ~below & ~(1u << lane);
+    const unsigned same = all & ~below & (later ? (later & -later) - 1 : ~0u);
+    const uint32_t end_flags = __shfl_sync(0xffffffffu, info.y, same ? 31 - __clz(same) : 0);
+    // every warp writes the same table, and reads what it wrote
+    if (opens)
+      groups[__popc(starts & below)] = make_uint4(same, info.x, (info.y & 2u) | (end_flags & 4u), info.z);
+    __syncwarp();
+    const int count = __popc(starts);
+    // few runs: a warp takes one value step of a run's tile; many: the whole tile
+    if (count * NT <= 3) {
+      for (int t = warp; t < count * NT * (D / 16); t += NW)
+        join_pieces<D, NT, 1>(p, groups[t / (NT * (D / 16))], t / (D / 16) % NT, t % (D / 16), smem, rest, lane);
+    } else {
+      for (int t = warp; t < count * NT; t += NW)
+        join_pieces<D, NT, D / 16>(p, groups[t / NT], t % NT, 0, smem, rest, lane);
     }
+    if (tid == 0 && p.ws_desc) {  // the run that leaves this CTA, if any, and the CTA that holds its last unit
+      const uint4 g = count ? groups[count - 1] : make_uint4(0u, 0u, 4u, 0u);
+      const uint32_t big = crem * (cq + 1);
+      int4 desc = make_int4(0, 0, 0, 0);
+      if ((g.z & 6u) == 2u)
+        desc = make_int4(g.y, 0, static_cast<int>(g.w < big ? g.w / (cq + 1) : crem + (g.w - big) / cq), 1);
+      p.ws_desc[blockIdx.x] = desc;
+    }
+  } else if (tid == 0 && p.ws_desc) {
+    p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  if (tid == 0 && p.ws_desc) p.ws_desc[blockIdx.x] = desc;
 
   // ---- sequences without keys: zeros
   if (!any_empty) return;
@@ -789,7 +822,7 @@ __global__ void __launch_bounds__(D * NT * 2) join_kernel(const Params p) {
     }
     R = M;
   }
-  store_quad<D>(p, desc.x, desc.y, col, g4, md, o, l0, l1);
+  store_quad<D>(p, static_cast<uint32_t>(desc.x), col, g4, md, o, l0, l1);
 }
 
 // ------------------------------------------------------------------------ host

@@ -572,3 +572,21 @@ def test_a_generation_over_the_8_bit_cache():
                                     num_kv_heads=Hkv, head_dim=d, block_size=bs, scale=scale)
     assert (np.abs(out.double().cpu().numpy() - ref) <= 1e-2 + 1e-2 * np.abs(ref)).all()
     assert st.item() == 0
+
+
+def test_one_workspace_serves_any_sizes_whatever_it_held():
+    """Calls of different sizes in turn over one buffer, which is filled with other bytes before some."""
+    cases = [([5000, 40], 128, 16, 16, 2), ([700] * 9, 64, 64, 6, 3), ([33000], 128, 32, 16, 1), ([1, 2, 3], 64, 16, 4, 4)]
+    size = max(native.paged_attention_decode_quant_workspace_size(len(n), Hq, Hkv, d, max(n)) for n, d, _, Hq, Hkv in cases)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    for round_ in range(3):
+        for i, (lens, d, bs, Hq, Hkv) in enumerate(cases):
+            if round_ == 1:
+                ws.fill_([0, 0xFF, 0xA5, 1][i])
+            elif round_ == 2:
+                ws.copy_(torch.randint(0, 256, ws.shape, generator=g, device="cuda", dtype=torch.uint8))
+            q, host, tables = decode_case(lens, d, bs, Hq, Hkv, seed=60 + i)
+            out = run_decode(q, cache_on_gpu(*host), tables, lens, d ** -0.5, ws=ws)
+            check_decode(out, q, host, tables, lens, d ** -0.5, f"round {round_}, case {i}")
