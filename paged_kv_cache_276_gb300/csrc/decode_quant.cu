@@ -367,12 +367,12 @@ __device__ __forceinline__ void store_quad(const Params &p, uint32_t run, int co
 // a reference (-inf) holds nothing, or NaN: it counts as it is.
 __device__ __forceinline__ float piece_factor(float r, float R) { return r == -INFINITY ? 1.f : fast_exp2(r - R); }
 
-// Join of one run's pieces in shared memory: SPAN value steps from md0 on of
-// tile nt.  The whole run goes to the output, a part of one to the workspace.
+// Join of one run's pieces in shared memory, tile nt, by one warp.  The whole
+// run goes to the output, a part of one to the workspace.
 //   g: {bits of the pieces' places, run, 2 began at the run's start | 4 ends it, -}
-template <int D, int NT, int SPAN>
-__device__ __forceinline__ void join_pieces(const Params &p, const uint4 g, int nt, int md0, const uint8_t *smem,
-                                         const uint8_t *rest, int lane) {
+template <int D, int NT>
+__device__ __forceinline__ void join_pieces(const Params &p, const uint4 g, int nt, const uint8_t *smem,
+                                            const uint8_t *rest, int lane) {
   using Sh = Shape<D, NT>;
   constexpr int COLS = NT * 8;
   const int col = nt * 8 + 2 * (lane & 3);
@@ -387,9 +387,9 @@ __device__ __forceinline__ void join_pieces(const Params &p, const uint4 g, int 
     R.x = fmaxf(R.x, r.x);
     R.y = fmaxf(R.y, r.y);
   }
-  float4 o[SPAN];
+  float4 o[D / 16];
 #pragma unroll
-  for (int m = 0; m < SPAN; ++m) o[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int md = 0; md < D / 16; ++md) o[md] = make_float4(0.f, 0.f, 0.f, 0.f);
   float2 l = make_float2(0.f, 0.f);
 #pragma unroll 1
   for (unsigned left = g.x; left; left &= left - 1) {
@@ -400,23 +400,23 @@ __device__ __forceinline__ void join_pieces(const Params &p, const uint4 g, int 
     l.x += pl.x * f0;
     l.y += pl.y * f1;
 #pragma unroll
-    for (int m = 0; m < SPAN; ++m) {
-      const float4 v = reinterpret_cast<const float4 *>(x)[((md0 + m) * NT + nt) * 32 + lane];
-      o[m].x += v.x * f0;
-      o[m].y += v.y * f1;
-      o[m].z += v.z * f0;
-      o[m].w += v.w * f1;
+    for (int md = 0; md < D / 16; ++md) {
+      const float4 v = reinterpret_cast<const float4 *>(x)[(md * NT + nt) * 32 + lane];
+      o[md].x += v.x * f0;
+      o[md].y += v.y * f1;
+      o[md].z += v.z * f0;
+      o[md].w += v.w * f1;
     }
   }
   if ((g.z & 6u) == 6u) {
 #pragma unroll
-    for (int m = 0; m < SPAN; ++m) store_quad<D>(p, g.y, col, lane >> 2, md0 + m, o[m], l.x, l.y);
+    for (int md = 0; md < D / 16; ++md) store_quad<D>(p, g.y, col, lane >> 2, md, o[md], l.x, l.y);
     return;
   }
   float *dst = p.ws + (static_cast<size_t>(blockIdx.x) * 2 + (g.z & 2u ? 1 : 0)) * Sh::kPieceFloats;
 #pragma unroll
-  for (int m = 0; m < SPAN; ++m) reinterpret_cast<float4 *>(dst)[((md0 + m) * NT + nt) * 32 + lane] = o[m];
-  if (md0 == 0 && lane < 4) {
+  for (int md = 0; md < D / 16; ++md) reinterpret_cast<float4 *>(dst)[(md * NT + nt) * 32 + lane] = o[md];
+  if (lane < 4) {
     *reinterpret_cast<float2 *>(dst + Sh::kTileFloats + col) = R;
     *reinterpret_cast<float2 *>(dst + Sh::kTileFloats + COLS + col) = l;
   }
@@ -745,15 +745,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       groups[__popc(starts & below)] = make_uint4(same, info.x, (info.y & 2u) | (end_flags & 4u), info.z);
     __syncwarp();
     const int count = __popc(starts);
-    // few runs: a warp takes one value step of a run's tile; many: the whole tile
-    if (count * NT <= 3) {
-      for (int t = warp; t < count * NT * (D / 16); t += NW)
-        join_pieces<D, NT, 1>(p, groups[t / (NT * (D / 16))], t / (D / 16) % NT, t % (D / 16), smem, rest, lane);
-    } else {
-      for (int t = warp; t < count * NT; t += NW)
-        join_pieces<D, NT, D / 16>(p, groups[t / NT], t % NT, 0, smem, rest, lane);
-    }
-    if (tid == 0 && p.ws_desc) {  // the run that leaves this CTA, if any, and the CTA that holds its last unit
+    if (tid == TH - 1 && p.ws_desc) {  // the run that leaves this CTA, if any, and the CTA that holds its last unit
       const uint4 g = count ? groups[count - 1] : make_uint4(0u, 0u, 4u, 0u);
       const uint32_t big = crem * (cq + 1);
       int4 desc = make_int4(0, 0, 0, 0);
@@ -761,6 +753,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         desc = make_int4(g.y, 0, static_cast<int>(g.w < big ? g.w / (cq + 1) : crem + (g.w - big) / cq), 1);
       p.ws_desc[blockIdx.x] = desc;
     }
+    for (int t = warp; t < count * NT; t += NW) join_pieces<D, NT>(p, groups[t / NT], t % NT, smem, rest, lane);
   } else if (tid == 0 && p.ws_desc) {
     p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
@@ -775,54 +768,75 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 }
 
 // The run that starts in CTA c and spans more (blockIdx.x = c): the exact merge
-// of its pieces, one accumulator quad per thread, eight pieces in flight.
+// of its pieces, CTA c's last and the first ones of the CTAs behind it.  Every
+// kSplit-th piece goes to one group of threads, five in flight (a run spans
+// 1/8 of the grid where one sequence has 8 KV heads: one round), and the
+// groups are joined in shared memory; a thread holds one accumulator quad.
 template <int D, int NT>
-__global__ void __launch_bounds__(D * NT * 2) join_kernel(const Params p) {
+struct JoinShape {
+  static constexpr int kLanes = D * NT * 2;
+  static constexpr int kSplit = kLanes <= 256 ? 4 : 2;
+  static constexpr int kThreads = kLanes * kSplit;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(JoinShape<D, NT>::kThreads) join_kernel(const Params p) {
   using Sh = Shape<D, NT>;
-  constexpr int COLS = NT * 8, FLY = 8;
+  using J = JoinShape<D, NT>;
+  constexpr int COLS = NT * 8, FLY = 5;
+  __shared__ float4 part[J::kSplit - 1][2][J::kLanes];
   grid_launch_dependents();
-  const int c0 = blockIdx.x;
-  const int t = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane & 3, g4 = lane >> 2;
+  const int c0 = blockIdx.x, grp = threadIdx.x / J::kLanes, quad = threadIdx.x % J::kLanes;
+  const int t = quad >> 5, lane = quad & 31, c4 = lane & 3, g4 = lane >> 2;
   const int md = t / NT, nt = t - md * NT, col = nt * 8 + 2 * c4;
   grid_dependency_wait();  // the pieces come from the grid launched just before
   const int4 desc = p.ws_desc[c0];
   if (desc.w == 0) return;
   const float *first = p.ws + (static_cast<size_t>(c0) * 2 + 1) * Sh::kPieceFloats;
-  const int n = desc.z - c0 + 1;  // pieces: CTA c0's last, then the first ones of the CTAs behind it
-  float2 R = make_float2(-INFINITY, -INFINITY);
-  float l0 = 0.f, l1 = 0.f;
+  const int n = desc.z - c0 + 1;
+  float2 R = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int base = 0; base < n; base += FLY) {
-    float2 r[FLY], l[FLY];
+  // acc := acc 2^(R - M) + piece 2^(r - M)
+  auto scale = [&](const float2 &M) {
+    const float f0 = piece_factor(R.x, M.x), f1 = piece_factor(R.y, M.y);
+    l.x *= f0, l.y *= f1, o.x *= f0, o.y *= f1, o.z *= f0, o.w *= f1;
+    R = M;
+  };
+  auto add = [&](const float2 &r, const float2 &pl, const float4 &v) {
+    const float f0 = piece_factor(r.x, R.x), f1 = piece_factor(r.y, R.y);
+    l.x += pl.x * f0, l.y += pl.y * f1, o.x += v.x * f0, o.y += v.y * f1, o.z += v.z * f0, o.w += v.w * f1;
+  };
+  for (int base = grp; base < n; base += FLY * J::kSplit) {
+    float2 r[FLY], pl[FLY];
     float4 v[FLY];
 #pragma unroll
     for (int k = 0; k < FLY; ++k) {
-      const bool in = base + k < n;
-      const float *x = first + (base + k == 0 ? 0 : (base + k) * 2 - 1) * Sh::kPieceFloats;
-      r[k] = in ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col) : make_float2(-INFINITY, -INFINITY);
-      l[k] = in ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + COLS + col) : make_float2(0.f, 0.f);
-      v[k] = in ? reinterpret_cast<const float4 *>(x)[t * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const int i = base + k * J::kSplit;
+      const float *x = first + (i == 0 ? 0 : i * 2 - 1) * static_cast<size_t>(Sh::kPieceFloats);
+      r[k] = i < n ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col) : make_float2(-INFINITY, -INFINITY);
+      pl[k] = i < n ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + COLS + col) : make_float2(0.f, 0.f);
+      v[k] = i < n ? reinterpret_cast<const float4 *>(x)[t * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float2 M = R;
 #pragma unroll
     for (int k = 0; k < FLY; ++k) M.x = fmaxf(M.x, r[k].x), M.y = fmaxf(M.y, r[k].y);
-    const float a0 = R.x == -INFINITY ? 1.f : fast_exp2(R.x - M.x), a1 = R.y == -INFINITY ? 1.f : fast_exp2(R.y - M.y);
-    l0 *= a0, l1 *= a1, o.x *= a0, o.y *= a1, o.z *= a0, o.w *= a1;
+    scale(M);
 #pragma unroll
-    for (int k = 0; k < FLY; ++k) {
-      // (a piece without a maximum holds nothing, or NaN)
-      const float f0 = r[k].x == -INFINITY ? 1.f : fast_exp2(r[k].x - M.x);
-      const float f1 = r[k].y == -INFINITY ? 1.f : fast_exp2(r[k].y - M.y);
-      l0 += l[k].x * f0;
-      l1 += l[k].y * f1;
-      o.x += v[k].x * f0;
-      o.y += v[k].y * f1;
-      o.z += v[k].z * f0;
-      o.w += v[k].w * f1;
-    }
-    R = M;
+    for (int k = 0; k < FLY; ++k) add(r[k], pl[k], v[k]);
   }
-  store_quad<D>(p, static_cast<uint32_t>(desc.x), col, g4, md, o, l0, l1);
+  if (grp > 0) {
+    part[grp - 1][0][quad] = o;
+    part[grp - 1][1][quad] = make_float4(R.x, R.y, l.x, l.y);
+  }
+  __syncthreads();
+  if (grp > 0) return;
+  for (int k = 1; k < min(n, J::kSplit); ++k) {
+    const float4 x = part[k - 1][1][quad];
+    const float2 r = make_float2(x.x, x.y);
+    scale(make_float2(fmaxf(R.x, r.x), fmaxf(R.y, r.y)));
+    add(r, make_float2(x.z, x.w), part[k - 1][0][quad]);
+  }
+  store_quad<D>(p, static_cast<uint32_t>(desc.x), col, g4, md, o, l.x, l.y);
 }
 
 // ------------------------------------------------------------------------ host
@@ -904,7 +918,7 @@ cudaError_t launch(const CUtensorMap &tmk, const CUtensorMap &tmv, const Params 
   auto k = decode_quant_kernel<D, BS, NT>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmemBytes);
   if (e == cudaSuccess) e = launch_pdl(k, grid, Sh::kThreads, Sh::kSmemBytes, stream, tmk, tmv, p);
-  if (e == cudaSuccess && grid > 1) e = launch_pdl(join_kernel<D, NT>, grid, D * NT * 2, 0, stream, p);
+  if (e == cudaSuccess && grid > 1) e = launch_pdl(join_kernel<D, NT>, grid, JoinShape<D, NT>::kThreads, 0, stream, p);
   return e;
 }
 

@@ -8,7 +8,6 @@ if the library is missing, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -517,50 +516,65 @@ def paged_attention_decode_static_scratch(q, k_cache, v_cache, block_tables, seq
 
 
 # ------------------------------------------------------- the cache in 8 bits
-def _quant_cache(k_codes, v_codes, k_exps, v_exps):
-    """The cache's shape (NB, Hkv, bs, d) and device, its four tensors checked."""
-    dev = k_codes.device
-    for t, n in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-        _need(t, torch.float8_e4m3fn, n, dev)
-    for t, n in ((k_exps, "k_exps"), (v_exps, "v_exps")):
-        _need(t, torch.uint8, n, dev)
-    if k_codes.dim() != 4 or v_codes.shape != k_codes.shape or k_exps.shape != k_codes.shape[:3] \
-            or v_exps.shape != k_exps.shape:
+# These calls are short on the GPU (a few microseconds for a decode step's
+# write), so the checks are written to cost little: one pass over the tensors,
+# addresses passed as plain integers.
+_BF16, _F8, _U8, _I32, _I64 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64
+
+
+def _need_all(dev, *triples):
+    """Each (tensor, dtype, name): a dense tensor of that type on ``dev``."""
+    for t, dtype, name in triples:
+        if t.__class__ is not torch.Tensor or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+            _need(t, dtype, name, dev)  # says what is wrong (a Tensor's subclass may be fine)
+
+
+def _quant_cache_shape(k_codes, v_codes, k_exps, v_exps):
+    shape = k_codes.shape
+    if len(shape) != 4 or v_codes.shape != shape or k_exps.shape != shape[:3] or v_exps.shape != shape[:3]:
         raise ValueError("shape mismatch: codes [NB, Hkv, bs, d] and exponents [NB, Hkv, bs] expected")
-    return k_codes.shape, dev
+    return shape
 
 
 def _status(d_status, dev):
-    if d_status is not None:
-        _need(d_status, torch.int32, "d_status", dev)
-        if d_status.numel() < 1:
-            raise ValueError("d_status: one int32 expected")
-    return _ptr(d_status)
+    if d_status is None:
+        return None
+    _need_all(dev, (d_status, _I32, "d_status"))
+    if d_status.numel() < 1:
+        raise ValueError("d_status: one int32 expected")
+    return d_status.data_ptr()
 
 
-def _on(dev):
-    """Context that makes ``dev`` current (its kernels are launched from there); nothing to do when it is."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-
-def _need_cuda(dev):
+def _launch(fn, name, dev, stream, args):
+    """Call ``fn(*args, stream)`` with ``dev`` current (its kernels are launched from there)."""
     if dev.type != "cuda":
         raise ValueError(f"the cache must be on a CUDA device, got {dev}")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != PKV_OK:
+        raise PkvError(rc, name)
 
 
 def _token_rows(t, name, shape, dev):
     """The stride in elements between tokens of [T, Hkv, d] rows whose own values are dense."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or t.dtype != _BF16:
         raise TypeError(f"{name} must be a torch.bfloat16 tensor")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
     T, Hkv, d = shape
-    if T <= 1 and t.is_contiguous():
+    if t.is_contiguous():
         return Hkv * d
     s = t.stride()
-    if T > 0 and (s[2] != 1 and d > 1 or s[1] != d and Hkv > 1 or s[0] < Hkv * d or s[0] % 8):
+    if T > 0 and (s[2] != 1 and d > 1 or s[1] != d and Hkv > 1 or T > 1 and (s[0] < Hkv * d or s[0] % 8)):
         raise ValueError(f"{name}: each token's [Hkv, d] rows must be dense, tokens a multiple of 8 elements apart")
     return s[0] if T > 1 else Hkv * d
 
@@ -569,34 +583,32 @@ def pkv_write_quant(k, v, slot_mapping, k_codes, v_codes, k_exps, v_exps, d_stat
     """Quantise new tokens into an 8-bit cache.  k, v: [T, Hkv, d] bf16, each token's rows dense (views of a
     fused projection's output are fine); slot_mapping: [T] int64, negative: skip; codes [NB, Hkv, bs, d]
     float8_e4m3fn, exponents [NB, Hkv, bs] uint8 (device).  d: a multiple of 16."""
-    (NB, Hkv, bs, d), dev = _quant_cache(k_codes, v_codes, k_exps, v_exps)
-    _need(slot_mapping, torch.int64, "slot_mapping", dev)
+    dev = k_codes.device
+    _need_all(dev, (k_codes, _F8, "k_codes"), (v_codes, _F8, "v_codes"), (k_exps, _U8, "k_exps"),
+              (v_exps, _U8, "v_exps"), (slot_mapping, _I64, "slot_mapping"))
+    NB, Hkv, bs, d = _quant_cache_shape(k_codes, v_codes, k_exps, v_exps)
     if slot_mapping.dim() != 1:
         raise ValueError("slot_mapping: [T] expected")
-    T = slot_mapping.shape[0]
-    ks, vs = _token_rows(k, "k", (T, Hkv, d), dev), _token_rows(v, "v", (T, Hkv, d), dev)
-    _need_cuda(dev)
-    with _on(dev):
-        _check(lib().pkv_write_quant(_ptr(k), _ptr(v), ks, vs, _ptr(slot_mapping), T, _ptr(k_codes), _ptr(v_codes),
-                                     _ptr(k_exps), _ptr(v_exps), NB, bs, Hkv, d, _status(d_status, dev),
-                                     _stream(stream, dev)), "pkv_write_quant")
+    shape = (slot_mapping.shape[0], Hkv, d)
+    ks, vs = _token_rows(k, "k", shape, dev), _token_rows(v, "v", shape, dev)
+    _launch(lib().pkv_write_quant, "pkv_write_quant", dev, stream,
+            (k.data_ptr(), v.data_ptr(), ks, vs, slot_mapping.data_ptr(), shape[0], k_codes.data_ptr(),
+             v_codes.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(), NB, bs, Hkv, d, _status(d_status, dev)))
 
 
 def pkv_read_quant(k_codes, v_codes, k_exps, v_exps, slot_mapping, k, v, d_status=None, stream=None):
     """Rows of listed slots of an 8-bit cache, exactly, into k, v [T, Hkv, d] bf16 (rows of negative slots stay
     as they are); the cache as in ``pkv_write_quant``."""
-    (NB, Hkv, bs, d), dev = _quant_cache(k_codes, v_codes, k_exps, v_exps)
-    _need(slot_mapping, torch.int64, "slot_mapping", dev)
-    _need(k, torch.bfloat16, "k", dev)
-    _need(v, torch.bfloat16, "v", dev)
+    dev = k_codes.device
+    _need_all(dev, (k_codes, _F8, "k_codes"), (v_codes, _F8, "v_codes"), (k_exps, _U8, "k_exps"),
+              (v_exps, _U8, "v_exps"), (slot_mapping, _I64, "slot_mapping"), (k, _BF16, "k"), (v, _BF16, "v"))
+    NB, Hkv, bs, d = _quant_cache_shape(k_codes, v_codes, k_exps, v_exps)
     T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
     if k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
         raise ValueError("shape mismatch between k/v, slot_mapping [T] and the cache")
-    _need_cuda(dev)
-    with _on(dev):
-        _check(lib().pkv_read_quant(_ptr(k_codes), _ptr(v_codes), _ptr(k_exps), _ptr(v_exps), _ptr(slot_mapping), T,
-                                    _ptr(k), _ptr(v), NB, bs, Hkv, d, _status(d_status, dev), _stream(stream, dev)),
-               "pkv_read_quant")
+    _launch(lib().pkv_read_quant, "pkv_read_quant", dev, stream,
+            (k_codes.data_ptr(), v_codes.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(), slot_mapping.data_ptr(), T,
+             k.data_ptr(), v.data_ptr(), NB, bs, Hkv, d, _status(d_status, dev)))
 
 
 def paged_attention_decode_quant_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len):
@@ -609,26 +621,24 @@ def paged_attention_decode_quant(q, k_codes, v_codes, k_exps, v_exps, block_tabl
     """Single-token decode over an 8-bit cache: q, out [B, 1, Hq, d] bf16; the cache as in ``pkv_write_quant``;
     tables [B, max_blocks] int32; lens [B] int32; workspace: a device buffer of
     ``paged_attention_decode_quant_workspace_size`` bytes (one per call that may overlap)."""
-    (NB, Hkv, bs, d), dev = _quant_cache(k_codes, v_codes, k_exps, v_exps)
-    _need(q, torch.bfloat16, "q", dev)
-    _need(out, torch.bfloat16, "out", dev)
-    _need(block_tables, torch.int32, "block_tables", dev)
-    _need(seq_lens, torch.int32, "seq_lens", dev)
-    if q.dim() != 4 or q.shape[1] != 1 or q.shape[3] != d or out.shape != q.shape or block_tables.dim() != 2 \
-            or block_tables.shape[0] != q.shape[0] or seq_lens.shape != q.shape[:1]:
+    dev = k_codes.device
+    _need_all(dev, (k_codes, _F8, "k_codes"), (v_codes, _F8, "v_codes"), (k_exps, _U8, "k_exps"),
+              (v_exps, _U8, "v_exps"), (q, _BF16, "q"), (out, _BF16, "out"), (block_tables, _I32, "block_tables"),
+              (seq_lens, _I32, "seq_lens"))
+    NB, Hkv, bs, d = _quant_cache_shape(k_codes, v_codes, k_exps, v_exps)
+    qs, ts = q.shape, block_tables.shape
+    if len(qs) != 4 or qs[1] != 1 or qs[3] != d or out.shape != qs or len(ts) != 2 or ts[0] != qs[0] \
+            or seq_lens.shape != qs[:1]:
         raise ValueError("shape mismatch")
-    ws_bytes = 0
+    ws, ws_bytes = None, 0
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous on {dev}")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _need_cuda(dev)
-    with _on(dev):
-        _check(lib().paged_attention_decode_quant(
-            _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_exps), _ptr(v_exps), _ptr(block_tables),
-            block_tables.shape[1], _ptr(seq_lens), q.shape[0], int(max_seq_len), q.shape[2], Hkv, d, bs, NB,
-            float(scale), _ptr(out), _ptr(workspace), ws_bytes, _status(d_status, dev), _stream(stream, dev)),
-            "paged_attention_decode_quant")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch(lib().paged_attention_decode_quant, "paged_attention_decode_quant", dev, stream,
+            (q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(),
+             block_tables.data_ptr(), ts[1], seq_lens.data_ptr(), qs[0], int(max_seq_len), qs[2], Hkv, d, bs, NB,
+             float(scale), out.data_ptr(), ws, ws_bytes, _status(d_status, dev)))
 
 
 # ------------------------------------------------------------- allocator
