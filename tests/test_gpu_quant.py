@@ -105,7 +105,7 @@ def gpu_bf16(b):
 @pytest.mark.parametrize("T,Hkv,d,bs,strided", [
     (1, 1, 16, 1, False), (300, 8, 128, 16, False), (257, 2, 64, 32, True), (33, 3, 48, 7, True), (40, 5, 80, 24, False),
     (64, 1, 96, 128, True), (21, 2, 112, 16, False), (19, 4, 192, 8, True), (17, 3, 256, 64, False), (9, 2, 512, 16, True),
-    (1, 8, 128, 16, True), (5000, 1, 32, 16, False),
+    (1, 8, 128, 16, True), (5000, 1, 32, 16, False), (5003, 8, 128, 16, True), (4999, 9, 64, 64, False),
 ])
 def test_write_bit_exact(T, Hkv, d, bs, strided):
     rng = np.random.default_rng(T + 7 * d + bs)
@@ -130,6 +130,33 @@ def test_write_bit_exact(T, Hkv, d, bs, strided):
     for got, want, what in zip(cache, host, ("key codes", "value codes", "key exponents", "value exponents")):
         g = u8(got)
         assert np.array_equal(g, want), f"{what}: {int((g != want).sum())} of {want.size} differ"
+
+
+def test_rows_aligned_to_16_bytes_only():
+    """Buffers 16 bytes off a 32-byte boundary, for the write's input and the read-back's output."""
+    T, Hkv, d, bs = 300, 3, 64, 16
+    rng = np.random.default_rng(12)
+    host = random_cache(40, Hkv, bs, d, rng, fill=0)
+    cache = cache_on_gpu(*[a.copy() for a in host])
+    slots = inputs.distinct_slots(T, 40 * bs, rng)
+    kb, vb = awkward_rows(T, Hkv, d, rng), awkward_rows(T, Hkv, d, rng)
+
+    def off16(b=None):
+        t = torch.zeros(T * Hkv * d + 16, dtype=torch.bfloat16, device="cuda")
+        t = t[8:8 + T * Hkv * d] if t.data_ptr() % 32 == 0 else t[:T * Hkv * d]
+        t = t.view(T, Hkv, d)
+        assert t.data_ptr() % 32 == 16
+        return t if b is None else t.copy_(gpu_bf16(b))
+
+    native.pkv_write_quant(off16(kb), off16(vb), dev(slots, torch.int64), *cache)
+    OQ.write(kb, vb, slots, *host)
+    k, v = off16(), off16()
+    native.pkv_read_quant(*cache, dev(slots, torch.int64), k, v)
+    torch.cuda.synchronize()
+    assert all(np.array_equal(u8(g), w) for g, w in zip(cache, host))
+    for got, codes, exps in ((k, host[0], host[2]), (v, host[1], host[3])):
+        want = OQ.values(codes[slots // bs, :, slots % bs], exps[slots // bs, :, slots % bs])
+        assert np.array_equal(got.double().cpu().numpy(), want, equal_nan=True)
 
 
 def test_write_out_of_range_slots_are_reported_and_skipped():
