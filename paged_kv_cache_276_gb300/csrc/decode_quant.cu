@@ -68,8 +68,8 @@ template <int D, int NT>
 struct Shape {
   static constexpr int kTokens = kUnitBytes / D;  // tokens of a unit
   static constexpr int kStages = 2;
-  // tokens of one softmax step: the whole unit where registers allow (12 warps: 168 a thread)
-  static constexpr int kStep = NT == 1 ? kTokens : kTokens / 2;
+  // tokens of one softmax step: the whole unit where registers allow (168 a thread with more than 8 warps, 255 with 8)
+  static constexpr int kStep = NT == 1 || D == 128 ? kTokens : kTokens / 2;
   static constexpr int kTileFloats = NT * 8 * D;  // O of one piece, in accumulator order
   static constexpr int kPieceFloats = kTileFloats + 2 * NT * 8;  // ..., m[cols], l[cols]
   static constexpr int kRingBytes = kStages * 2 * kUnitBytes;

@@ -517,16 +517,26 @@ def paged_attention_decode_static_scratch(q, k_cache, v_cache, block_tables, seq
 
 # ------------------------------------------------------- the cache in 8 bits
 # These calls are short on the GPU (a few microseconds for a decode step's
-# write), so the checks are written to cost little: one pass over the tensors,
-# addresses passed as plain integers.
+# write), so their checks are written to cost little: one expression over the
+# tensors (about 0.15 us each), which only on failure is gone through one by one
+# for its message; addresses go to the library as plain integers.
 _BF16, _F8, _U8, _I32, _I64 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64
 
 
-def _need_all(dev, *triples):
-    """Each (tensor, dtype, name): a dense tensor of that type on ``dev``."""
-    for t, dtype, name in triples:
-        if t.__class__ is not torch.Tensor or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
-            _need(t, dtype, name, dev)  # says what is wrong (a Tensor's subclass may be fine)
+def _need_each(k_codes, v_codes, k_exps, v_exps, *others):
+    """The cache's tensors, and (tensor, dtype, name) of others on its device: raises for the first that is wrong."""
+    dev = k_codes.device if isinstance(k_codes, torch.Tensor) else None
+    for t, dtype, name in ((k_codes, _F8, "k_codes"), (v_codes, _F8, "v_codes"), (k_exps, _U8, "k_exps"),
+                           (v_exps, _U8, "v_exps")) + others:
+        _need(t, dtype, name, dev)
+
+
+def _quant_cache_ok(k_codes, v_codes, k_exps, v_exps):
+    i = k_codes.get_device()
+    return (k_codes.dtype is _F8 and v_codes.dtype is _F8 and k_exps.dtype is _U8 and v_exps.dtype is _U8
+            and v_codes.get_device() == i and k_exps.get_device() == i and v_exps.get_device() == i
+            and k_codes.is_contiguous() and v_codes.is_contiguous() and k_exps.is_contiguous()
+            and v_exps.is_contiguous())
 
 
 def _quant_cache_shape(k_codes, v_codes, k_exps, v_exps):
@@ -536,38 +546,37 @@ def _quant_cache_shape(k_codes, v_codes, k_exps, v_exps):
     return shape
 
 
-def _status(d_status, dev):
+def _status(d_status, index):
     if d_status is None:
         return None
-    _need_all(dev, (d_status, _I32, "d_status"))
-    if d_status.numel() < 1:
-        raise ValueError("d_status: one int32 expected")
+    if not isinstance(d_status, torch.Tensor) or d_status.dtype is not _I32 or d_status.get_device() != index:
+        raise TypeError("d_status must be a torch.int32 tensor on the cache's device")
     return d_status.data_ptr()
 
 
-def _launch(fn, name, dev, stream, args):
-    """Call ``fn(*args, stream)`` with ``dev`` current (its kernels are launched from there)."""
-    if dev.type != "cuda":
-        raise ValueError(f"the cache must be on a CUDA device, got {dev}")
+def _launch(fn, name, index, stream, args):
+    """Call ``fn(*args, stream)`` with CUDA device ``index`` current (the kernels are launched from there)."""
+    if index < 0:
+        raise ValueError("the cache must be on a CUDA device")
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+        stream = torch._C._cuda_getCurrentRawStream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev.index:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             rc = fn(*args, stream)
     if rc != PKV_OK:
         raise PkvError(rc, name)
 
 
-def _token_rows(t, name, shape, dev):
+def _token_rows(t, name, shape, index):
     """The stride in elements between tokens of [T, Hkv, d] rows whose own values are dense."""
     if not isinstance(t, torch.Tensor) or t.dtype != _BF16:
         raise TypeError(f"{name} must be a torch.bfloat16 tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the cache's device, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
     T, Hkv, d = shape
@@ -583,32 +592,44 @@ def pkv_write_quant(k, v, slot_mapping, k_codes, v_codes, k_exps, v_exps, d_stat
     """Quantise new tokens into an 8-bit cache.  k, v: [T, Hkv, d] bf16, each token's rows dense (views of a
     fused projection's output are fine); slot_mapping: [T] int64, negative: skip; codes [NB, Hkv, bs, d]
     float8_e4m3fn, exponents [NB, Hkv, bs] uint8 (device).  d: a multiple of 16."""
-    dev = k_codes.device
-    _need_all(dev, (k_codes, _F8, "k_codes"), (v_codes, _F8, "v_codes"), (k_exps, _U8, "k_exps"),
-              (v_exps, _U8, "v_exps"), (slot_mapping, _I64, "slot_mapping"))
+    try:
+        i = k_codes.get_device()
+        ok = (_quant_cache_ok(k_codes, v_codes, k_exps, v_exps) and slot_mapping.dtype is _I64
+              and slot_mapping.get_device() == i and slot_mapping.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        _need_each(k_codes, v_codes, k_exps, v_exps, (slot_mapping, _I64, "slot_mapping"))
     NB, Hkv, bs, d = _quant_cache_shape(k_codes, v_codes, k_exps, v_exps)
     if slot_mapping.dim() != 1:
         raise ValueError("slot_mapping: [T] expected")
     shape = (slot_mapping.shape[0], Hkv, d)
-    ks, vs = _token_rows(k, "k", shape, dev), _token_rows(v, "v", shape, dev)
-    _launch(lib().pkv_write_quant, "pkv_write_quant", dev, stream,
+    ks, vs = _token_rows(k, "k", shape, i), _token_rows(v, "v", shape, i)
+    _launch(lib().pkv_write_quant, "pkv_write_quant", i, stream,
             (k.data_ptr(), v.data_ptr(), ks, vs, slot_mapping.data_ptr(), shape[0], k_codes.data_ptr(),
-             v_codes.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(), NB, bs, Hkv, d, _status(d_status, dev)))
+             v_codes.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(), NB, bs, Hkv, d, _status(d_status, i)))
 
 
 def pkv_read_quant(k_codes, v_codes, k_exps, v_exps, slot_mapping, k, v, d_status=None, stream=None):
     """Rows of listed slots of an 8-bit cache, exactly, into k, v [T, Hkv, d] bf16 (rows of negative slots stay
     as they are); the cache as in ``pkv_write_quant``."""
-    dev = k_codes.device
-    _need_all(dev, (k_codes, _F8, "k_codes"), (v_codes, _F8, "v_codes"), (k_exps, _U8, "k_exps"),
-              (v_exps, _U8, "v_exps"), (slot_mapping, _I64, "slot_mapping"), (k, _BF16, "k"), (v, _BF16, "v"))
+    try:
+        i = k_codes.get_device()
+        ok = (_quant_cache_ok(k_codes, v_codes, k_exps, v_exps) and slot_mapping.dtype is _I64 and k.dtype is _BF16
+              and v.dtype is _BF16 and slot_mapping.get_device() == i and k.get_device() == i and v.get_device() == i
+              and slot_mapping.is_contiguous() and k.is_contiguous() and v.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        _need_each(k_codes, v_codes, k_exps, v_exps, (slot_mapping, _I64, "slot_mapping"), (k, _BF16, "k"),
+                   (v, _BF16, "v"))
     NB, Hkv, bs, d = _quant_cache_shape(k_codes, v_codes, k_exps, v_exps)
     T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
     if k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
         raise ValueError("shape mismatch between k/v, slot_mapping [T] and the cache")
-    _launch(lib().pkv_read_quant, "pkv_read_quant", dev, stream,
+    _launch(lib().pkv_read_quant, "pkv_read_quant", i, stream,
             (k_codes.data_ptr(), v_codes.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(), slot_mapping.data_ptr(), T,
-             k.data_ptr(), v.data_ptr(), NB, bs, Hkv, d, _status(d_status, dev)))
+             k.data_ptr(), v.data_ptr(), NB, bs, Hkv, d, _status(d_status, i)))
 
 
 def paged_attention_decode_quant_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len):
@@ -621,10 +642,18 @@ def paged_attention_decode_quant(q, k_codes, v_codes, k_exps, v_exps, block_tabl
     """Single-token decode over an 8-bit cache: q, out [B, 1, Hq, d] bf16; the cache as in ``pkv_write_quant``;
     tables [B, max_blocks] int32; lens [B] int32; workspace: a device buffer of
     ``paged_attention_decode_quant_workspace_size`` bytes (one per call that may overlap)."""
-    dev = k_codes.device
-    _need_all(dev, (k_codes, _F8, "k_codes"), (v_codes, _F8, "v_codes"), (k_exps, _U8, "k_exps"),
-              (v_exps, _U8, "v_exps"), (q, _BF16, "q"), (out, _BF16, "out"), (block_tables, _I32, "block_tables"),
-              (seq_lens, _I32, "seq_lens"))
+    try:
+        i = k_codes.get_device()
+        ok = (_quant_cache_ok(k_codes, v_codes, k_exps, v_exps) and q.dtype is _BF16 and out.dtype is _BF16
+              and block_tables.dtype is _I32 and seq_lens.dtype is _I32 and q.get_device() == i
+              and out.get_device() == i and block_tables.get_device() == i and seq_lens.get_device() == i
+              and q.is_contiguous() and out.is_contiguous() and block_tables.is_contiguous()
+              and seq_lens.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        _need_each(k_codes, v_codes, k_exps, v_exps, (q, _BF16, "q"), (out, _BF16, "out"),
+                   (block_tables, _I32, "block_tables"), (seq_lens, _I32, "seq_lens"))
     NB, Hkv, bs, d = _quant_cache_shape(k_codes, v_codes, k_exps, v_exps)
     qs, ts = q.shape, block_tables.shape
     if len(qs) != 4 or qs[1] != 1 or qs[3] != d or out.shape != qs or len(ts) != 2 or ts[0] != qs[0] \
@@ -632,13 +661,13 @@ def paged_attention_decode_quant(q, k_codes, v_codes, k_exps, v_exps, block_tabl
         raise ValueError("shape mismatch")
     ws, ws_bytes = None, 0
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {dev}")
+        if workspace.get_device() != i or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the cache's device")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch(lib().paged_attention_decode_quant, "paged_attention_decode_quant", dev, stream,
+    _launch(lib().paged_attention_decode_quant, "paged_attention_decode_quant", i, stream,
             (q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(),
              block_tables.data_ptr(), ts[1], seq_lens.data_ptr(), qs[0], int(max_seq_len), qs[2], Hkv, d, bs, NB,
-             float(scale), out.data_ptr(), ws, ws_bytes, _status(d_status, dev)))
+             float(scale), out.data_ptr(), ws, ws_bytes, _status(d_status, i)))
 
 
 # ------------------------------------------------------------- allocator

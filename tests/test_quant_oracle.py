@@ -185,3 +185,22 @@ def test_python_checks_shapes_types_and_devices(native):
         native.paged_attention_decode_quant(q, *cache, tbl.long(), lens, 8, 0.1, q.clone())
 
 
+
+
+def test_python_says_what_is_not_a_tensor(native):
+    slots, kv = torch.zeros(3, dtype=torch.int64), torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    cache = cpu_cache()
+    with pytest.raises(TypeError, match="v_codes must be a torch.Tensor"):
+        native.pkv_write_quant(kv, kv, slots, cache[0], None, *cache[2:])
+    with pytest.raises(TypeError, match="slot_mapping must be a torch.Tensor"):
+        native.pkv_write_quant(kv, kv, [0, 1, 2], *cache)
+    with pytest.raises(TypeError, match="k must be"):
+        native.pkv_write_quant(None, kv, slots, *cache)
+    with pytest.raises(TypeError, match="v must be a torch.Tensor"):
+        native.pkv_read_quant(*cache, slots, kv, 3)
+    q = torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16)
+    tbl, lens = torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError, match="seq_lens must be a torch.Tensor"):
+        native.paged_attention_decode_quant(q, *cache, tbl, None, 8, 0.1, q.clone())
+    with pytest.raises(TypeError, match="d_status"):
+        native.paged_attention_decode_quant(q, *cache, tbl, lens, 8, 0.1, q.clone(), None, torch.zeros(1))
