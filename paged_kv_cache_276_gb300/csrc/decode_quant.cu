@@ -34,9 +34,9 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <utility>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "pkv.h"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -894,31 +894,13 @@ int check_decode(const void *q, const void *k_codes, const void *v_codes, const 
   return PKV_OK;
 }
 
-// Launch with programmatic stream serialisation: the grid may start while the
-// previous kernel in the stream drains; it waits before it reads anything.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), int grid, int block, size_t smem, cudaStream_t stream,
-                       Args &&...args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
 template <int D, int BS, int NT>
 cudaError_t launch(const CUtensorMap &tmk, const CUtensorMap &tmv, const Params &p, int grid, cudaStream_t stream) {
   using Sh = Shape<D, NT>;
   auto k = decode_quant_kernel<D, BS, NT>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmemBytes);
-  if (e == cudaSuccess) e = launch_pdl(k, grid, Sh::kThreads, Sh::kSmemBytes, stream, tmk, tmv, p);
-  if (e == cudaSuccess && grid > 1) e = launch_pdl(join_kernel<D, NT>, grid, JoinShape<D, NT>::kThreads, 0, stream, p);
+  if (e == cudaSuccess) e = launch_overlapped(k, grid, Sh::kThreads, Sh::kSmemBytes, stream, tmk, tmv, p);
+  if (e == cudaSuccess && grid > 1) e = launch_overlapped(join_kernel<D, NT>, grid, JoinShape<D, NT>::kThreads, 0, stream, p);
   return e;
 }
 

@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "pkv.h"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const uint4 *__restrict
   // the grid queued behind this one may become resident now (it waits for this
   // grid's writes before it reads the cache)
   grid_launch_dependents();
+  grid_dependency_wait();  // the rows may come from the kernel launched just before
   constexpr int GROUPS = kThreads / W;
   const int c = threadIdx.x % W;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (GROUPS * ROWS) + threadIdx.x / W;
@@ -215,6 +217,7 @@ template <int W, bool WIDE>
 __global__ void __launch_bounds__(kThreads) read_kernel(uint4 *__restrict__ k, uint4 *__restrict__ v,
                                                         const RowParams p, const CachePtrs in) {
   grid_launch_dependents();
+  grid_dependency_wait();
   const int c = threadIdx.x % W;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W;
   int64_t t, src;
@@ -254,28 +257,32 @@ RowParams row_params(const int64_t *slots, int num_tokens, int num_blocks, int b
   return p;
 }
 
-// CTAs for so many row pairs, `each` of them per group of lanes; 0: more than a
-// grid's x dimension holds.
-unsigned row_grid(int64_t rows, int lanes, int each) {
-  const int64_t per = static_cast<int64_t>(kThreads / lanes) * each, n = (rows + per - 1) / per;
-  return n <= 0x7fffffffll ? static_cast<unsigned>(n) : 0u;
+// CTAs for so many row pairs, `each` of them per group of lanes.
+int64_t row_grid(int64_t rows, int lanes, int each) {
+  const int64_t per = static_cast<int64_t>(kThreads / lanes) * each;
+  return (rows + per - 1) / per;
+}
+
+template <typename K, typename... Args>
+int launch_grid(K kernel, int64_t grid, void *stream, const Args &...args) {
+  if (grid > 0x7fffffffll) return PKV_ERR_UNSUPPORTED;  // more CTAs than a grid's x dimension holds
+  const cudaError_t e = launch_overlapped(kernel, static_cast<unsigned>(grid), kThreads, 0, as_stream(stream), args...);
+  return e == cudaSuccess ? PKV_OK : (set_cuda_error(e), PKV_ERR_CUDA);
 }
 
 bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
-// lanes per row: the power of two that covers head_dim / 16
+// f with the lanes per row (the power of two that covers head_dim / 16) and
+// whether rows are aligned to 32 bytes, as types.
 template <typename F>
-void by_lanes(int chunks, bool wide, F &&f) {
-  auto go = [&](auto w) {
-    if (wide) f(w, std::true_type());
-    else f(w, std::false_type());
-  };
-  if (chunks <= 1) go(std::integral_constant<int, 1>());
-  else if (chunks <= 2) go(std::integral_constant<int, 2>());
-  else if (chunks <= 4) go(std::integral_constant<int, 4>());
-  else if (chunks <= 8) go(std::integral_constant<int, 8>());
-  else if (chunks <= 16) go(std::integral_constant<int, 16>());
-  else go(std::integral_constant<int, 32>());
+int launch_rows(int chunks, bool wide, F &&f) {
+  auto go = [&](auto w) { return wide ? f(w, std::true_type()) : f(w, std::false_type()); };
+  if (chunks <= 1) return go(std::integral_constant<int, 1>());
+  if (chunks <= 2) return go(std::integral_constant<int, 2>());
+  if (chunks <= 4) return go(std::integral_constant<int, 4>());
+  if (chunks <= 8) return go(std::integral_constant<int, 8>());
+  if (chunks <= 16) return go(std::integral_constant<int, 16>());
+  return go(std::integral_constant<int, 32>());
 }
 
 }  // namespace
@@ -298,25 +305,20 @@ int pkv_write_quant(const pkv_bf16 *k, const pkv_bf16 *v, int64_t k_stride, int6
   p.v_stride = v_stride;
   const pkv::CachePtrs out{reinterpret_cast<uint4 *>(k_codes), reinterpret_cast<uint4 *>(v_codes), k_exps, v_exps};
   const bool wide = pkv::aligned32(k) && pkv::aligned32(v) && k_stride % 16 == 0 && v_stride % 16 == 0;
-  bool fits = true;
-  pkv::by_lanes(p.chunks, wide, [&](auto w, auto wd) {
+  return pkv::launch_rows(p.chunks, wide, [&](auto w, auto wd) {
     constexpr int W = decltype(w)::value;
     constexpr bool WIDE = decltype(wd)::value;
-    auto launch = [&](auto kernel, unsigned grid) {
-      if (grid == 0) fits = false;
-      else
-        kernel<<<grid, pkv::kThreads, 0, pkv::as_stream(stream)>>>(reinterpret_cast<const uint4 *>(k),
-                                                                   reinterpret_cast<const uint4 *>(v), p, out);
+    auto launch = [&](auto kernel, int64_t grid) {
+      return pkv::launch_grid(kernel, grid, stream, reinterpret_cast<const uint4 *>(k),
+                              reinterpret_cast<const uint4 *>(v), p, out);
     };
     // two row pairs per thread once that still gives every SM four CTAs.
     // Measured, one / two: 2048 rows 2.2 / 2.9 us, 65536 rows 11.8 / 10.9,
     // 262144 rows 38.9 / 34.8
-    const unsigned two = pkv::row_grid(p.rows, W, 2);
-    if (two >= 4u * static_cast<unsigned>(pkv::num_sms())) launch(pkv::write_kernel<W, WIDE, 2>, two);
-    else launch(pkv::write_kernel<W, WIDE, 1>, pkv::row_grid(p.rows, W, 1));
+    const int64_t two = pkv::row_grid(p.rows, W, 2);
+    if (two >= 4 * pkv::num_sms()) return launch(pkv::write_kernel<W, WIDE, 2>, two);
+    return launch(pkv::write_kernel<W, WIDE, 1>, pkv::row_grid(p.rows, W, 1));
   });
-  if (!fits) return PKV_ERR_UNSUPPORTED;
-  return pkv::check_launch();
 }
 
 int pkv_read_quant(const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t *k_exps, const uint8_t *v_exps,
@@ -330,17 +332,11 @@ int pkv_read_quant(const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t
   const pkv::CachePtrs in{reinterpret_cast<uint4 *>(const_cast<uint8_t *>(k_codes)),
                           reinterpret_cast<uint4 *>(const_cast<uint8_t *>(v_codes)), const_cast<uint8_t *>(k_exps),
                           const_cast<uint8_t *>(v_exps)};
-  bool fits = true;
-  pkv::by_lanes(p.chunks, pkv::aligned32(k) && pkv::aligned32(v), [&](auto w, auto wd) {
+  return pkv::launch_rows(p.chunks, pkv::aligned32(k) && pkv::aligned32(v), [&](auto w, auto wd) {
     constexpr int W = decltype(w)::value;
-    const unsigned grid = pkv::row_grid(p.rows, W, 1);
-    if (grid == 0) fits = false;
-    else
-      pkv::read_kernel<W, decltype(wd)::value><<<grid, pkv::kThreads, 0, pkv::as_stream(stream)>>>(
-          reinterpret_cast<uint4 *>(k), reinterpret_cast<uint4 *>(v), p, in);
+    return pkv::launch_grid(pkv::read_kernel<W, decltype(wd)::value>, pkv::row_grid(p.rows, W, 1), stream,
+                            reinterpret_cast<uint4 *>(k), reinterpret_cast<uint4 *>(v), p, in);
   });
-  if (!fits) return PKV_ERR_UNSUPPORTED;
-  return pkv::check_launch();
 }
 
 }  // extern "C"
