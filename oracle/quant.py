@@ -58,10 +58,8 @@ def encode(y):
 def row_exponents(x):
     """[..., d] float64 rows -> the smallest e with max |finite x| <= 448 * 2^e, clamped (int)."""
     a = np.where(np.isfinite(x), np.abs(x), 0.0).max(-1)
-    e = np.full(a.shape, E_MIN, dtype=np.int64)
-    for k in range(E_MIN, E_MAX):  # count up while 448 * 2^k is still too small
-        e = np.where(a > TOP * 2.0 ** k, k + 1, e)
-    return e
+    too_small = TOP * 2.0 ** np.arange(E_MIN, E_MAX, dtype=np.float64)  # 448 * 2^k: e is above k where it is below a
+    return E_MIN + np.searchsorted(too_small, a, side="left")
 
 
 def quantise(bits):
@@ -103,17 +101,20 @@ def decode(q_bits, k_codes, v_codes, k_exps, v_exps, tables, lens, scale):
         L = int(lens[i])
         if L == 0:
             continue
-        ids = [int(tables[i][j]) for j in range(-(-L // bs))]
-        for h in range(Hkv):
-            k = np.concatenate([values(k_codes[b, h], k_exps[b, h]) for b in ids])[:L]
-            v = np.concatenate([values(v_codes[b, h], v_exps[b, h]) for b in ids])[:L]
-            ve = np.concatenate([np.clip(v_exps[b, h].astype(np.int64), 96, 158) - 127 for b in ids])[:L]
-            for g in range(h * G, h * G + G):
-                s = (k @ q[i, g]) * scale
-                w = np.exp(s - s.max())
-                w = w / w.sum()
-                out[i, g] = w @ v
-                mag[i, g] = w @ np.abs(v)
-                dot[i, g] = (np.abs(k) @ np.abs(q[i, g])).max() * abs(scale)
-                top[i, g] = (w * 2.0 ** ve.astype(np.float64)).max()
+        ids = np.array([int(tables[i][j]) for j in range(-(-L // bs))])
+
+        def rows(x):  # the sequence's blocks in order, one KV head after the other: [Hkv, L, ...]
+            x = x[ids].swapaxes(0, 1)
+            return x.reshape((Hkv, len(ids) * bs) + x.shape[3:])[:, :L]
+
+        k, v = values(rows(k_codes), rows(k_exps)), values(rows(v_codes), rows(v_exps))
+        ve = np.clip(rows(v_exps).astype(np.int64), E_MIN + BIAS, E_MAX + BIAS) - BIAS
+        qi = q[i].reshape(Hkv, G, d)  # query head g reads KV head g // G
+        s = (qi @ k.swapaxes(1, 2)) * scale
+        w = np.exp(s - s.max(-1, keepdims=True))
+        w = w / w.sum(-1, keepdims=True)
+        out[i] = (w @ v).reshape(Hq, d)
+        mag[i] = (w @ np.abs(v)).reshape(Hq, d)
+        dot[i] = (np.abs(qi) @ np.abs(k).swapaxes(1, 2)).max(-1).reshape(Hq) * abs(scale)
+        top[i] = (w * 2.0 ** ve.astype(np.float64)[:, None, :]).max(-1).reshape(Hq)
     return out, mag, dot, top

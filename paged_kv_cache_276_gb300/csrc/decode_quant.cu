@@ -57,7 +57,7 @@ struct Params {
   const uint8_t *k_exps, *v_exps;
   const int32_t *block_tables, *seq_lens;
   __nv_bfloat16 *out;
-  float *ws;      // [grid][2] pieces of runs that span CTAs, then [grid] descriptors
+  float *ws;      // [grid][2] pieces of runs that span CTAs, then [grid] descriptors; NULL: no run does
   int4 *ws_desc;  // {sequence | KV head << 16, -, last CTA of the run, 1} of the run that leaves CTA c, or .w = 0
   int32_t *status;
   int num_seqs, max_blocks, max_len, num_q_heads, num_kv_heads, group, num_blocks;
@@ -509,25 +509,30 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   any_empty = __syncthreads_or(any_empty);
   const uint32_t U = total * p.num_kv_heads;  // below 2^31 (checked on the host)
   // as many CTAs as give every warp a unit; the others have none.  CTA c's
-  // range, then the warp's part of it: equal to within a unit.
+  // range, then the warp's part of it: equal to within a unit.  Where no run has
+  // more units than a CTA has warps (no workspace), a CTA's range is moved to
+  // the runs' borders: no run spans CTAs.
   const uint32_t nc = max(1u, min(gridDim.x, (U + NW - 1) / NW));
   const uint32_t cq = U / nc, crem = U - cq * nc;
+  const bool whole = p.ws == nullptr && nc > 1;
   uint32_t u0 = 0, u1 = 0;
+  Cursor c{};
   if (blockIdx.x < nc) {
-    const uint32_t cs = blockIdx.x * cq + min(blockIdx.x, crem), size = cq + (blockIdx.x < crem ? 1 : 0);
-    const uint32_t wq = size / NW, wrem = size - wq * NW, w = warp;
-    u0 = cs + w * wq + min(w, wrem);
-    u1 = u0 + wq + (w < wrem ? 1 : 0);
-  }
-
-  bool ok = true;
-  if (u0 < u1) {
-    // ---- the run that unit u0 belongs to: the last chunk that starts at or before it
-    Cursor c;
-    {
+    uint32_t cs = blockIdx.x * cq + min(blockIdx.x, crem), ce = cs + cq + (blockIdx.x < crem ? 1 : 0);
+#pragma unroll 1
+    for (int step = whole ? 0 : 2; step < 3; ++step) {  // the run at cs, at ce, at this warp's start
+      if (step == 2) {
+        const uint32_t size = ce - cs, wq = size / NW, wrem = size - wq * NW, w = warp;
+        u0 = cs + w * wq + min(w, wrem);
+        u1 = u0 + wq + (w < wrem ? 1 : 0);
+        if (u0 == u1) break;
+      }
+      const uint32_t u = step == 0 ? cs : step == 1 ? ce : u0;
+      if (u >= U) continue;  // ce of the last CTA
+      // the last chunk that starts at or before u
       int at = 0;
 #pragma unroll
-      for (int k = 0; k < NW; ++k) at += chunk_start[k * 32 + lane] <= u0 ? 1 : 0;
+      for (int k = 0; k < NW; ++k) at += chunk_start[k * 32 + lane] <= u ? 1 : 0;
       at = __reduce_add_sync(0xffffffffu, at) - 1;
       uint32_t base = chunk_start[at];
       c.seq = at;
@@ -541,7 +546,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             const uint32_t t = __shfl_up_sync(0xffffffffu, pre, off);
             if (lane >= off) pre += t;
           }
-          const unsigned in = __ballot_sync(0xffffffffu, u0 < base + pre);
+          const unsigned in = __ballot_sync(0xffffffffu, u < base + pre);
           if (in || seq + 32 >= p.num_seqs) {
             const int src = in ? __ffs(in) - 1 : 31;
             c.seq = min(seq + src, p.num_seqs - 1);
@@ -553,12 +558,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         }
       }
       c.n = max(1, static_cast<int>(units(c.len)));
-      c.h = static_cast<int>((u0 - base) / static_cast<uint32_t>(c.n));
-      c.j = static_cast<int>(u0 - base) - c.h * c.n;
-      c.wbase = -32;
-      c.window = -1;
-      c.from0 = c.j == 0;
+      c.h = static_cast<int>((u - base) / static_cast<uint32_t>(c.n));
+      c.j = static_cast<int>(u - base) - c.h * c.n;
+      const uint32_t border = c.j == 0 ? u : u + (c.n - c.j);  // the first run that starts at or behind u
+      if (step == 0) cs = border;
+      if (step == 1) ce = border;
     }
+  }
+
+  bool ok = true;
+  if (u0 < u1) {
+    c.wbase = -32;
+    c.window = -1;
+    c.from0 = c.j == 0;
 
     const uint64_t pol = l2_policy_evict_first();
     uint32_t next = u0;  // next unit to issue
@@ -843,11 +855,13 @@ __global__ void __launch_bounds__(JoinShape<D, NT>::kThreads) join_kernel(const 
 struct Plan {
   int grid = 1;
   size_t piece_bytes = 0;
-  size_t ws_bytes() const { return grid > 1 ? grid * (2 * piece_bytes + sizeof(int4)) : 0; }
+  bool whole = false;  // runs are not split between CTAs
+  size_t ws_bytes() const { return grid > 1 && !whole ? grid * (2 * piece_bytes + sizeof(int4)) : 0; }
 };
 
 // The grid: one CTA per SM, fewer when the longest possible batch has fewer
-// than a unit per warp.  One CTA needs no workspace and no second kernel.
+// than a unit per warp.  One CTA needs no workspace and no second kernel, and so
+// do short sequences.
 Plan make_plan(int num_seqs, int num_kv_heads, int group, int head_dim, int max_seq_len) {
   const int nt = group > 8 ? 2 : 1, tokens = kUnitBytes / head_dim;
   const int warps = head_dim == 128 ? (nt == 1 ? Shape<128, 1>::kWarps : Shape<128, 2>::kWarps)
@@ -855,6 +869,9 @@ Plan make_plan(int num_seqs, int num_kv_heads, int group, int head_dim, int max_
   const double units = static_cast<double>(num_seqs) * num_kv_heads * ((max_seq_len + (tokens - 1ll)) / tokens);
   Plan plan;
   plan.grid = static_cast<int>(std::max(1.0, std::min<double>(num_sms(), std::ceil(units / warps))));
+  // A run of at most a unit per warp is not worth splitting between CTAs: the
+  // second kernel costs more (about 3 us) than the runs' uneven ends.
+  plan.whole = (max_seq_len + (tokens - 1ll)) / tokens <= warps;
   plan.piece_bytes = (static_cast<size_t>(nt) * 8 * head_dim + 2 * nt * 8) * sizeof(float);
   return plan;
 }
@@ -900,7 +917,7 @@ cudaError_t launch(const CUtensorMap &tmk, const CUtensorMap &tmv, const Params 
   auto k = decode_quant_kernel<D, BS, NT>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmemBytes);
   if (e == cudaSuccess) e = launch_overlapped(k, grid, Sh::kThreads, Sh::kSmemBytes, stream, tmk, tmv, p);
-  if (e == cudaSuccess && grid > 1) e = launch_overlapped(join_kernel<D, NT>, grid, JoinShape<D, NT>::kThreads, 0, stream, p);
+  if (e == cudaSuccess && p.ws) e = launch_overlapped(join_kernel<D, NT>, grid, JoinShape<D, NT>::kThreads, 0, stream, p);
   return e;
 }
 
@@ -958,7 +975,7 @@ int paged_attention_decode_quant(const pkv_bf16 *q, const uint8_t *k_codes, cons
   p.block_tables = block_tables;
   p.seq_lens = seq_lens;
   p.out = reinterpret_cast<__nv_bfloat16 *>(out);
-  if (plan.grid > 1) {
+  if (plan.ws_bytes() > 0) {
     p.ws = static_cast<float *>(workspace);
     p.ws_desc = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + plan.grid * 2 * plan.piece_bytes);
   }

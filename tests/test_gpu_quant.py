@@ -290,6 +290,18 @@ def test_decode_many_sequences():
     check_decode(run_decode(q, cache_on_gpu(*host), tables, lens, 0.125), q, host, tables, lens, 0.125)
 
 
+@pytest.mark.parametrize("d,Hq,Hkv,top", [(128, 6, 3, 384), (128, 6, 3, 385), (64, 4, 2, 768), (64, 4, 2, 769), (128, 24, 2, 256),
+                                          (128, 24, 2, 257), (64, 12, 1, 640), (64, 12, 1, 641), (128, 5, 5, 33)])
+def test_decode_short_sequences(d, Hq, Hkv, top):
+    """Batches around the length up to which no sequence is split between CTAs."""
+    rng = np.random.default_rng(top)
+    for B in (40, 400):
+        lens = rng.integers(0, top + 1, B)
+        lens[rng.integers(0, B, 3)] = top
+        q, host, tables = decode_case(lens.tolist(), d, 16, Hq, Hkv, seed=top + B)
+        check_decode(run_decode(q, cache_on_gpu(*host), tables, lens, d ** -0.5), q, host, tables, lens, d ** -0.5)
+
+
 def test_decode_all_empty():
     q, host, tables = decode_case([0, 0, 0], 128, 16, 8, 2, seed=2)
     for max_len in (0, 100, 100000):

@@ -204,3 +204,21 @@ def test_python_says_what_is_not_a_tensor(native):
         native.paged_attention_decode_quant(q, *cache, tbl, None, 8, 0.1, q.clone())
     with pytest.raises(TypeError, match="d_status"):
         native.paged_attention_decode_quant(q, *cache, tbl, lens, 8, 0.1, q.clone(), None, torch.zeros(1))
+
+
+def test_decode_oracle_against_a_plain_loop():
+    rng = np.random.default_rng(0)
+    B, Hkv, G, d, bs, NB, scale = 3, 2, 3, 16, 4, 9, 0.1
+    kc, vc = (rng.integers(0, 127, (NB, Hkv, bs, d)).astype(np.uint8) for _ in range(2))
+    ke, ve = (rng.integers(110, 120, (NB, Hkv, bs)).astype(np.uint8) for _ in range(2))
+    q = np.round(rng.standard_normal((B, Hkv * G, d)) * 8) / 8
+    lens, tables = [5, 0, 11], np.array([rng.permutation(NB)[:3] for _ in range(B)])
+    out = OQ.decode(OQ.bf16_bits(q), kc, vc, ke, ve, tables, lens, scale)[0]
+    for i in range(B):
+        for g in range(Hkv * G):
+            h, num, den = g // G, np.zeros(d), 0.0
+            for t in range(lens[i]):
+                b, o = tables[i][t // bs], t % bs
+                w = np.exp(scale * 2.0 ** (int(ke[b, h, o]) - 127) * (q[i, g] @ OQ.TABLE[kc[b, h, o]]))
+                num, den = num + w * OQ.TABLE[vc[b, h, o]] * 2.0 ** (int(ve[b, h, o]) - 127), den + w
+            assert np.allclose(out[i, g], num / den if den else 0.0, rtol=1e-12)
