@@ -8,9 +8,9 @@
 // per lane, so the row's maximum is a few shuffles and a row is read once.  No
 // loop: a CTA per few rows lets the hardware balance a ragged end (with a grid
 // of 8 CTAs per SM that walks the rows, read-back took 41.8 us instead of 32.2).
-// Measured at 32768 tokens x 8 KV heads x 128: write 34.8 us (5.8 TB/s),
-// read-back 32.2 us (6.3 TB/s), of 6.78 TB/s for a plain copy; a decode step's
-// 256 tokens 2.2 us.
+// Measured at 32768 tokens x 8 KV heads x 128: write 31.0 us (6.5 TB/s),
+// read-back 31.6 us (6.4 TB/s), of 6.78 TB/s for a plain copy; the 256 tokens of
+// a decode step 2.1 us, a launch's latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -153,47 +153,39 @@ __device__ __forceinline__ void store16(uint4 *dst, const uint4 &a, const uint4 
   }
 }
 
-// W lanes per (token, KV head) row pair: lane c of the group holds values
-// 16 c .. 16 c + 15 of the key row and of the value row.  A thread has ROWS row
-// pairs in flight.
-template <int W, bool WIDE, int ROWS>
-__global__ void __launch_bounds__(kThreads) write_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
-                                                         const RowParams p, const CachePtrs out) {
+// W lanes per (token, KV head) row pair: lane c of the group holds values 16 c ..
+// 16 c + 15 of the key row and of the value row.  Eight CTAs an SM (32 registers
+// a thread) keep most loads in flight.  At 262144 row pairs of 128 values:
+// 31.2 us; with 40 registers 36.9; two row pairs per thread (63) 34.5; keys and
+// values by different threads 37.7.
+template <int W, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 8) write_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
+                                                            const RowParams p, const CachePtrs out) {
   // the grid queued behind this one may become resident now (it waits for this
   // grid's writes before it reads the cache)
   grid_launch_dependents();
   grid_dependency_wait();  // the rows may come from the kernel launched just before
-  constexpr int GROUPS = kThreads / W;
   const int c = threadIdx.x % W;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (GROUPS * ROWS) + threadIdx.x / W;
-  bool live[ROWS];
-  int64_t dst[ROWS];
-  uint4 x[ROWS][4];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int64_t row = row0 + i * GROUPS;
-    int64_t t = 0;
-    int h = 0;
-    live[i] = row < p.rows && locate(p, row, c == 0, &t, &h, &dst[i]) && c < p.chunks;
-    x[i][0] = x[i][1] = x[i][2] = x[i][3] = make_uint4(0u, 0u, 0u, 0u);
-    if (live[i]) {
-      const int64_t at = (static_cast<int64_t>(h) * p.chunks + c) * 2;
-      load16<WIDE>(k + (t * p.k_stride) / 8 + at, x[i][0], x[i][1]);
-      load16<WIDE>(v + (t * p.v_stride) / 8 + at, x[i][2], x[i][3]);
-    }
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W;
+  int64_t t = 0, dst = 0;
+  int h = 0;
+  const bool live = row < p.rows && locate(p, row, c == 0, &t, &h, &dst) && c < p.chunks;
+  uint4 ka = make_uint4(0u, 0u, 0u, 0u), kb = ka, va = ka, vb = ka;
+  if (live) {
+    const int64_t at = (static_cast<int64_t>(h) * p.chunks + c) * 2;
+    load16<WIDE>(k + (t * p.k_stride) / 8 + at, ka, kb);
+    load16<WIDE>(v + (t * p.v_stride) / 8 + at, va, vb);
   }
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    uint8_t ke, ve;
-    const uint4 kc = quantise<W>(x[i][0], x[i][1], &ke), vc = quantise<W>(x[i][2], x[i][3], &ve);
-    if (live[i]) {
-      out.k_codes[dst[i] * p.chunks + c] = kc;
-      out.v_codes[dst[i] * p.chunks + c] = vc;
-      if (c == 0) {
-        out.k_exps[dst[i]] = ke;
-        out.v_exps[dst[i]] = ve;
-      }
-    }
+  uint8_t e;
+  uint4 codes = quantise<W>(ka, kb, &e);
+  if (live) {
+    out.k_codes[dst * p.chunks + c] = codes;
+    if (c == 0) out.k_exps[dst] = e;
+  }
+  codes = quantise<W>(va, vb, &e);
+  if (live) {
+    out.v_codes[dst * p.chunks + c] = codes;
+    if (c == 0) out.v_exps[dst] = e;
   }
 }
 
@@ -257,16 +249,17 @@ RowParams row_params(const int64_t *slots, int num_tokens, int num_blocks, int b
   return p;
 }
 
-// CTAs for so many row pairs, `each` of them per group of lanes.
-int64_t row_grid(int64_t rows, int lanes, int each) {
-  const int64_t per = static_cast<int64_t>(kThreads / lanes) * each;
+// CTAs for so many rows of `lanes` lanes.
+int64_t row_grid(int64_t rows, int lanes) {
+  const int64_t per = kThreads / lanes;
   return (rows + per - 1) / per;
 }
 
 template <typename K, typename... Args>
 int launch_grid(K kernel, int64_t grid, void *stream, const Args &...args) {
   if (grid > 0x7fffffffll) return PKV_ERR_UNSUPPORTED;  // more CTAs than a grid's x dimension holds
-  const cudaError_t e = launch_overlapped(kernel, static_cast<unsigned>(grid), kThreads, 0, as_stream(stream), args...);
+  const cudaError_t e =
+      launch_overlapped(kernel, static_cast<unsigned>(grid), kThreads, 0, as_stream(stream), args...);
   return e == cudaSuccess ? PKV_OK : (set_cuda_error(e), PKV_ERR_CUDA);
 }
 
@@ -308,16 +301,8 @@ int pkv_write_quant(const pkv_bf16 *k, const pkv_bf16 *v, int64_t k_stride, int6
   return pkv::launch_rows(p.chunks, wide, [&](auto w, auto wd) {
     constexpr int W = decltype(w)::value;
     constexpr bool WIDE = decltype(wd)::value;
-    auto launch = [&](auto kernel, int64_t grid) {
-      return pkv::launch_grid(kernel, grid, stream, reinterpret_cast<const uint4 *>(k),
-                              reinterpret_cast<const uint4 *>(v), p, out);
-    };
-    // two row pairs per thread once that still gives every SM four CTAs.
-    // Measured, one / two: 2048 rows 2.2 / 2.9 us, 65536 rows 11.8 / 10.9,
-    // 262144 rows 38.9 / 34.8
-    const int64_t two = pkv::row_grid(p.rows, W, 2);
-    if (two >= 4 * pkv::num_sms()) return launch(pkv::write_kernel<W, WIDE, 2>, two);
-    return launch(pkv::write_kernel<W, WIDE, 1>, pkv::row_grid(p.rows, W, 1));
+    return pkv::launch_grid(pkv::write_kernel<W, WIDE>, pkv::row_grid(p.rows, W), stream,
+                            reinterpret_cast<const uint4 *>(k), reinterpret_cast<const uint4 *>(v), p, out);
   });
 }
 
@@ -334,7 +319,7 @@ int pkv_read_quant(const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t
                           const_cast<uint8_t *>(v_exps)};
   return pkv::launch_rows(p.chunks, pkv::aligned32(k) && pkv::aligned32(v), [&](auto w, auto wd) {
     constexpr int W = decltype(w)::value;
-    return pkv::launch_grid(pkv::read_kernel<W, decltype(wd)::value>, pkv::row_grid(p.rows, W, 1), stream,
+    return pkv::launch_grid(pkv::read_kernel<W, decltype(wd)::value>, pkv::row_grid(p.rows, W), stream,
                             reinterpret_cast<uint4 *>(k), reinterpret_cast<uint4 *>(v), p, in);
   });
 }

@@ -629,3 +629,23 @@ def test_one_workspace_serves_any_sizes_whatever_it_held():
             q, host, tables = decode_case(lens, d, bs, Hq, Hkv, seed=60 + i)
             out = run_decode(q, cache_on_gpu(*host), tables, lens, d ** -0.5, ws=ws)
             check_decode(out, q, host, tables, lens, d ** -0.5, f"round {round_}, case {i}")
+
+
+@pytest.mark.parametrize("top", [1, 900])
+def test_the_largest_batch(top):
+    """65535 sequences of no or one token (and three longer ones): a lone value row comes back as it is."""
+    B, Hq, Hkv, d, bs = 65535, 2, 1, 64, 16
+    rng = np.random.default_rng(top)
+    lens = rng.integers(0, 2, B)
+    lens[[0, 40000, B - 1]] = top
+    host = random_cache(100, Hkv, bs, d, rng)
+    tables = rng.integers(0, 100, (B, -(-top // bs))).astype(np.int32)
+    q = torch.from_numpy(rng.standard_normal((B, 1, Hq, d))).to(torch.bfloat16).cuda()
+    out = run_decode(q, cache_on_gpu(*host), tables, lens, 0.125)
+    long = np.flatnonzero(lens == top)[:3] if top > 1 else np.array([0])
+    check_decode(out[long], q[long], host, tables[long], lens[long], 0.125)
+    v = OQ.values(host[1][:, 0, 0], host[3][:, 0, 0])[tables[:, 0]]  # the first token of each sequence's first block
+    got = out[:, 0].double().cpu().numpy()
+    one = lens == 1
+    assert np.array_equal(got[one], np.broadcast_to(v[one][:, None], got[one].shape))
+    assert not got[lens == 0].any()
