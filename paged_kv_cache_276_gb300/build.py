@@ -1,10 +1,12 @@
-"""Build the native library libpkv.so (CUDA kernels for sm_103a + host allocator).
+"""Build the native library libpkv.so (CUDA kernels for sm_103a + host allocator)
+and _bind.so, the Python entry of its shortest calls.
 
 Usage: python -m paged_kv_cache_276_gb300.build [--force]
 
 Translation units are compiled in parallel with nvcc, then linked into
 ``paged_kv_cache_276_gb300/_build/libpkv.so`` (in-tree, git-ignored).  The CUDA
 runtime is linked statically, so the library only needs the driver at run time.
+_bind.so is a Python extension beside it, over PyTorch's C++ tensors.
 """
 from __future__ import annotations
 
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
+BIND = os.path.join(BUILD, "_bind.so")
 
 SOURCES = ["decode.cu", "chunk_tc.cu", "cache_ops.cu", "quant_ops.cu", "decode_quant.cu", "alloc.cpp", "step.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -43,9 +47,9 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -62,15 +66,41 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_bind() -> str:
+    obj = os.path.join(BUILD, "bind.o")
+    torch_inc = os.path.join(_torch_dir(), "include")
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    subprocess.run(["g++", "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
+                    "-I", sysconfig.get_paths()["include"], "-I", torch_inc,
+                    "-I", os.path.join(torch_inc, "torch", "csrc", "api", "include"), "-I", cuda_inc], check=True)
+    return obj
+
+
+def _link_bind(obj: str):
+    tmp = BIND + f".tmp{os.getpid()}"
+    subprocess.run(["g++", "-shared", obj, "-o", tmp, "-L", BUILD, "-l:libpkv.so", "-Wl,-rpath,$ORIGIN",
+                    "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
+                   check=True)
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(_compile, SOURCES))
+        bind_obj = bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "static"], check=True)
     os.replace(tmp, LIB)
+    _link_bind(bind_obj)
     return LIB
 
 

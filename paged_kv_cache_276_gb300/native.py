@@ -1,5 +1,6 @@
 """ctypes binding of libpkv.so: the C ABI declared in include/pkv.h, one Python
-function per C entry point with the same name.
+function per C entry point with the same name (the 8-bit cache's calls go through
+a small extension, _bind.so, for their host time).
 
 Argument marshalling only: shapes are read off the tensors, pointers and the
 current CUDA stream are passed through, return codes become exceptions.  Every
@@ -9,6 +10,7 @@ if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -516,120 +518,100 @@ def paged_attention_decode_static_scratch(q, k_cache, v_cache, block_tables, seq
 
 
 # ------------------------------------------------------- the cache in 8 bits
-# These calls are short on the GPU (a few microseconds for a decode step's
-# write), so their checks are written to cost little: one expression over the
-# tensors (about 0.15 us each), which only on failure is gone through one by one
-# for its message; addresses go to the library as plain integers.
+# These calls take less time on the GPU than a marshalling through ctypes takes
+# on the host, so they go through _bind.so, which checks the tensors and calls
+# the C ABI.  It answers _RECHECK for arguments that the call does not take;
+# they are then gone through here for the message.
 _BF16, _F8, _U8, _I32, _I64 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64
+_RECHECK = 1
+BIND_PATH = os.path.join(_HERE, "_build", "_bind.so")
+_bind_module = None
 
 
-def _need_each(k_codes, v_codes, k_exps, v_exps, *others):
-    """The cache's tensors, and (tensor, dtype, name) of others on its device: raises for the first that is wrong."""
+def _bind():
+    """The loaded extension; raises if it has not been built."""
+    global _bind_module
+    if _bind_module is None:
+        lib()
+        with _lock:
+            if _bind_module is None:
+                if not os.path.exists(BIND_PATH):
+                    raise RuntimeError(
+                        f"{BIND_PATH} is missing: build it with `python -m paged_kv_cache_276_gb300.build`")
+                spec = importlib.util.spec_from_file_location(f"{__package__}._bind", BIND_PATH)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                _bind_module = module
+    return _bind_module
+
+
+def _handle(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
+
+
+def _refuse_cache(k_codes, v_codes, k_exps, v_exps, d_status, *others):
+    """Raise for the first argument that is not what a call takes; returns the cache's shape.
+    others: (tensor, dtype, name) of further tensors on the cache's device."""
     dev = k_codes.device if isinstance(k_codes, torch.Tensor) else None
     for t, dtype, name in ((k_codes, _F8, "k_codes"), (v_codes, _F8, "v_codes"), (k_exps, _U8, "k_exps"),
                            (v_exps, _U8, "v_exps")) + others:
         _need(t, dtype, name, dev)
-
-
-def _quant_cache_ok(k_codes, v_codes, k_exps, v_exps):
-    i = k_codes.get_device()
-    return (k_codes.dtype is _F8 and v_codes.dtype is _F8 and k_exps.dtype is _U8 and v_exps.dtype is _U8
-            and v_codes.get_device() == i and k_exps.get_device() == i and v_exps.get_device() == i
-            and k_codes.is_contiguous() and v_codes.is_contiguous() and k_exps.is_contiguous()
-            and v_exps.is_contiguous())
-
-
-def _quant_cache_shape(k_codes, v_codes, k_exps, v_exps):
-    shape = k_codes.shape
-    if len(shape) != 4 or v_codes.shape != shape or k_exps.shape != shape[:3] or v_exps.shape != shape[:3]:
-        raise ValueError("shape mismatch: codes [NB, Hkv, bs, d] and exponents [NB, Hkv, bs] expected")
-    return shape
-
-
-def _status(d_status, index):
-    if d_status is None:
-        return None
-    if not isinstance(d_status, torch.Tensor) or d_status.dtype is not _I32 or d_status.get_device() != index:
+    if d_status is not None and (not isinstance(d_status, torch.Tensor) or d_status.dtype != _I32
+                                 or d_status.device != dev):
         raise TypeError("d_status must be a torch.int32 tensor on the cache's device")
-    return d_status.data_ptr()
+    if k_codes.dim() != 4 or v_codes.shape != k_codes.shape or k_exps.shape != k_codes.shape[:3] \
+            or v_exps.shape != k_exps.shape:
+        raise ValueError("shape mismatch: codes [NB, Hkv, bs, d] and exponents [NB, Hkv, bs] expected")
+    return k_codes.shape
 
 
-def _launch(fn, name, index, stream, args):
-    """Call ``fn(*args, stream)`` with CUDA device ``index`` current (the kernels are launched from there)."""
-    if index < 0:
-        raise ValueError("the cache must be on a CUDA device")
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == index:
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, stream)
-    if rc != PKV_OK:
-        raise PkvError(rc, name)
+def _refuse_rest(dev):
+    if dev.type != "cuda":
+        raise ValueError(f"the cache must be on a CUDA device, got {dev}")
+    raise ValueError("an argument is not what the call takes (a size beyond 31 bits, or not a number)")
 
 
-def _token_rows(t, name, shape, index):
-    """The stride in elements between tokens of [T, Hkv, d] rows whose own values are dense."""
+def _refuse_token_rows(t, name, shape, dev):
     if not isinstance(t, torch.Tensor) or t.dtype != _BF16:
         raise TypeError(f"{name} must be a torch.bfloat16 tensor")
-    if t.get_device() != index:
+    if t.device != dev:
         raise ValueError(f"{name} must be on the cache's device, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
     T, Hkv, d = shape
-    if t.is_contiguous():
-        return Hkv * d
     s = t.stride()
-    if T > 0 and (s[2] != 1 and d > 1 or s[1] != d and Hkv > 1 or T > 1 and (s[0] < Hkv * d or s[0] % 8)):
+    if not t.is_contiguous() and (s[2] != 1 and d > 1 or s[1] != d and Hkv > 1
+                                  or T > 1 and (s[0] < Hkv * d or s[0] % 8)):
         raise ValueError(f"{name}: each token's [Hkv, d] rows must be dense, tokens a multiple of 8 elements apart")
-    return s[0] if T > 1 else Hkv * d
 
 
 def pkv_write_quant(k, v, slot_mapping, k_codes, v_codes, k_exps, v_exps, d_status=None, stream=None):
     """Quantise new tokens into an 8-bit cache.  k, v: [T, Hkv, d] bf16, each token's rows dense (views of a
     fused projection's output are fine); slot_mapping: [T] int64, negative: skip; codes [NB, Hkv, bs, d]
     float8_e4m3fn, exponents [NB, Hkv, bs] uint8 (device).  d: a multiple of 16."""
-    try:
-        i = k_codes.get_device()
-        ok = (_quant_cache_ok(k_codes, v_codes, k_exps, v_exps) and slot_mapping.dtype is _I64
-              and slot_mapping.get_device() == i and slot_mapping.is_contiguous())
-    except AttributeError:
-        ok = False
-    if not ok:
-        _need_each(k_codes, v_codes, k_exps, v_exps, (slot_mapping, _I64, "slot_mapping"))
-    NB, Hkv, bs, d = _quant_cache_shape(k_codes, v_codes, k_exps, v_exps)
-    if slot_mapping.dim() != 1:
-        raise ValueError("slot_mapping: [T] expected")
-    shape = (slot_mapping.shape[0], Hkv, d)
-    ks, vs = _token_rows(k, "k", shape, i), _token_rows(v, "v", shape, i)
-    _launch(lib().pkv_write_quant, "pkv_write_quant", i, stream,
-            (k.data_ptr(), v.data_ptr(), ks, vs, slot_mapping.data_ptr(), shape[0], k_codes.data_ptr(),
-             v_codes.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(), NB, bs, Hkv, d, _status(d_status, i)))
+    rc = _bind().write_quant(k, v, slot_mapping, k_codes, v_codes, k_exps, v_exps, d_status, _handle(stream))
+    if rc == _RECHECK:
+        NB, Hkv, bs, d = _refuse_cache(k_codes, v_codes, k_exps, v_exps, d_status, (slot_mapping, _I64, "slot_mapping"))
+        if slot_mapping.dim() != 1:
+            raise ValueError("slot_mapping: [T] expected")
+        for t, name in ((k, "k"), (v, "v")):
+            _refuse_token_rows(t, name, (slot_mapping.shape[0], Hkv, d), k_codes.device)
+        _refuse_rest(k_codes.device)
+    _check(rc, "pkv_write_quant")
 
 
 def pkv_read_quant(k_codes, v_codes, k_exps, v_exps, slot_mapping, k, v, d_status=None, stream=None):
     """Rows of listed slots of an 8-bit cache, exactly, into k, v [T, Hkv, d] bf16 (rows of negative slots stay
     as they are); the cache as in ``pkv_write_quant``."""
-    try:
-        i = k_codes.get_device()
-        ok = (_quant_cache_ok(k_codes, v_codes, k_exps, v_exps) and slot_mapping.dtype is _I64 and k.dtype is _BF16
-              and v.dtype is _BF16 and slot_mapping.get_device() == i and k.get_device() == i and v.get_device() == i
-              and slot_mapping.is_contiguous() and k.is_contiguous() and v.is_contiguous())
-    except AttributeError:
-        ok = False
-    if not ok:
-        _need_each(k_codes, v_codes, k_exps, v_exps, (slot_mapping, _I64, "slot_mapping"), (k, _BF16, "k"),
-                   (v, _BF16, "v"))
-    NB, Hkv, bs, d = _quant_cache_shape(k_codes, v_codes, k_exps, v_exps)
-    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
-    if k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
-        raise ValueError("shape mismatch between k/v, slot_mapping [T] and the cache")
-    _launch(lib().pkv_read_quant, "pkv_read_quant", i, stream,
-            (k_codes.data_ptr(), v_codes.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(), slot_mapping.data_ptr(), T,
-             k.data_ptr(), v.data_ptr(), NB, bs, Hkv, d, _status(d_status, i)))
+    rc = _bind().read_quant(k_codes, v_codes, k_exps, v_exps, slot_mapping, k, v, d_status, _handle(stream))
+    if rc == _RECHECK:
+        NB, Hkv, bs, d = _refuse_cache(k_codes, v_codes, k_exps, v_exps, d_status,
+                                       (slot_mapping, _I64, "slot_mapping"), (k, _BF16, "k"), (v, _BF16, "v"))
+        T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+        if k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
+            raise ValueError("shape mismatch between k/v, slot_mapping [T] and the cache")
+        _refuse_rest(k_codes.device)
+    _check(rc, "pkv_read_quant")
 
 
 def paged_attention_decode_quant_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len):
@@ -642,32 +624,19 @@ def paged_attention_decode_quant(q, k_codes, v_codes, k_exps, v_exps, block_tabl
     """Single-token decode over an 8-bit cache: q, out [B, 1, Hq, d] bf16; the cache as in ``pkv_write_quant``;
     tables [B, max_blocks] int32; lens [B] int32; workspace: a device buffer of
     ``paged_attention_decode_quant_workspace_size`` bytes (one per call that may overlap)."""
-    try:
-        i = k_codes.get_device()
-        ok = (_quant_cache_ok(k_codes, v_codes, k_exps, v_exps) and q.dtype is _BF16 and out.dtype is _BF16
-              and block_tables.dtype is _I32 and seq_lens.dtype is _I32 and q.get_device() == i
-              and out.get_device() == i and block_tables.get_device() == i and seq_lens.get_device() == i
-              and q.is_contiguous() and out.is_contiguous() and block_tables.is_contiguous()
-              and seq_lens.is_contiguous())
-    except AttributeError:
-        ok = False
-    if not ok:
-        _need_each(k_codes, v_codes, k_exps, v_exps, (q, _BF16, "q"), (out, _BF16, "out"),
-                   (block_tables, _I32, "block_tables"), (seq_lens, _I32, "seq_lens"))
-    NB, Hkv, bs, d = _quant_cache_shape(k_codes, v_codes, k_exps, v_exps)
-    qs, ts = q.shape, block_tables.shape
-    if len(qs) != 4 or qs[1] != 1 or qs[3] != d or out.shape != qs or len(ts) != 2 or ts[0] != qs[0] \
-            or seq_lens.shape != qs[:1]:
-        raise ValueError("shape mismatch")
-    ws, ws_bytes = None, 0
-    if workspace is not None:
-        if workspace.get_device() != i or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous, on the cache's device")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch(lib().paged_attention_decode_quant, "paged_attention_decode_quant", i, stream,
-            (q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(),
-             block_tables.data_ptr(), ts[1], seq_lens.data_ptr(), qs[0], int(max_seq_len), qs[2], Hkv, d, bs, NB,
-             float(scale), out.data_ptr(), ws, ws_bytes, _status(d_status, i)))
+    rc = _bind().decode_quant(q, k_codes, v_codes, k_exps, v_exps, block_tables, seq_lens, int(max_seq_len),
+                              float(scale), out, workspace, d_status, _handle(stream))
+    if rc == _RECHECK:
+        d = _refuse_cache(k_codes, v_codes, k_exps, v_exps, d_status, (q, _BF16, "q"), (out, _BF16, "out"),
+                          (block_tables, _I32, "block_tables"), (seq_lens, _I32, "seq_lens"))[3]
+        if q.dim() != 4 or q.shape[1] != 1 or q.shape[3] != d or out.shape != q.shape or block_tables.dim() != 2 \
+                or block_tables.shape[0] != q.shape[0] or seq_lens.shape != q.shape[:1]:
+            raise ValueError("shape mismatch")
+        if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.device != k_codes.device
+                                      or not workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        _refuse_rest(k_codes.device)
+    _check(rc, "paged_attention_decode_quant")
 
 
 # ------------------------------------------------------------- allocator
