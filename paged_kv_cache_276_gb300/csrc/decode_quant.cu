@@ -51,6 +51,7 @@ constexpr int kUnitBytes = 4096;  // key codes of one unit; the value codes take
 // when an x exceeds it by more than 15, so weights stay below 2^15 (fp16 holds
 // 65504) and most units skip the rescale.
 constexpr float kHeadroom = 7.f, kSlack = 15.f;
+constexpr int kDirectUnits = 2;  // runs of at most so many units may go to a warp whole
 
 struct Params {
   const __nv_bfloat16 *q;
@@ -61,6 +62,7 @@ struct Params {
   int4 *ws_desc;  // {sequence | KV head << 16, -, last CTA of the run, 1} of the run that leaves CTA c, or .w = 0
   int32_t *status;
   int num_seqs, max_blocks, max_len, num_q_heads, num_kv_heads, group, num_blocks;
+  int direct;  // whole runs go round the warps (no sequence has more than kDirectUnits units)
   float scale_log2;
 };
 
@@ -427,6 +429,7 @@ struct Cursor {
   int seq, h, j, n, len;
   int wbase, window;  // 32 table entries from wbase on, one per lane
   bool from0;         // the current piece began at its run's first unit
+  bool done;          // nothing is left to issue
 };
 
 template <int D, int BS, int NT>
@@ -461,6 +464,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     for (int s = 0; s < S; ++s) mbar_init(full + 8 * s, 1 + EXP_LANES);
     mbar_init_fence();
   }
+  __syncwarp();  // a warp's barriers are its own
   if (tid < 2 * NW) pieces[tid] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) {
     tma_prefetch_desc(&tmk);
@@ -468,7 +472,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   }
   grid_dependency_wait();  // the inputs may come from the kernel launched just before
 
-  // ---- prefix sums of the runs' units: thread i holds sequences [i CH, (i + 1) CH)
   const int cap = capped_len(p, BS);
   const int CH = (p.num_seqs + TH - 1) / TH;
   auto length = [&](int seq) {
@@ -476,102 +479,142 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     return L < 0 ? 0 : min(L, cap);
   };
   auto units = [&](int L) { return (static_cast<uint32_t>(L) + UT - 1) / UT; };
-  uint32_t mine = 0;
-  int any_empty = 0;
-  for (int k = 0; k < CH; ++k) {
-    const int seq = tid * CH + k;
-    if (seq >= p.num_seqs) break;
-    int L = p.seq_lens[seq];
-    if (L < 0 || L > cap) {
-      if (blockIdx.x == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_LEN);
-      L = L < 0 ? 0 : cap;
-    }
-    mine += units(L);
-    any_empty |= L == 0;
-    if (k == 0) chunk_len[tid] = L;
-  }
-  uint32_t incl = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const uint32_t t = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += t;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  uint32_t before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const uint32_t x = warp_sum[w];
-    if (w < warp) before += x;
-    total += x;
-  }
-  chunk_start[tid] = (before + incl - mine) * p.num_kv_heads;
-  any_empty = __syncthreads_or(any_empty);
-  const uint32_t U = total * p.num_kv_heads;  // below 2^31 (checked on the host)
-  // as many CTAs as give every warp a unit; the others have none.  CTA c's
-  // range, then the warp's part of it: equal to within a unit.  Where no run has
-  // more units than a CTA has warps (no workspace), a CTA's range is moved to
-  // the runs' borders: no run spans CTAs.
-  const uint32_t nc = max(1u, min(gridDim.x, (U + NW - 1) / NW));
-  const uint32_t cq = U / nc, crem = U - cq * nc;
-  const bool whole = p.ws == nullptr && nc > 1;
-  uint32_t u0 = 0, u1 = 0;
   Cursor c{};
-  if (blockIdx.x < nc) {
-    uint32_t cs = blockIdx.x * cq + min(blockIdx.x, crem), ce = cs + cq + (blockIdx.x < crem ? 1 : 0);
-#pragma unroll 1
-    for (int step = whole ? 0 : 2; step < 3; ++step) {  // the run at cs, at ce, at this warp's start
-      if (step == 2) {
-        const uint32_t size = ce - cs, wq = size / NW, wrem = size - wq * NW, w = warp;
-        u0 = cs + w * wq + min(w, wrem);
-        u1 = u0 + wq + (w < wrem ? 1 : 0);
-        if (u0 == u1) break;
+  uint32_t u0 = 0, u1 = 0;      // this warp's units of the batch's; direct: [0, whatever its runs have)
+  uint32_t cq = 0, crem = 0;    // units of a CTA, and how many CTAs have one more
+  int any_empty = 0;            // a sequence without keys
+  // Direct: warp i takes the runs i, i + (number of warps), ...; the next one
+  // with keys (the others' outputs are zeros).  A run is a unit or two, so its
+  // table entries load beside its length.
+  const uint32_t runs = static_cast<uint32_t>(p.num_seqs) * static_cast<uint32_t>(p.num_kv_heads);
+  const uint32_t warps = gridDim.x * NW;
+  uint32_t run = blockIdx.x * NW + warp;
+  auto take_run = [&]() {
+    for (;; run += warps) {
+      if (run >= runs) {
+        c.done = true;
+        return;
       }
-      const uint32_t u = step == 0 ? cs : step == 1 ? ce : u0;
-      if (u >= U) continue;  // ce of the last CTA
-      // the last chunk that starts at or before u
-      int at = 0;
-#pragma unroll
-      for (int k = 0; k < NW; ++k) at += chunk_start[k * 32 + lane] <= u ? 1 : 0;
-      at = __reduce_add_sync(0xffffffffu, at) - 1;
-      uint32_t base = chunk_start[at];
-      c.seq = at;
-      c.len = chunk_len[at];
-      if (CH > 1) {  // walk the chunk, 32 sequences at a time
-        for (int seq = at * CH;; seq += 32) {
-          const int s = seq + lane, L = s < p.num_seqs ? length(s) : 0;
-          uint32_t pre = units(L) * p.num_kv_heads;
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t t = __shfl_up_sync(0xffffffffu, pre, off);
-            if (lane >= off) pre += t;
-          }
-          const unsigned in = __ballot_sync(0xffffffffu, u < base + pre);
-          if (in || seq + 32 >= p.num_seqs) {
-            const int src = in ? __ffs(in) - 1 : 31;
-            c.seq = min(seq + src, p.num_seqs - 1);
-            c.len = __shfl_sync(0xffffffffu, L, src);
-            base += src > 0 ? __shfl_sync(0xffffffffu, pre, src - 1) : 0;
-            break;
-          }
-          base += __shfl_sync(0xffffffffu, pre, 31);
-        }
+      c.seq = static_cast<int>(run / static_cast<uint32_t>(p.num_kv_heads));
+      c.h = static_cast<int>(run - static_cast<uint32_t>(c.seq) * p.num_kv_heads);
+      const int L = p.seq_lens[c.seq];
+      c.window = lane < p.max_blocks ? p.block_tables[static_cast<size_t>(c.seq) * p.max_blocks + lane] : -1;
+      c.len = L < 0 ? 0 : min(L, cap);
+      if (L != c.len && c.h == 0 && lane == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_LEN);
+      if (c.len > 0) break;
+      uint4 *dst = reinterpret_cast<uint4 *>(
+          p.out + (static_cast<size_t>(c.seq) * p.num_q_heads + static_cast<size_t>(c.h) * p.group) * D);
+      for (int k = lane; k < p.group * (D / 8); k += 32) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (runs - run <= warps) {  // (the sum may pass 32 bits)
+        c.done = true;
+        return;
       }
-      c.n = max(1, static_cast<int>(units(c.len)));
-      c.h = static_cast<int>((u - base) / static_cast<uint32_t>(c.n));
-      c.j = static_cast<int>(u - base) - c.h * c.n;
-      const uint32_t border = c.j == 0 ? u : u + (c.n - c.j);  // the first run that starts at or behind u
-      if (step == 0) cs = border;
-      if (step == 1) ce = border;
     }
-  }
-
-  bool ok = true;
-  if (u0 < u1) {
+    c.n = static_cast<int>(units(c.len));
+    c.j = 0;
+    c.wbase = 0;
+    c.from0 = true;
+  };
+  if (p.direct) {
+    u1 = 0xffffffffu;
+    take_run();
+  } else {
+    // ---- prefix sums of the runs' units: thread i holds sequences [i CH, (i + 1) CH)
+    uint32_t mine = 0;
+    for (int k = 0; k < CH; ++k) {
+      const int seq = tid * CH + k;
+      if (seq >= p.num_seqs) break;
+      int L = p.seq_lens[seq];
+      if (L < 0 || L > cap) {
+        if (blockIdx.x == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_LEN);
+        L = L < 0 ? 0 : cap;
+      }
+      mine += units(L);
+      any_empty |= L == 0;
+      if (k == 0) chunk_len[tid] = L;
+    }
+    uint32_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += t;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    uint32_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const uint32_t x = warp_sum[w];
+      if (w < warp) before += x;
+      total += x;
+    }
+    chunk_start[tid] = (before + incl - mine) * p.num_kv_heads;
+    any_empty = __syncthreads_or(any_empty);
+    const uint32_t U = total * p.num_kv_heads;  // below 2^31 (checked on the host)
+    // as many CTAs as give every warp a unit; the others have none.  CTA c's
+    // range, then the warp's part of it: equal to within a unit.  Where no run has
+    // more units than a CTA has warps (no workspace), a CTA's range is moved to
+    // the runs' borders: no run spans CTAs.
+    const uint32_t nc = max(1u, min(gridDim.x, (U + NW - 1) / NW));
+    cq = U / nc;
+    crem = U - cq * nc;
+    const bool whole = p.ws == nullptr && nc > 1;
+    if (blockIdx.x < nc) {
+      uint32_t cs = blockIdx.x * cq + min(blockIdx.x, crem), ce = cs + cq + (blockIdx.x < crem ? 1 : 0);
+#pragma unroll 1
+      for (int step = whole ? 0 : 2; step < 3; ++step) {  // the run at cs, at ce, at this warp's start
+        if (step == 2) {
+          const uint32_t size = ce - cs, wq = size / NW, wrem = size - wq * NW, w = warp;
+          u0 = cs + w * wq + min(w, wrem);
+          u1 = u0 + wq + (w < wrem ? 1 : 0);
+          if (u0 == u1) break;
+        }
+        const uint32_t u = step == 0 ? cs : step == 1 ? ce : u0;
+        if (u >= U) continue;  // ce of the last CTA
+        // the last chunk that starts at or before u
+        int at = 0;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) at += chunk_start[k * 32 + lane] <= u ? 1 : 0;
+        at = __reduce_add_sync(0xffffffffu, at) - 1;
+        uint32_t base = chunk_start[at];
+        c.seq = at;
+        c.len = chunk_len[at];
+        if (CH > 1) {  // walk the chunk, 32 sequences at a time
+          for (int seq = at * CH;; seq += 32) {
+            const int s = seq + lane, L = s < p.num_seqs ? length(s) : 0;
+            uint32_t pre = units(L) * p.num_kv_heads;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+              const uint32_t t = __shfl_up_sync(0xffffffffu, pre, off);
+              if (lane >= off) pre += t;
+            }
+            const unsigned in = __ballot_sync(0xffffffffu, u < base + pre);
+            if (in || seq + 32 >= p.num_seqs) {
+              const int src = in ? __ffs(in) - 1 : 31;
+              c.seq = min(seq + src, p.num_seqs - 1);
+              c.len = __shfl_sync(0xffffffffu, L, src);
+              base += src > 0 ? __shfl_sync(0xffffffffu, pre, src - 1) : 0;
+              break;
+            }
+            base += __shfl_sync(0xffffffffu, pre, 31);
+          }
+        }
+        c.n = max(1, static_cast<int>(units(c.len)));
+        c.h = static_cast<int>((u - base) / static_cast<uint32_t>(c.n));
+        c.j = static_cast<int>(u - base) - c.h * c.n;
+        const uint32_t border = c.j == 0 ? u : u + (c.n - c.j);  // the first run that starts at or behind u
+        if (step == 0) cs = border;
+        if (step == 1) ce = border;
+      }
+    }
     c.wbase = -32;
     c.window = -1;
     c.from0 = c.j == 0;
+    c.done = u0 == u1;
+  }
 
+  bool ok = true;
+  if (!c.done) {
     const uint64_t pol = l2_policy_evict_first();
     uint32_t next = u0;  // next unit to issue
     // Issue the cursor's unit into stage s and move the cursor on (whole warp).
@@ -625,12 +668,22 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             p.q + (static_cast<size_t>(c.seq) * p.num_q_heads + static_cast<size_t>(c.h) * p.group) * D + lane * 64));
       __syncwarp();  // meta[s] is there for every lane
       ++next;
+      if (next == u1) c.done = true;
       if (!ends) {
         ++c.j;
         return;
       }
       c.j = 0;
       c.from0 = true;
+      if (p.direct) {
+        if (runs - run <= warps) {
+          c.done = true;
+        } else {
+          run += warps;
+          take_run();
+        }
+        return;
+      }
       if (next >= u1 || ++c.h < p.num_kv_heads) return;
       c.h = 0;
       do {
@@ -640,15 +693,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       c.wbase = -32;
     };
 
-    const int count = static_cast<int>(u1 - u0);
-    for (int s = 0; s < S && s < count; ++s) issue(s);
+    for (int s = 0; s < S && !c.done; ++s) issue(s);
 
     Acc<D, NT> acc;
     uint32_t qf[NT][D / 16][2];
     float cf[NT][2];
     const int g4 = lane >> 2, c4 = lane & 3;
     int i = 0;
-    for (; i < count; ++i) {
+    for (; i < static_cast<int>(next - u0); ++i) {
       const int s = i % S;
       const int4 m = meta[s];
       if (m.z & (1 << 16)) {  // while the unit is on its way
@@ -672,7 +724,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
                                                valid - t, lane);
       }
       __syncwarp();
-      if (next < u1) issue(s);
+      if (!c.done) issue(s);
       if (m.z & (1 << 17)) {  // the piece ends here
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -735,6 +787,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     if (!ok)
       for (int k = i + 1; k < static_cast<int>(next - u0); ++k) mbar_wait(full + 8 * (k % S), (k / S) & 1);
   }
+  if (p.direct) return;
   const bool failed = __syncthreads_or(!ok);
 
   // ---- join the pieces of each run
@@ -855,7 +908,8 @@ __global__ void __launch_bounds__(JoinShape<D, NT>::kThreads) join_kernel(const 
 struct Plan {
   int grid = 1;
   size_t piece_bytes = 0;
-  bool whole = false;  // runs are not split between CTAs
+  bool whole = false;   // runs are not split between CTAs
+  bool direct = false;  // nor between warps
   size_t ws_bytes() const { return grid > 1 && !whole ? grid * (2 * piece_bytes + sizeof(int4)) : 0; }
 };
 
@@ -869,9 +923,17 @@ Plan make_plan(int num_seqs, int num_kv_heads, int group, int head_dim, int max_
   const double units = static_cast<double>(num_seqs) * num_kv_heads * ((max_seq_len + (tokens - 1ll)) / tokens);
   Plan plan;
   plan.grid = static_cast<int>(std::max(1.0, std::min<double>(num_sms(), std::ceil(units / warps))));
+  const long long longest = (max_seq_len + (tokens - 1ll)) / tokens;
+  // Runs of a unit or two go to the warps whole, without prefix sums or joins,
+  // where each warp gets one at most, or so many that uneven numbers do not
+  // matter.  Measured, this way / by equal units: 3 sequences 3.6 / 4.6 us, 1688
+  // runs of up to 2 units 7.1 / 10.6, 4096 of 2 (2.2 a warp) 22.0 / 20.5.
+  const double runs = static_cast<double>(num_seqs) * num_kv_heads, slots = static_cast<double>(num_sms()) * warps;
+  plan.direct = longest <= kDirectUnits && (runs <= slots || runs >= 8 * slots);
+  if (plan.direct) plan.grid = static_cast<int>(std::min<double>(num_sms(), std::ceil(runs / warps)));
   // A run of at most a unit per warp is not worth splitting between CTAs: the
   // second kernel costs more (about 3 us) than the runs' uneven ends.
-  plan.whole = (max_seq_len + (tokens - 1ll)) / tokens <= warps;
+  plan.whole = longest <= warps;
   plan.piece_bytes = (static_cast<size_t>(nt) * 8 * head_dim + 2 * nt * 8) * sizeof(float);
   return plan;
 }
@@ -980,6 +1042,7 @@ int paged_attention_decode_quant(const pkv_bf16 *q, const uint8_t *k_codes, cons
     p.ws_desc = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + plan.grid * 2 * plan.piece_bytes);
   }
   p.status = d_status;
+  p.direct = plan.direct;
   p.num_seqs = num_seqs;
   p.max_blocks = max_blocks_per_seq;
   p.max_len = max_seq_len;

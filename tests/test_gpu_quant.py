@@ -302,6 +302,25 @@ def test_decode_short_sequences(d, Hq, Hkv, top):
         check_decode(run_decode(q, cache_on_gpu(*host), tables, lens, d ** -0.5), q, host, tables, lens, d ** -0.5)
 
 
+@pytest.mark.parametrize("d,Hq,Hkv,bs,top", [(128, 8, 2, 16, 64), (128, 8, 2, 16, 65), (64, 4, 4, 32, 128), (64, 4, 4, 32, 129),
+                                             (128, 16, 1, 128, 64), (64, 12, 1, 64, 128), (128, 3, 3, 64, 1), (64, 1, 1, 16, 33)])
+def test_decode_very_short_sequences(d, Hq, Hkv, bs, top):
+    """Batches around the length up to which a sequence is one warp's, from one sequence to more runs than warps."""
+    rng = np.random.default_rng(top + bs)
+    for B in (1, 5, 300, 900 if Hkv > 1 else 2000):
+        lens = rng.integers(0, top + 1, B)
+        lens[rng.integers(0, B, 3)] = top
+        q, host, tables = decode_case(lens.tolist(), d, bs, Hq, Hkv, seed=top + B)
+        st = status_tensor()
+        out = run_decode(q, cache_on_gpu(*host), tables, lens, d ** -0.5, status=st)
+        assert st.item() == 0
+        check_decode(out, q, host, tables, lens, d ** -0.5)
+        bad = lens.copy()
+        bad[0] = -3
+        out = run_decode(q, cache_on_gpu(*host), tables, bad, d ** -0.5, max_len=top, status=st)
+        assert st.item() == native.PKV_STATUS_BAD_LEN and not out[0].any()
+
+
 def test_decode_all_empty():
     q, host, tables = decode_case([0, 0, 0], 128, 16, 8, 2, seed=2)
     for max_len in (0, 100, 100000):
