@@ -51,7 +51,8 @@ constexpr int kUnitBytes = 4096;  // key codes of one unit; the value codes take
 // when an x exceeds it by more than 15, so weights stay below 2^15 (fp16 holds
 // 65504) and most units skip the rescale.
 constexpr float kHeadroom = 7.f, kSlack = 15.f;
-constexpr int kDirectUnits = 2;  // runs of at most so many units may go to a warp whole
+constexpr int kDirectUnits = 2;   // runs of at most so many units may go to a warp whole
+constexpr int kDirectRounds = 2;  // ... of so many per warp to a CTA
 
 struct Params {
   const __nv_bfloat16 *q;
@@ -62,7 +63,7 @@ struct Params {
   int4 *ws_desc;  // {sequence | KV head << 16, -, last CTA of the run, 1} of the run that leaves CTA c, or .w = 0
   int32_t *status;
   int num_seqs, max_blocks, max_len, num_q_heads, num_kv_heads, group, num_blocks;
-  int direct;  // whole runs go round the warps (no sequence has more than kDirectUnits units)
+  int direct;  // 1: whole runs go round the warps; k > 1: k warps of a CTA share a run; 0: equal ranges of units
   float scale_log2;
 };
 
@@ -483,12 +484,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   uint32_t u0 = 0, u1 = 0;      // this warp's units of the batch's; direct: [0, whatever its runs have)
   uint32_t cq = 0, crem = 0;    // units of a CTA, and how many CTAs have one more
   int any_empty = 0;            // a sequence without keys
-  // Direct: warp i takes the runs i, i + (number of warps), ...; the next one
-  // with keys (the others' outputs are zeros).  A run is a unit or two, so its
-  // table entries load beside its length.
+  // Direct, 1: warp i takes the runs i, i + (number of warps), ...; the next one
+  // with keys (the others' outputs are zeros).  Direct, k > 1: k consecutive
+  // warps of a CTA share one run.  The table entries load beside a run's length.
   const uint32_t runs = static_cast<uint32_t>(p.num_seqs) * static_cast<uint32_t>(p.num_kv_heads);
   const uint32_t warps = gridDim.x * NW;
+  int part = 0;
   uint32_t run = blockIdx.x * NW + warp;
+  if (p.direct > 1) {
+    const int together = NW / p.direct, mine = warp / p.direct;
+    part = warp - mine * p.direct;
+    run = mine < together ? blockIdx.x * together + mine : runs;
+  }
   auto take_run = [&]() {
     for (;; run += warps) {
       if (run >= runs) {
@@ -500,20 +507,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       const int L = p.seq_lens[c.seq];
       c.window = lane < p.max_blocks ? p.block_tables[static_cast<size_t>(c.seq) * p.max_blocks + lane] : -1;
       c.len = L < 0 ? 0 : min(L, cap);
-      if (L != c.len && c.h == 0 && lane == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_LEN);
-      if (c.len > 0) break;
-      uint4 *dst = reinterpret_cast<uint4 *>(
-          p.out + (static_cast<size_t>(c.seq) * p.num_q_heads + static_cast<size_t>(c.h) * p.group) * D);
-      for (int k = lane; k < p.group * (D / 8); k += 32) dst[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (runs - run <= warps) {  // (the sum may pass 32 bits)
+      c.n = static_cast<int>(units(c.len));
+      c.wbase = 0;
+      if (p.direct > 1) {
+        const int q = c.n / p.direct, r = c.n - q * p.direct;
+        c.j = part * q + min(part, r);
+        u1 = q + (part < r ? 1 : 0);
+      }
+      c.from0 = c.j == 0;
+      if (L != c.len && c.h == 0 && part == 0 && lane == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_LEN);
+      if (c.n > 0) {
+        c.done = u1 == 0;
+        return;
+      }
+      if (part == 0) {
+        uint4 *dst = reinterpret_cast<uint4 *>(
+            p.out + (static_cast<size_t>(c.seq) * p.num_q_heads + static_cast<size_t>(c.h) * p.group) * D);
+        for (int k = lane; k < p.group * (D / 8); k += 32) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (p.direct > 1 || runs - run <= warps) {  // (the sum may pass 32 bits)
         c.done = true;
         return;
       }
     }
-    c.n = static_cast<int>(units(c.len));
-    c.j = 0;
-    c.wbase = 0;
-    c.from0 = true;
   };
   if (p.direct) {
     u1 = 0xffffffffu;
@@ -675,7 +691,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       }
       c.j = 0;
       c.from0 = true;
-      if (p.direct) {
+      if (p.direct == 1) {
         if (runs - run <= warps) {
           c.done = true;
         } else {
@@ -787,7 +803,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     if (!ok)
       for (int k = i + 1; k < static_cast<int>(next - u0); ++k) mbar_wait(full + 8 * (k % S), (k / S) & 1);
   }
-  if (p.direct) return;
+  if (p.direct == 1) return;
   const bool failed = __syncthreads_or(!ok);
 
   // ---- join the pieces of each run
@@ -909,7 +925,7 @@ struct Plan {
   int grid = 1;
   size_t piece_bytes = 0;
   bool whole = false;   // runs are not split between CTAs
-  bool direct = false;  // nor between warps
+  int direct = 0;       // as Params::direct
   size_t ws_bytes() const { return grid > 1 && !whole ? grid * (2 * piece_bytes + sizeof(int4)) : 0; }
 };
 
@@ -927,13 +943,23 @@ Plan make_plan(int num_seqs, int num_kv_heads, int group, int head_dim, int max_
   // Runs of a unit or two go to the warps whole, without prefix sums or joins,
   // where each warp gets one at most, or so many that uneven numbers do not
   // matter.  Measured, this way / by equal units: 3 sequences 3.6 / 4.6 us, 1688
-  // runs of up to 2 units 7.1 / 10.6, 4096 of 2 (2.2 a warp) 22.0 / 20.5.
+  // runs of up to 2 units 7.1 / 10.6, 4096 of 2 (2.2 a warp) 22.0 / 20.5.  Where
+  // there are few longer ones, a run gets as many warps of one CTA as the longest
+  // has units, and only a join: 22 x up to 120 tokens x 8 heads 5.4 / 8.4 us,
+  // 18 x up to 380 8.1 / 10.1, 8 x 704 9.4 / 11.2; at four units a warp it is
+  // even (8 x 1400 13.1 / 13.5, 2 x 1400 12.6 / 10.5).
   const double runs = static_cast<double>(num_seqs) * num_kv_heads, slots = static_cast<double>(num_sms()) * warps;
-  plan.direct = longest <= kDirectUnits && (runs <= slots || runs >= 8 * slots);
-  if (plan.direct) plan.grid = static_cast<int>(std::min<double>(num_sms(), std::ceil(runs / warps)));
+  const int share = static_cast<int>(std::min<long long>(warps, std::max(1ll, longest))), together = warps / share;
+  if (longest <= kDirectUnits && (runs <= slots || runs >= 8 * slots)) {
+    plan.direct = 1;
+    plan.grid = static_cast<int>(std::min<double>(num_sms(), std::ceil(runs / warps)));
+  } else if (longest <= kDirectRounds * warps && runs <= static_cast<double>(num_sms()) * together) {
+    plan.direct = share;
+    plan.grid = static_cast<int>(std::ceil(runs / together));
+  }
   // A run of at most a unit per warp is not worth splitting between CTAs: the
   // second kernel costs more (about 3 us) than the runs' uneven ends.
-  plan.whole = longest <= warps;
+  plan.whole = longest <= warps || plan.direct;
   plan.piece_bytes = (static_cast<size_t>(nt) * 8 * head_dim + 2 * nt * 8) * sizeof(float);
   return plan;
 }

@@ -291,11 +291,12 @@ def test_decode_many_sequences():
 
 
 @pytest.mark.parametrize("d,Hq,Hkv,top", [(128, 6, 3, 384), (128, 6, 3, 385), (64, 4, 2, 768), (64, 4, 2, 769), (128, 24, 2, 256),
-                                          (128, 24, 2, 257), (64, 12, 1, 640), (64, 12, 1, 641), (128, 5, 5, 33)])
+                                          (128, 24, 2, 257), (64, 12, 1, 640), (64, 12, 1, 641), (128, 5, 5, 33),
+                                          (128, 2, 2, 704), (128, 2, 2, 705), (64, 2, 1, 1536), (64, 2, 1, 1537)])
 def test_decode_short_sequences(d, Hq, Hkv, top):
     """Batches around the length up to which no sequence is split between CTAs."""
     rng = np.random.default_rng(top)
-    for B in (40, 400):
+    for B in (1, 40, 400 if top < 700 else 160):
         lens = rng.integers(0, top + 1, B)
         lens[rng.integers(0, B, 3)] = top
         q, host, tables = decode_case(lens.tolist(), d, 16, Hq, Hkv, seed=top + B)
