@@ -17,14 +17,22 @@
 // every SM streaming however the lengths are spread.  All (sequence, KV head)
 // runs are cut into units of kUnitBytes of keys (32 tokens at head_dim 128, 64
 // at 64) and laid end to end; every warp of a grid of one CTA per SM takes an
-// equal, contiguous range of units.  The lengths' prefix sums are taken by every
-// CTA at its start, so there is no host-built list and a captured graph follows
-// its lengths.  A warp streams its units through a ring of its own (TMA with the
+// equal, contiguous range of units (short batches: make_plan).  The lengths'
+// prefix sums are taken by every CTA at its start, so there is no host-built
+// list and a captured graph follows its lengths.  A warp streams its units through a ring of its own (TMA with the
 // 128-byte swizzle for the codes, cp.async for the exponents, one mbarrier per
 // stage) and refills a stage right after it has used it: no barrier between
 // warps until the end.  A run that a warp holds whole is written at once; pieces
 // of a run are joined in shared memory at the CTA's end, and runs that span
-// CTAs through the workspace by a second kernel.
+// CTAs through the workspace by a second kernel.  Joins follow the order of the
+// keys: results repeat bit for bit.
+//
+// Measured (both kernels, back to back in a graph): 16 x 32768 tokens, 64 q / 8
+// KV heads of 128, block 32: 173 us, 6.3 TB/s of 6.78 for a plain copy; 256
+// mixed lengths, 32 / 8, block 16: 75.5 us, 5.9 TB/s; one sequence of 32768:
+// 20.7 us, of which the copies take 12.6, start and joins the rest.  Units of
+// half or twice the size, or more stages with fewer warps, were 1 % faster on
+// the first at best and 7 to 28 % slower on the second.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -74,12 +82,13 @@ struct Shape {
   // tokens of one softmax step: the whole unit where registers allow (168 a thread with more than 8 warps, 255 with 8)
   static constexpr int kStep = NT == 1 || D == 128 ? kTokens : kTokens / 2;
   static constexpr int kTileFloats = NT * 8 * D;  // O of one piece, in accumulator order
-  static constexpr int kPieceFloats = kTileFloats + 2 * NT * 8;  // ..., m[cols], l[cols]
+  static constexpr int kPieceFloats = kTileFloats + 2 * NT * 8;  // ..., R[cols], l[cols]
   static constexpr int kRingBytes = kStages * 2 * kUnitBytes;
   static constexpr int kExpBytes = kStages * 2 * kTokens;
   static constexpr int kMetaBytes = kStages * (16 + 8);  // an int4 and a barrier per stage
   static constexpr int kWarpBytes = kRingBytes + kExpBytes + kMetaBytes + kPieceFloats * 4;
-  // as many warps as shared memory (227 KB a CTA) holds rings for
+  // as many warps as shared memory (227 KB a CTA) holds rings and pieces for; 8
+  // of them where two tiles at head_dim 128 need 255 registers a thread
   static constexpr int kWarps = D == 128 ? (NT == 1 ? 11 : 8) : (NT == 1 ? 12 : 10);
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kSmemBytes = 1024 + kWarps * kWarpBytes;
@@ -117,9 +126,10 @@ __device__ __forceinline__ int lds_u8(uint32_t a) {
   return static_cast<int>(r);
 }
 
-// 16 bytes global -> shared by this thread, asynchronously.
+// 16 bytes global -> shared by this thread, asynchronously, past L1 (which may
+// hold the line from before the newest tokens were written).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // One arrival on `bar` once this thread's cp.async copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -447,7 +457,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   __shared__ uint32_t warp_sum[NW];
   __shared__ __align__(16) uint32_t chunk_start[TH];  // first unit of each thread's sequences
   __shared__ int chunk_len[TH];         // their length, where a thread has one sequence
-  __shared__ uint4 pieces[2 * NW];      // each warp's first and last incomplete piece (see flush)
+  __shared__ uint4 pieces[2 * NW];      // each warp's incomplete pieces: from another warp's run, and of a run it starts
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
