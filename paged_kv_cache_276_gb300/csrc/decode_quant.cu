@@ -59,6 +59,8 @@ constexpr int kUnitBytes = 4096;  // key codes of one unit; the value codes take
 // when an x exceeds it by more than 15, so weights stay below 2^15 (fp16 holds
 // 65504) and most units skip the rescale.
 constexpr float kHeadroom = 7.f, kSlack = 15.f;
+// R before any x: every x moves it, and 2^(-inf - R) is still 0.
+constexpr float kNoRef = -1e38f;
 constexpr int kDirectUnits = 2;   // runs of at most so many units may go to a warp whole
 constexpr int kDirectRounds = 2;  // ... of so many per warp to a CTA
 
@@ -153,7 +155,7 @@ struct Acc {
   __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      r[nt][0] = r[nt][1] = -INFINITY;
+      r[nt][0] = r[nt][1] = kNoRef;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int md = 0; md < D / 16; ++md) o[md][nt][0] = o[md][nt][1] = o[md][nt][2] = o[md][nt][3] = 0.f;
@@ -249,60 +251,68 @@ __device__ __forceinline__ void attend_tokens(Acc<D, NT> &acc, const uint32_t (&
       for (int i = 0; i < 4; ++i) s[mt][0][i] += s2[i];
   }
 
-  // x = log2(e) s + ve, masked; the columns' largest
-  float top[NT][2], inv[MT][2];
+  // The tokens' scales, one lane per token of 32: {2^ke in the low half, 2^-ve in
+  // the high one} (powers of two are the upper 16 bits of an fp32), and ve.
+  uint32_t pow[MT / 2];
+  float add[MT / 2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+  for (int k = 0; k < MT / 2; ++k) {
+    const int ke = quant::clamp_exp(lds_u8(keb + k * 32 + lane)), ve = quant::clamp_exp(lds_u8(veb + k * 32 + lane));
+    pow[k] = static_cast<uint32_t>(ke + 127) << 7 | static_cast<uint32_t>(127 - ve) << 23;
+    add[k] = static_cast<float>(ve);
+  }
+  // x = log2(e) s + ve; the columns' largest
+  float top[NT][2], inv[MT][2];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const int tok = mt * 16 + g4 + 8 * hf;
-      const bool seen = tok < valid;
-      const int ke = quant::clamp_exp(lds_u8(keb + tok));
-      const int ve = quant::clamp_exp(lds_u8(veb + tok));
-      const float kf = quant::pow2i(ke), vf = static_cast<float>(ve);
-      inv[mt][hf] = quant::pow2i(-ve);
+      const int src = (mt & 1) * 16 + 8 * hf + g4;
+      const uint32_t pw = __shfl_sync(0xffffffffu, pow[mt >> 1], src);
+      const float vf = __shfl_sync(0xffffffffu, add[mt >> 1], src);
+      const float kf = __uint_as_float(pw << 16);
+      inv[mt][hf] = __uint_as_float(pw & 0xFFFF0000u);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = 2 * hf + e;
-          const float x = seen ? fmaf(s[mt][nt][i] * kf, cf[nt][e], vf) : -INFINITY;
-          s[mt][nt][i] = x;
-          top[nt][e] = fmaxf(top[nt][e], x);
-        }
+        for (int e = 0; e < 2; ++e) s[mt][nt][2 * hf + e] = fmaf(s[mt][nt][2 * hf + e] * kf, cf[nt][e], vf);
     }
-  float sub[NT][2], alpha[NT][2];
-  bool moved = false;
+  if (valid < 16 * MT) {  // warp-uniform
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (mt * 16 + g4 + 8 * (i >> 1) >= valid) s[mt][nt][i] = -INFINITY;
+  }
+  bool moves = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float t = top[nt][e];
+      float t = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+      for (int mt = 1; mt < MT; ++mt) t = fmax3(t, s[mt][nt][e], s[mt][nt][2 + e]);
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-      const float r = acc.r[nt][e];
-      alpha[nt][e] = 1.f;
-      if (t > r + kSlack) {  // also while r is -inf and t is not
-        const float n = t - kHeadroom;
-        alpha[nt][e] = fast_exp2(r - n);
-        acc.r[nt][e] = n;
-        moved = true;
-      }
-      sub[nt][e] = acc.r[nt][e] == -INFINITY ? 0.f : acc.r[nt][e];
+      top[nt][e] = t;
+      moves |= t > acc.r[nt][e] + kSlack;
     }
-  if (__any_sync(0xffffffffu, moved)) {
+  if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        acc.l[nt][e] *= alpha[nt][e];
+        const float r = acc.r[nt][e], n = top[nt][e] > r + kSlack ? top[nt][e] - kHeadroom : r;
+        const float alpha = fast_exp2(r - n);
+        acc.r[nt][e] = n;
+        acc.l[nt][e] *= alpha;
 #pragma unroll
         for (int md = 0; md < D / 16; ++md) {
-          acc.o[md][nt][e] *= alpha[nt][e];
-          acc.o[md][nt][e + 2] *= alpha[nt][e];
+          acc.o[md][nt][e] *= alpha;
+          acc.o[md][nt][e + 2] *= alpha;
         }
       }
   }
@@ -315,8 +325,8 @@ __device__ __forceinline__ void attend_tokens(Acc<D, NT> &acc, const uint32_t (&
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const float w0 = fast_exp2(s[mt][nt][2 * hf] - sub[nt][0]);
-        const float w1 = fast_exp2(s[mt][nt][2 * hf + 1] - sub[nt][1]);
+        const float w0 = fast_exp2(s[mt][nt][2 * hf] - acc.r[nt][0]);
+        const float w1 = fast_exp2(s[mt][nt][2 * hf + 1] - acc.r[nt][1]);
         acc.l[nt][0] = fmaf(w0, inv[mt][hf], acc.l[nt][0]);
         acc.l[nt][1] = fmaf(w1, inv[mt][hf], acc.l[nt][1]);
         pb[mt][nt][hf] = movmatrix_trans(pack_f16x2(w0, w1));
@@ -376,9 +386,8 @@ __device__ __forceinline__ void store_quad(const Params &p, uint32_t run, int co
   if (col + 1 < p.group) row[D / 2] = pack_bf16x2(o.y * i1, o.w * i1);
 }
 
-// Weight of a piece with reference r in a join to reference R; a piece without
-// a reference (-inf) holds nothing, or NaN: it counts as it is.
-__device__ __forceinline__ float piece_factor(float r, float R) { return r == -INFINITY ? 1.f : fast_exp2(r - R); }
+// Weight of a piece with reference r in a join to the largest reference R.
+__device__ __forceinline__ float piece_factor(float r, float R) { return fast_exp2(r - R); }
 
 // Join of one run's pieces in shared memory, tile nt, by one warp.  The whole
 // run goes to the output, a part of one to the workspace.
@@ -393,7 +402,7 @@ __device__ __forceinline__ void join_pieces(const Params &p, const uint4 g, int 
     return reinterpret_cast<const float *>((k & 1) ? smem + (k >> 1) * Sh::kRingBytes
                                                    : rest + (k >> 1) * (Sh::kPieceFloats * 4));
   };
-  float2 R = make_float2(-INFINITY, -INFINITY);
+  float2 R = make_float2(kNoRef, kNoRef);
 #pragma unroll 1
   for (unsigned left = g.x; left; left &= left - 1) {
     const float2 r = *reinterpret_cast<const float2 *>(place(__ffs(left) - 1) + Sh::kTileFloats + col);
@@ -885,7 +894,7 @@ __global__ void __launch_bounds__(JoinShape<D, NT>::kThreads) join_kernel(const 
   if (desc.w == 0) return;
   const float *first = p.ws + (static_cast<size_t>(c0) * 2 + 1) * Sh::kPieceFloats;
   const int n = desc.z - c0 + 1;
-  float2 R = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f);
+  float2 R = make_float2(kNoRef, kNoRef), l = make_float2(0.f, 0.f);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   // acc := acc 2^(R - M) + piece 2^(r - M)
   auto scale = [&](const float2 &M) {
@@ -904,7 +913,7 @@ __global__ void __launch_bounds__(JoinShape<D, NT>::kThreads) join_kernel(const 
     for (int k = 0; k < FLY; ++k) {
       const int i = base + k * J::kSplit;
       const float *x = first + (i == 0 ? 0 : i * 2 - 1) * static_cast<size_t>(Sh::kPieceFloats);
-      r[k] = i < n ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col) : make_float2(-INFINITY, -INFINITY);
+      r[k] = i < n ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col) : make_float2(kNoRef, kNoRef);
       pl[k] = i < n ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + COLS + col) : make_float2(0.f, 0.f);
       v[k] = i < n ? reinterpret_cast<const float4 *>(x)[t * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
