@@ -611,7 +611,9 @@ size_t paged_attention_decode_quant_workspace_size(int num_seqs, int num_q_heads
  *   q, out        device, [num_seqs][1][num_q_heads][head_dim] bf16
  *   block_tables, max_blocks_per_seq, seq_lens, max_seq_len, d_status: as
  *                 paged_attention_decode (table entries past a sequence's
- *                 blocks may hold anything)
+ *                 blocks may hold anything).  max_seq_len picks the schedule
+ *                 too: a tight bound on short sequences saves the workspace
+ *                 and a kernel
  *   workspace     device scratch, 16-byte aligned, at least
  *                 paged_attention_decode_quant_workspace_size(...) bytes (may
  *                 be NULL when that is 0); its contents need not be

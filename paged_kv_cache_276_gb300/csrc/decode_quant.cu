@@ -30,7 +30,7 @@
 // Measured (both kernels, back to back in a graph): 16 x 32768 tokens, 64 q / 8
 // KV heads of 128, block 32: 173 us, 6.3 TB/s of 6.78 for a plain copy; 256
 // mixed lengths, 32 / 8, block 16: 75.5 us, 5.9 TB/s; one sequence of 32768:
-// 20.7 us, of which the copies take 12.6, start and joins the rest.  Units of
+// 20.3 us, of which the copies take 12.6, start and joins the rest.  Units of
 // half or twice the size, or more stages with fewer warps, were 1 % faster on
 // the first at best and 7 to 28 % slower on the second.
 #include <cuda.h>
@@ -867,11 +867,60 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   }
 }
 
-// The run that starts in CTA c and spans more (blockIdx.x = c): the exact merge
-// of its pieces, CTA c's last and the first ones of the CTAs behind it.  Every
-// kSplit-th piece goes to one group of threads, five in flight (a run spans
-// 1/8 of the grid where one sequence has 8 KV heads: one round), and the
-// groups are joined in shared memory; a thread holds one accumulator quad.
+// A thread's share of the join of a run's pieces: one accumulator quad.
+struct Joined {
+  float2 R = make_float2(kNoRef, kNoRef), l = make_float2(0.f, 0.f);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void refer_to(const float2 &M) {
+    const float f0 = piece_factor(R.x, M.x), f1 = piece_factor(R.y, M.y);
+    l.x *= f0, l.y *= f1, o.x *= f0, o.y *= f1, o.z *= f0, o.w *= f1;
+    R = M;
+  }
+  __device__ __forceinline__ void add(const float2 &r, const float2 &pl, const float4 &v) {
+    const float f0 = piece_factor(r.x, R.x), f1 = piece_factor(r.y, R.y);
+    l.x += pl.x * f0, l.y += pl.y * f1, o.x += v.x * f0, o.y += v.y * f1, o.z += v.z * f0, o.w += v.w * f1;
+  }
+  // Pieces i0, i0 + step, ... of the n that follow each other from `first` on
+  // (CTA c0's last piece, then the first ones of the CTAs behind it), FLY of
+  // them in flight; quad `t` of head column `col`.
+  template <int D, int NT, int FLY>
+  __device__ __forceinline__ void take(const float *first, int n, int i0, int step, int t, int col, int lane) {
+    using Sh = Shape<D, NT>;
+#pragma unroll 1
+    for (int base = i0; base < n; base += FLY * step) {
+      float2 r[FLY], pl[FLY];
+      float4 v[FLY];
+#pragma unroll
+      for (int k = 0; k < FLY; ++k) {
+        const int i = base + k * step;
+        const float *x = first + (i == 0 ? 0 : i * 2 - 1) * static_cast<size_t>(Sh::kPieceFloats);
+        r[k] = i < n ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col) : make_float2(kNoRef, kNoRef);
+        pl[k] = i < n ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + NT * 8 + col) : make_float2(0.f, 0.f);
+        v[k] = i < n ? reinterpret_cast<const float4 *>(x)[t * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float2 M = R;
+#pragma unroll
+      for (int k = 0; k < FLY; ++k) M.x = fmaxf(M.x, r[k].x), M.y = fmaxf(M.y, r[k].y);
+      refer_to(M);
+#pragma unroll
+      for (int k = 0; k < FLY; ++k) add(r[k], pl[k], v[k]);
+    }
+  }
+  // Another thread's share of the same quad, through shared memory.
+  __device__ __forceinline__ void give(float4 *slot) const {
+    slot[0] = o;
+    slot[1] = make_float4(R.x, R.y, l.x, l.y);
+  }
+  __device__ __forceinline__ void get(const float4 *slot) {
+    const float4 x = slot[1];
+    refer_to(make_float2(fmaxf(R.x, x.x), fmaxf(R.y, x.y)));
+    add(make_float2(x.x, x.y), make_float2(x.z, x.w), slot[0]);
+  }
+};
+
+// The run that starts in CTA c and spans more (blockIdx.x = c), by one block:
+// every kSplit-th piece goes to one group of threads, five in flight, and the
+// groups are joined in shared memory.
 template <int D, int NT>
 struct JoinShape {
   static constexpr int kLanes = D * NT * 2;
@@ -881,62 +930,67 @@ struct JoinShape {
 
 template <int D, int NT>
 __global__ void __launch_bounds__(JoinShape<D, NT>::kThreads) join_kernel(const Params p) {
-  using Sh = Shape<D, NT>;
   using J = JoinShape<D, NT>;
-  constexpr int COLS = NT * 8, FLY = 5;
-  __shared__ float4 part[J::kSplit - 1][2][J::kLanes];
+  __shared__ float4 part[J::kSplit - 1][J::kLanes][2];
   grid_launch_dependents();
   const int c0 = blockIdx.x, grp = threadIdx.x / J::kLanes, quad = threadIdx.x % J::kLanes;
-  const int t = quad >> 5, lane = quad & 31, c4 = lane & 3, g4 = lane >> 2;
-  const int md = t / NT, nt = t - md * NT, col = nt * 8 + 2 * c4;
+  const int t = quad >> 5, lane = quad & 31, md = t / NT, col = (t - md * NT) * 8 + 2 * (lane & 3);
   grid_dependency_wait();  // the pieces come from the grid launched just before
   const int4 desc = p.ws_desc[c0];
   if (desc.w == 0) return;
-  const float *first = p.ws + (static_cast<size_t>(c0) * 2 + 1) * Sh::kPieceFloats;
   const int n = desc.z - c0 + 1;
-  float2 R = make_float2(kNoRef, kNoRef), l = make_float2(0.f, 0.f);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // acc := acc 2^(R - M) + piece 2^(r - M)
-  auto scale = [&](const float2 &M) {
-    const float f0 = piece_factor(R.x, M.x), f1 = piece_factor(R.y, M.y);
-    l.x *= f0, l.y *= f1, o.x *= f0, o.y *= f1, o.z *= f0, o.w *= f1;
-    R = M;
-  };
-  auto add = [&](const float2 &r, const float2 &pl, const float4 &v) {
-    const float f0 = piece_factor(r.x, R.x), f1 = piece_factor(r.y, R.y);
-    l.x += pl.x * f0, l.y += pl.y * f1, o.x += v.x * f0, o.y += v.y * f1, o.z += v.z * f0, o.w += v.w * f1;
-  };
-  for (int base = grp; base < n; base += FLY * J::kSplit) {
-    float2 r[FLY], pl[FLY];
-    float4 v[FLY];
-#pragma unroll
-    for (int k = 0; k < FLY; ++k) {
-      const int i = base + k * J::kSplit;
-      const float *x = first + (i == 0 ? 0 : i * 2 - 1) * static_cast<size_t>(Sh::kPieceFloats);
-      r[k] = i < n ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + col) : make_float2(kNoRef, kNoRef);
-      pl[k] = i < n ? *reinterpret_cast<const float2 *>(x + Sh::kTileFloats + COLS + col) : make_float2(0.f, 0.f);
-      v[k] = i < n ? reinterpret_cast<const float4 *>(x)[t * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    float2 M = R;
-#pragma unroll
-    for (int k = 0; k < FLY; ++k) M.x = fmaxf(M.x, r[k].x), M.y = fmaxf(M.y, r[k].y);
-    scale(M);
-#pragma unroll
-    for (int k = 0; k < FLY; ++k) add(r[k], pl[k], v[k]);
-  }
-  if (grp > 0) {
-    part[grp - 1][0][quad] = o;
-    part[grp - 1][1][quad] = make_float4(R.x, R.y, l.x, l.y);
-  }
+  Joined acc;
+  acc.take<D, NT, 5>(p.ws + (static_cast<size_t>(c0) * 2 + 1) * Shape<D, NT>::kPieceFloats, n, grp, J::kSplit, t, col, lane);
+  if (grp > 0) acc.give(part[grp - 1][quad]);
   __syncthreads();
   if (grp > 0) return;
-  for (int k = 1; k < min(n, J::kSplit); ++k) {
-    const float4 x = part[k - 1][1][quad];
-    const float2 r = make_float2(x.x, x.y);
-    scale(make_float2(fmaxf(R.x, r.x), fmaxf(R.y, r.y)));
-    add(r, make_float2(x.z, x.w), part[k - 1][0][quad]);
+  for (int k = 1; k < min(n, J::kSplit); ++k) acc.get(part[k - 1][quad]);
+  store_quad<D>(p, static_cast<uint32_t>(desc.x), col, lane >> 2, md, acc.o, acc.l.x, acc.l.y);
+}
+
+// For few runs, which span many CTAs each: block (x, t) joins quad row t of the
+// x-th run that spans CTAs, every 32nd piece by one warp, three in flight.
+constexpr int kFewWarps = 32;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kFewWarps * 32) join_few_kernel(const Params p, int ctas) {
+  constexpr int kLast = 4;  // warps of the last but one step
+  __shared__ float4 part[kFewWarps][32][2];
+  __shared__ int leaving[kFewWarps], found[3];
+  grid_launch_dependents();
+  const int t = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int md = t / NT, col = (t - md * NT) * 8 + 2 * (lane & 3);
+  if (threadIdx.x == 0) found[0] = -1;
+  grid_dependency_wait();
+  // thread c stands for CTA c: the one whose run is the x-th to leave
+  const int4 d = static_cast<int>(threadIdx.x) < ctas ? p.ws_desc[threadIdx.x] : make_int4(0, 0, 0, 0);
+  const unsigned leaves = __ballot_sync(0xffffffffu, d.w != 0);
+  if (lane == 0) leaving[warp] = __popc(leaves);
+  __syncthreads();
+  if (d.w != 0) {
+    int before = __popc(leaves & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) before += leaving[w];
+    if (before == static_cast<int>(blockIdx.x)) {
+      found[0] = threadIdx.x;
+      found[1] = d.z;
+      found[2] = d.x;
+    }
   }
-  store_quad<D>(p, static_cast<uint32_t>(desc.x), col, g4, md, o, l.x, l.y);
+  __syncthreads();
+  const int c0 = found[0], n = found[1] - c0 + 1;
+  if (c0 < 0) return;
+  Joined acc;
+  acc.take<D, NT, 3>(p.ws + (static_cast<size_t>(c0) * 2 + 1) * Shape<D, NT>::kPieceFloats, n, warp, kFewWarps, t, col, lane);
+  acc.give(part[warp][lane]);
+  __syncthreads();
+  if (warp < kLast) {
+    for (int k = warp + kLast; k < min(n, kFewWarps); k += kLast) acc.get(part[k][lane]);
+    acc.give(part[warp][lane]);
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  for (int k = 1; k < min(n, kLast); ++k) acc.get(part[k][lane]);
+  store_quad<D>(p, static_cast<uint32_t>(found[2]), col, lane >> 2, md, acc.o, acc.l.x, acc.l.y);
 }
 
 // ------------------------------------------------------------------------ host
@@ -1024,7 +1078,15 @@ cudaError_t launch(const CUtensorMap &tmk, const CUtensorMap &tmv, const Params 
   auto k = decode_quant_kernel<D, BS, NT>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmemBytes);
   if (e == cudaSuccess) e = launch_overlapped(k, grid, Sh::kThreads, Sh::kSmemBytes, stream, tmk, tmv, p);
-  if (e == cudaSuccess && p.ws) e = launch_overlapped(join_kernel<D, NT>, grid, JoinShape<D, NT>::kThreads, 0, stream, p);
+  if (e != cudaSuccess || !p.ws) return e;
+  // Runs of eight pieces and more, of which there are few, go to more blocks.
+  // Measured, join_kernel / join_few_kernel: 1 run of 131072 tokens 23.3 / 16.9
+  // us, 2 of 65536 19.8 / 16.7, 8 of 32768 21.0 / 20.3, 16 of 20000 22.2 / 22.1.
+  const long long runs = static_cast<long long>(p.num_seqs) * p.num_kv_heads;
+  if (grid > 8 * runs && grid <= kFewWarps * 32)
+    e = launch_overlapped(join_few_kernel<D, NT>, dim3(static_cast<unsigned>(runs), D / 16 * NT), kFewWarps * 32, 0, stream, p, grid);
+  else
+    e = launch_overlapped(join_kernel<D, NT>, grid, JoinShape<D, NT>::kThreads, 0, stream, p);
   return e;
 }
 

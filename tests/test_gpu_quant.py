@@ -282,6 +282,17 @@ def test_decode_long_and_mixed_lengths(lens, Hq, Hkv, d, bs):
                      d ** -0.5)
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,d,bs", [([60000], 4, 1, 128, 64), ([70001], 12, 1, 128, 128), ([40000, 0, 33001], 2, 1, 64, 16),
+                                              ([50000], 48, 3, 64, 32), ([45000, 1], 21, 3, 128, 16), ([20000], 7, 7, 64, 64)])
+def test_decode_few_long_runs(lens, Hq, Hkv, d, bs):
+    """A run over up to the whole grid: many pieces to join, with one to seven runs."""
+    q, host, tables = decode_case(lens, d, bs, Hq, Hkv, seed=sum(lens) % 997)
+    cache = cache_on_gpu(*host)
+    out = run_decode(q, cache, tables, lens, d ** -0.5)
+    check_decode(out, q, host, tables, lens, d ** -0.5)
+    assert np.array_equal(bits(run_decode(q, cache, tables, lens, d ** -0.5)), bits(out))
+
+
 def test_decode_many_sequences():
     rng = np.random.default_rng(4)
     lens = np.minimum(rng.geometric(0.03, 3000), 200).astype(np.int64)
