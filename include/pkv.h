@@ -579,7 +579,9 @@ int pkv_write_quant(const pkv_bf16 *k, const pkv_bf16 *v, int64_t k_stride, int6
  * be listed any number of times.  Rows of negative slots are not written;
  * slots >= num_blocks * block_size set PKV_STATUS_BAD_SLOT and their rows are
  * not written.
- *   k, v          device, [num_tokens][num_kv_heads][head_dim] bf16 (written)
+ *   k, v          device, [num_tokens][num_kv_heads][head_dim] bf16, 16-byte
+ *                 aligned (written)
+ *   the four cache arrays as above (read; code arrays 16-byte aligned)
  * Exponent bytes outside [96, 158] (a slot that was never written) count as the
  * nearer bound.  Sizes as pkv_write_quant.
  */
@@ -608,7 +610,9 @@ size_t paged_attention_decode_quant_workspace_size(int num_seqs, int num_q_heads
  *   out[i][0][g][:] = sum_{t < L} softmax_t(scale * q[i][0][g] . k_t) v_t,
  * rounded to bf16 (nearest even); L = 0 gives zeros.  The newest token's rows
  * are in the cache already (pkv_write_quant before this call).
- *   q, out        device, [num_seqs][1][num_q_heads][head_dim] bf16
+ *   q, out        device, [num_seqs][1][num_q_heads][head_dim] bf16, 16-byte
+ *                 aligned (read; written)
+ *   the four cache arrays as above (read; all 16-byte aligned)
  *   block_tables, max_blocks_per_seq, seq_lens, max_seq_len, d_status: as
  *                 paged_attention_decode (table entries past a sequence's
  *                 blocks may hold anything).  max_seq_len picks the schedule
@@ -627,7 +631,8 @@ size_t paged_attention_decode_quant_workspace_size(int num_seqs, int num_q_heads
  * Supported: head_dim in {64, 128}; block_size in {16, 32, 64, 128};
  *   num_q_heads / num_kv_heads <= 16; num_seqs and num_kv_heads <= 65535;
  *   num_seqs * num_kv_heads * head_dim * (the longest sequence that max_seq_len
- *   and the tables allow) below 2^43.
+ *   and the tables allow) below 2^43; the cache's rows (num_blocks *
+ *   num_kv_heads * block_size) below 2^31 - 512.
  *   Other sizes return PKV_ERR_UNSUPPORTED.
  */
 int paged_attention_decode_quant(const pkv_bf16 *q, const uint8_t *k_codes, const uint8_t *v_codes,

@@ -19,13 +19,14 @@
 // at 64) and laid end to end; every warp of a grid of one CTA per SM takes an
 // equal, contiguous range of units (short batches: make_plan).  The lengths'
 // prefix sums are taken by every CTA at its start, so there is no host-built
-// list and a captured graph follows its lengths.  A warp streams its units through a ring of its own (TMA with the
-// 128-byte swizzle for the codes, cp.async for the exponents, one mbarrier per
-// stage) and refills a stage right after it has used it: no barrier between
-// warps until the end.  A run that a warp holds whole is written at once; pieces
-// of a run are joined in shared memory at the CTA's end, and runs that span
-// CTAs through the workspace by a second kernel.  Joins follow the order of the
-// keys: results repeat bit for bit.
+// list and a captured graph follows its lengths.  A warp streams its units
+// through a ring of its own (TMA with the 128-byte swizzle for the codes,
+// cp.async for the exponents, one mbarrier per stage) and refills a stage right
+// after it has used it: no barrier between warps until the end.  A run that a
+// warp holds whole is written at once; pieces of a run are joined in shared
+// memory at the CTA's end, and runs that span CTAs through the workspace by a
+// second kernel.  Joins take the pieces in an order that the sizes fix: results
+// repeat bit for bit.
 //
 // Measured (both kernels, back to back in a graph): 16 x 32768 tokens, 64 q / 8
 // KV heads of 128, block 32: 173 us, 6.3 TB/s of 6.78 for a plain copy; 256

@@ -157,9 +157,11 @@ __device__ __forceinline__ void store16(uint4 *dst, const uint4 &a, const uint4 
 // 16 c + 15 of the key row and of the value row.  Eight CTAs an SM (32 registers
 // a thread) keep most loads in flight.  At 262144 row pairs of 128 values:
 // 31.2 us; with 40 registers 36.9; two row pairs per thread (63) 34.5; keys and
-// values by different threads 37.7.
+// values by different threads 37.7.  (No __restrict__ on the inputs: the kernel
+// just before may still be writing them when this one becomes resident, so they
+// are not read-only for this kernel's whole life.)
 template <int W, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 8) write_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
+__global__ void __launch_bounds__(kThreads, 8) write_kernel(const uint4 *k, const uint4 *v,
                                                             const RowParams p, const CachePtrs out) {
   // the grid queued behind this one may become resident now (it waits for this
   // grid's writes before it reads the cache)

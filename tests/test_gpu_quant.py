@@ -558,6 +558,44 @@ def test_back_to_back_calls_over_one_workspace():
         check_decode(o, q, host, tables, lens, s)
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv", [([30000], 8, 1), ([9000, 7000], 16, 2), ([700, 2300, 1500, 3000, 40, 900], 16, 8)])
+def test_a_chain_of_calls_hands_its_data_on(lens, Hq, Hkv):
+    """Calls queued without a gap, each reading what the one before wrote (a query from an output, a row
+    from a read-back) or a workspace that the one before used: the same bits as one call at a time."""
+    d, bs, B = 128, 16, len(lens)
+    q, host, tables = decode_case(lens, d, bs, Hq, Hkv, seed=77)
+    cache = cache_on_gpu(*host)
+    t, n = dev(tables, torch.int32), dev(lens, torch.int32)
+    ws = workspace_for(B, Hq, Hkv, d, max(lens))
+    last = dev(np.array([tables[i, (L - 1) // bs] * bs + (L - 1) % bs for i, L in enumerate(lens)]), torch.int64)
+    first = dev(np.array([tables[i, 0] * bs for i in range(B)]), torch.int64)
+    k, v = (torch.zeros((B, Hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    a, b = torch.empty_like(q), torch.empty_like(q)
+
+    def chain(wait):
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        c = [x.clone() for x in cache]
+        x, outs = q.clone(), []
+        torch.cuda.synchronize()
+        for i in range(6):
+            for src, dst in ((x, a), (a, b), (b, x)):  # every buffer is read, written and read again
+                native.paged_attention_decode_quant(src, *c, t, n, max(lens), 0.3, dst, ws)
+                pause()
+            native.pkv_read_quant(*c, first if i % 2 else last, k, v)
+            pause()
+            native.pkv_write_quant(k, v, last if i % 2 else first, *c)
+            pause()
+            if i % 3 == 2:
+                outs.append(x.clone())
+        torch.cuda.synchronize()
+        return outs + [a.clone(), b.clone()] + c
+
+    want = chain(True)
+    for _ in range(5):
+        for g, w in zip(chain(False), want):
+            assert torch.equal(g.view(torch.uint8), w.view(torch.uint8))
+
+
 # ---------------------------------------------------------- the three together
 def as_bf16_blocks(codes, exps):
     """The byte arrays as pkv_block_copy and the swaps take them (include/pkv.h)."""
