@@ -624,7 +624,8 @@ size_t paged_attention_decode_quant_workspace_size(int num_seqs, int num_q_heads
  *                 initialised and are not preserved.  Calls that may overlap
  *                 on the GPU need a workspace each.
  * Slots past a sequence's end never contribute, whatever bytes they hold.  A
- * NaN stored at a visible key or value makes the outputs that use it NaN.
+ * NaN stored at a visible key or value makes the outputs that use it NaN, and
+ * so does a query value that is not finite (its head's outputs).
  * Block ids outside [0, num_blocks) set PKV_STATUS_BAD_BLOCK; the block's keys
  * and values read as zeros.  Exponent bytes outside [96, 158] (which
  * pkv_write_quant never stores) count as the nearer bound.

@@ -376,13 +376,15 @@ __device__ __forceinline__ void attend_tokens(Acc<D, NT> &acc, const uint32_t (&
 }
 
 // Values g D/8 + 2 md and + 1 of heads col and col + 1 from their joined accumulators.
+// A run has a key at least and its largest weight is not lost, so a sum of 0 means
+// scores of -inf throughout (an infinite query): 0 / 0, as the formula has it.
 template <int D>
 __device__ __forceinline__ void store_quad(const Params &p, uint32_t run, int col, int g4, int md, const float4 &o,
                                            float l0, float l1) {
   const size_t seq = run & 0xFFFFu, h = run >> 16;
   uint32_t *row = reinterpret_cast<uint32_t *>(p.out + (seq * p.num_q_heads + h * p.group + col) * D + g4 * (D / 8) +
                                                2 * md);
-  const float i0 = l0 == 0.f ? 0.f : 1.f / l0, i1 = l1 == 0.f ? 0.f : 1.f / l1;
+  const float i0 = 1.f / l0, i1 = 1.f / l1;
   if (col < p.group) row[0] = pack_bf16x2(o.x * i0, o.z * i0);
   if (col + 1 < p.group) row[D / 2] = pack_bf16x2(o.y * i1, o.w * i1);
 }
@@ -781,7 +783,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             for (int e = 0; e < 2; ++e) {
               const int col = nt * 8 + 2 * c4 + e;
               if (col >= p.group) continue;
-              const float l = acc.l[nt][e], inv = l == 0.f ? 0.f : 1.f / l;
+              const float inv = 1.f / acc.l[nt][e];  // (store_quad)
               uint32_t w[D / 16];
 #pragma unroll
               for (int md = 0; md < D / 16; ++md)

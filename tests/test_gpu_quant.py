@@ -381,6 +381,27 @@ def test_nan_at_a_visible_key_or_value_shows():
     assert not out[2].any()
 
 
+@pytest.mark.parametrize("bound", [40, 5000, 30000])
+def test_infinite_queries_show(bound):
+    """A query head with an infinity has no finite answer, not even where all its scores are -inf
+    (0 / 0); the other heads of its group keep theirs.  The bounds take the three schedules."""
+    lens, bs, d = [1, 40, 33], 16, 64
+    if bound > 40:
+        lens = [1, bound, 700]
+    q, host, tables = decode_case(lens, d, bs, 8, 2, seed=16)
+    q[:, 0, 1, 0] = float("-inf")
+    q[:, 0, 6, 0] = float("inf")
+    host[0][..., 0] = 0x38  # every key's first value is positive
+    got = run_decode(q, cache_on_gpu(*host), tables, lens, 0.125)[:, 0].double().cpu().numpy()
+    assert np.isnan(got[:, [1, 6]]).all()
+    rest = [0, 2, 3, 4, 5, 7]
+    assert np.isfinite(got[:, rest]).all()
+    q[:, 0, [1, 6], 0] = 0.0
+    out = run_decode(q, cache_on_gpu(*host), tables, lens, 0.125)
+    check_decode(out, q, host, tables, lens, 0.125)
+    assert np.array_equal(out[:, 0].double().cpu().numpy()[:, rest], got[:, rest])
+
+
 def test_values_of_every_size():
     """Rows of values 2^62 apart and zero rows, with the weight on any of them: the weights' sum
     must not lose the keys whose values are small."""
