@@ -487,8 +487,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     for (int s = 0; s < S; ++s) mbar_init(full + 8 * s, 1 + EXP_LANES);
     mbar_init_fence();
   }
-  __syncwarp();  // a warp's barriers are its own
-  if (tid < 2 * NW) pieces[tid] = make_uint4(0u, 0u, 0u, 0u);
+  // A warp clears its own two entries: where runs are shared by a CTA's warps
+  // (direct > 1) nothing orders one warp's clearing before another's record.
+  if (lane < 2) pieces[2 * warp + lane] = make_uint4(0u, 0u, 0u, 0u);
+  __syncwarp();  // a warp's barriers and entries are its own
   if (tid == 0) {
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);

@@ -739,3 +739,32 @@ def test_the_largest_batch(top):
     one = lens == 1
     assert np.array_equal(got[one], np.broadcast_to(v[one][:, None], got[one].shape))
     assert not got[lens == 0].any()
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,bs,top", [(128, 8, 2, 16, 350), (128, 4, 1, 32, 700), (64, 6, 3, 16, 1500), (128, 32, 2, 64, 256),
+                                             (64, 16, 1, 128, 640)])
+def test_runs_shared_by_a_ctas_warps_keep_every_piece(d, Hq, Hkv, bs, top):
+    """Small batches whose runs are cut over the warps of one CTA, called many times beside a stream that
+    keeps the SMs' schedulers busy, so that a CTA's warps start far apart: each warp's piece is joined
+    every time (a lost one would leave its tokens out, and no status says so)."""
+    rng = np.random.default_rng(top)
+    lens = [top, 1] + rng.integers(top // 2, top + 1, 4).tolist()
+    q, host, tables = decode_case(lens, d, bs, Hq, Hkv, seed=top + d)
+    assert native.paged_attention_decode_quant_workspace_size(len(lens), Hq, Hkv, d, top) == 0  # no other schedule
+    cache = cache_on_gpu(*host)
+    t, n = dev(tables, torch.int32), dev(lens, torch.int32)
+    want = run_decode(q, cache, tables, lens, d ** -0.5)
+    check_decode(want, q, host, tables, lens, d ** -0.5)
+    busy, side = torch.randn((1 << 20), device="cuda"), torch.cuda.Stream()
+    outs = [torch.full_like(q, float("nan")) for _ in range(300)]
+    st = status_tensor()
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        if i % 2 == 0:
+            with torch.cuda.stream(side):
+                busy.sin_()
+        native.paged_attention_decode_quant(q, *cache, t, n, top, d ** -0.5, out, None, st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    for out in outs:
+        assert np.array_equal(bits(out), bits(want))
