@@ -83,7 +83,7 @@ struct Params {
   int num_seqs;
   // launched right behind a grid whose results this one does not read (the
   // chunk kernel of a mixed step), which waited for our inputs before it let
-  // this grid start: no wait here, so the two grids run side by side
+  // this grid start: its work waits for nothing, so the two grids run side by side
   int skip_dependency_wait;
   // nothing this grid reads is written by the kernels launched before it (the
   // layers of one decode step): it streams at once and waits for them only
@@ -296,6 +296,14 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32)
   grid_launch_dependents();
   // inputs may come from the kernel launched just before
   if (!p.skip_dependency_wait && !p.wait_before_writes) grid_dependency_wait();
+  // A grid that works beside the one before it must not complete before it: the
+  // grids queued behind wait for this one alone and take its end for the end of
+  // everything ahead.  Beside a mixed step's chunks the items may end early, so
+  // the launch adds a CTA behind them that does nothing but wait.
+  if (p.skip_dependency_wait && blockIdx.x + 1 == gridDim.x) {
+    grid_dependency_wait();
+    return;
+  }
   int part, h, seq, L, window0, b0 = -1;
   if (p.items) {
     // a host-built work list: one 16-byte load names this CTA's partition, its
@@ -764,7 +772,9 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 template <int D, int BS>
 int launch(const CUtensorMap &tmk, const CUtensorMap &tmv, const Params &p, int num_seqs, int q_len,
            int grid_items, cudaStream_t stream, cudaEvent_t main_done) {
-  const dim3 grid = p.items ? dim3(grid_items) : dim3(p.max_parts, p.num_kv_heads, num_seqs);
+  // a list beside a mixed step's chunks gets one CTA more, which waits for them (decode_kernel)
+  const dim3 grid = p.items ? dim3(static_cast<unsigned>(grid_items) + (p.skip_dependency_wait ? 1 : 0))
+                            : dim3(p.max_parts, p.num_kv_heads, num_seqs);
   constexpr size_t smem = smem_bytes<D, BS>();
   cudaError_t e;
   if (q_len == 1) {

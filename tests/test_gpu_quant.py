@@ -768,3 +768,144 @@ def test_runs_shared_by_a_ctas_warps_keep_every_piece(d, Hq, Hkv, bs, top):
     assert st.item() == 0
     for out in outs:
         assert np.array_equal(bits(out), bits(want))
+
+
+# ------------------------------------- behind and before the bf16 cache's kernels
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("decodes", ["unsplit", "split", "none listed"])
+def test_calls_behind_a_mixed_step_wait_for_its_chunks(decodes, captured):
+    """paged_attention_mixed with long chunks beside a few short decodes, which end long before, then at
+    once an 8-bit call that reads the chunks' outputs (a decode's queries, a write's rows) or overwrites
+    the queries they read (a read-back): the same bits as with a wait in between."""
+    Hq, Hkv, bs, d, n_dec, C = 32, 8, 16, 128, 8, 4096
+    lens, scale = [60, 200, 1, 17, 33, 128, 90, 150, 8192, 8192], 0.1
+    q_start = dev(np.concatenate([np.arange(n_dec + 1), [n_dec + C, n_dec + 2 * C]]), torch.int32)
+    rng = np.random.default_rng(3)
+    NB = sum(inputs.entries_to_fill(n, bs) for n in lens) + 3
+    tables, _ = inputs.permuted_tables(lens, bs, NB, rng, max_blocks=8192 // bs + 2)
+    kc, vc = (inputs.randn_bf16((NB, Hkv, bs, d), 90 + i, "cuda") for i in range(2))
+    rows = n_dec + 2 * C
+    q0 = inputs.randn_bf16((rows, Hq, d), 92, "cuda")
+    part = 256 if decodes != "split" else 64
+    items = native.pkv_decode_items(np.asarray(lens[:n_dec], dtype=np.int32), tables[:n_dec], Hkv, bs, part, d)
+    if decodes == "none listed":
+        items = np.zeros_like(items)
+    items, t, n = torch.as_tensor(items, device="cuda"), dev(tables, torch.int32), dev(lens, torch.int32)
+    ws = torch.empty(max(16, native.paged_attention_workspace_size(n_dec, 1, Hq, d, 200, part)), dtype=torch.uint8,
+                     device="cuda")
+    # the 8-bit side: a batch of 64 short sequences, whose queries are outputs of the last chunk
+    low = [9 + i % 50 for i in range(64)]
+    _, host, low_tables = decode_case(low, d, bs, Hq, Hkv, seed=93)
+    cache = cache_on_gpu(*host)
+    lt, ln = dev(low_tables, torch.int32), dev(low, torch.int32)
+    slots = dev([low_tables[i, 0] * bs + i % 9 for i in range(64)], torch.int64)
+    many = dev(rng.integers(0, host[0].shape[0] * bs, rows * Hq // Hkv // 2), torch.int64)  # half of q's bytes each
+    q, out = q0.clone(), torch.empty_like(q0)
+    res = torch.empty((64, 1, Hq, d), dtype=torch.bfloat16, device="cuda")
+    st = status_tensor()
+
+    def mixed():
+        native.paged_attention_mixed(q, kc, vc, t, n, q_start, scale, out, n_dec, items, 200, part, ws, 100, d_status=st)
+
+    def reads():
+        native.paged_attention_decode_quant(out[-64:].unsqueeze(1), *cache, lt, ln, 64, scale, res, None, st)
+
+    def overwrites():
+        rows_of_q = q.view(-1, Hkv, d)
+        native.pkv_read_quant(*cache, many, rows_of_q[:len(many)], rows_of_q[len(many):], st)
+
+    def writes():
+        native.pkv_write_quant(out[-64:, :Hkv], out[-64:, Hkv:2 * Hkv], slots, *cache, st)
+
+    def state():
+        return [x.clone() for x in (q, out, res, *cache)]
+
+    def restore(saved):
+        for x, s in zip((q, out, res, *cache), saved):
+            x.copy_(s)
+        torch.cuda.synchronize()
+
+    out.fill_(float("nan"))
+    res.fill_(float("nan"))
+    start = state()
+    for calls in ([overwrites], [reads, overwrites], [writes, reads], [reads, writes, overwrites]):
+        restore(start)
+        mixed()
+        torch.cuda.synchronize()
+        for f in calls:
+            f()
+            torch.cuda.synchronize()
+        want = state()
+        assert want[1][n_dec:].isfinite().all()
+        restore(start)
+        if captured:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                mixed()
+                for f in calls:
+                    f()
+        for _ in range(3):
+            restore(start)
+            if captured:
+                g.replay()
+            else:
+                mixed()
+                for f in calls:
+                    f()
+            torch.cuda.synchronize()
+            for got, w in zip(state(), want):
+                assert torch.equal(got.view(torch.uint8), w.view(torch.uint8))
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 16, 2), (64, 8, 4)])
+def test_a_chain_across_both_caches_hands_its_data_on(d, Hq, Hkv):
+    """Calls of the 8-bit and of the bf16 cache queued without a gap, each reading what the one before
+    wrote (queries from outputs, cache rows from a read-back) or overwriting what it read: the same
+    bits as one call at a time."""
+    lens, bs, scale, C = [900, 40, 2500], 16, 0.2, 24
+    q, host, tables = decode_case(lens, d, bs, Hq, Hkv, seed=78)
+    cache = cache_on_gpu(*host)
+    NB, B = host[0].shape[0], len(lens)
+    kc, vc = (inputs.randn_bf16((NB, Hkv, bs, d), 95 + i, "cuda") for i in range(2))
+    t, n = dev(tables, torch.int32), dev(lens, torch.int32)
+    ws8 = workspace_for(B, Hq, Hkv, d, max(lens))
+    ws = torch.empty(native.paged_attention_workspace_size(B, 1, Hq, d, max(lens), 256), dtype=torch.uint8, device="cuda")
+    last = dev([tables[i, (L - 1) // bs] * bs + (L - 1) % bs for i, L in enumerate(lens)], torch.int64)
+    all_slots = dev(np.arange(NB * bs), torch.int64)
+    q_start = dev([0, C, 2 * C, 3 * C], torch.int32)
+    k, v = (torch.zeros((NB * bs, Hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    chunk, chunk_out = (torch.zeros((3 * C, Hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def chain(wait):
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        c, pool = [x.clone() for x in cache], [kc.clone(), vc.clone()]
+        x, rows = q.clone(), inputs.randn_bf16(chunk.shape, 97, "cuda")
+        torch.cuda.synchronize()
+        for i in range(4):
+            native.paged_attention_decode_quant(x, *c, t, n, max(lens), scale, a, ws8)
+            pause()
+            native.paged_attention_decode(a, *pool, t, n, max(lens), scale, b, ws, 256)
+            pause()
+            native.paged_attention_decode_quant(b, *c, t, n, max(lens), scale, x, ws8)
+            pause()
+            native.paged_attention_prefill(rows, *pool, t, n, q_start, scale, chunk_out)
+            pause()
+            native.pkv_write_quant(chunk_out[:B, :Hkv], chunk_out[C:C + B, :Hkv], last, *c)
+            pause()
+            native.pkv_read_quant(*c, all_slots, k, v)
+            pause()
+            # the read-back rows as a bf16 pool of blocks of one head, and as a chunk's queries
+            native.paged_attention_prefill(k.view(-1, Hq, d)[:3 * C], *pool, t, n, q_start, scale, rows)
+            pause()
+            native.pkv_write(k, v, all_slots, *pool)
+            pause()
+        torch.cuda.synchronize()
+        return [a.clone(), b.clone(), x, chunk_out.clone(), rows, k.clone(), v.clone()] + c + pool
+
+    want = chain(True)
+    assert all(torch.isfinite(w.float()).all() for w in want[:7])
+    for _ in range(4):
+        for g, w in zip(chain(False), want):
+            assert torch.equal(g.view(torch.uint8), w.view(torch.uint8))
