@@ -299,23 +299,28 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32)
   // A grid that works beside the one before it must not complete before it: the
   // grids queued behind wait for this one alone and take its end for the end of
   // everything ahead.  Beside a mixed step's chunks the items may end early, so
-  // the launch adds a CTA behind them that does nothing but wait.
+  // the launch adds a CTA behind them that does nothing but wait.  Where the CTAs
+  // wait before they write, one that has nothing to write waits too (the first:
+  // there may be no other).
   if (p.skip_dependency_wait && blockIdx.x + 1 == gridDim.x) {
     grid_dependency_wait();
     return;
   }
+  auto nothing_to_write = [&] {
+    if (p.wait_before_writes && blockIdx.x == 0) grid_dependency_wait();
+  };
   int part, h, seq, L, window0, b0 = -1;
   if (p.items) {
     // a host-built work list: one 16-byte load names this CTA's partition, its
     // length and its first block, so the first copy needs no other load
     const int4 it = p.items[1 + blockIdx.x];
-    if (static_cast<int>(blockIdx.x) >= p.items[0].x) return;  // past the list (a grid sized for a bound)
+    if (static_cast<int>(blockIdx.x) >= p.items[0].x) return nothing_to_write();  // past the list (a grid sized for a bound)
     seq = it.x;
     h = it.y & 0xffff;
     part = static_cast<int>(static_cast<unsigned>(it.y) >> 16);
     if (seq < 0 || seq >= p.num_seqs || h >= p.num_kv_heads || part >= p.max_parts) {
       if (threadIdx.x == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_ITEM);
-      return;
+      return nothing_to_write();
     }
     window0 = warp == kDecodeWarps ? first_window(p, seq, part, lane) : -1;
     L = clamp_item_len(p, seq, it.z, BS, threadIdx.x == 0);
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32)
   }
   const int part_tokens = p.part_blocks * BS;
   const int nparts = L > 0 ? (L + part_tokens - 1) / part_tokens : 1;
-  if (part >= nparts) return;
+  if (part >= nparts) return nothing_to_write();
   const int blk0 = part * p.part_blocks;
   const int tok0 = blk0 * BS;  // first key of the partition
   const int ntok = max(0, min(L, tok0 + p.part_blocks * BS) - tok0);
@@ -453,8 +458,8 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32)
           so[(warp * COLS + nt * 8 + 2 * c4 + (i & 1)) * DP + md * 16 + g4 + (i >> 1) * 8] = acc.o[md][nt][i];
   }
   __syncthreads();
-  if (*abort_flag) return;
   if (p.wait_before_writes && !p.skip_dependency_wait) grid_dependency_wait();
+  if (*abort_flag) return;
 
   const int rows = p.num_q_heads;  // q_len == 1
   for (int idx = threadIdx.x; idx < p.group * D; idx += blockDim.x) {

@@ -909,3 +909,56 @@ def test_a_chain_across_both_caches_hands_its_data_on(d, Hq, Hkv):
     for _ in range(4):
         for g, w in zip(chain(False), want):
             assert torch.equal(g.view(torch.uint8), w.view(torch.uint8))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_an_overlapped_decode_without_items_wait_for_the_work_ahead(captured):
+    """A long prefill, an overlapped list decode whose list names nothing (a graph's bound on an idle
+    step), then a read-back over the queries that the prefill reads: the same bits as with waits."""
+    Hq, Hkv, bs, d, C = 32, 8, 16, 128, 4096
+    NB = 2 * C // bs
+    kc, vc, q0 = (inputs.randn_bf16(shape, 99 + i, "cuda") for i, shape in
+                  enumerate([(NB, Hkv, bs, d), (NB, Hkv, bs, d), (C, Hq, d)]))
+    table, n, q_start = dev([np.arange(NB)], torch.int32), dev([2 * C], torch.int32), dev([0, C], torch.int32)
+    dq = inputs.randn_bf16((4, 1, Hq, d), 103, "cuda")
+    tables4, lens4 = dev(np.arange(32).reshape(4, 8), torch.int32), dev([40, 1, 128, 77], torch.int32)
+    items = torch.zeros((1 + 4 * Hkv, 4), dtype=torch.int32, device="cuda")
+    dout = torch.full_like(dq, 3.0)
+    host = random_cache(40, Hkv, bs, d, np.random.default_rng(5))
+    cache = cache_on_gpu(*host)
+    many = dev(np.random.default_rng(6).integers(0, 40 * bs, C * Hq // Hkv // 2), torch.int64)
+    q, out, st = q0.clone(), torch.empty_like(q0), status_tensor()
+
+    def run(pause):
+        native.paged_attention_prefill(q, kc, vc, table, n, q_start, 0.1, out, st)
+        pause()
+        native.paged_attention_decode_items(dq, None, None, None, kc, vc, tables4, lens4, 128, 0.1, dout, items,
+                                            partition_size=128, d_status=st, overlap=True)
+        pause()
+        rows = q.view(-1, Hkv, d)
+        native.pkv_read_quant(*cache, many, rows[:len(many)], rows[len(many):], st)
+        pause()
+
+    def restore():
+        q.copy_(q0)
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+
+    restore()
+    run(torch.cuda.synchronize)
+    want = [q.clone(), out.clone()]
+    assert want[1].isfinite().all()
+    restore()
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(lambda: None)
+    for _ in range(4):
+        restore()
+        if captured:
+            g.replay()
+        else:
+            run(lambda: None)
+        torch.cuda.synchronize()
+        assert all(np.array_equal(bits(a), bits(b)) for a, b in zip((q, out), want))
+    assert (dout == 3.0).all() and st.item() == 0
