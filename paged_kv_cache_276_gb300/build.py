@@ -1,12 +1,15 @@
 """Build the native library libpkv.so (CUDA kernels for sm_103a + host allocator)
-and _bind.so, the Python entry of its shortest calls.
+and the extension _bind.so, the Python entry of its shortest calls.
 
 Usage: python -m paged_kv_cache_276_gb300.build [--force]
 
 Translation units are compiled in parallel with nvcc, then linked into
 ``paged_kv_cache_276_gb300/_build/libpkv.so`` (in-tree, git-ignored).  The CUDA
 runtime is linked statically, so the library only needs the driver at run time.
-_bind.so is a Python extension beside it, over PyTorch's C++ tensors.
+The extension beside it is compiled against Python's and a CUDA PyTorch's C++
+headers, which the library does not need: where they are missing the library is
+built all the same, with a warning, and the calls that go through the extension
+raise.
 """
 from __future__ import annotations
 
@@ -16,6 +19,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -46,11 +50,12 @@ def _deps():
     return files
 
 
+def _fresh(path: str) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in _deps())
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return _fresh(LIB) and _fresh(BIND)
 
 
 def _compile(src: str) -> str:
@@ -82,25 +87,40 @@ def _compile_bind() -> str:
 
 
 def _link_bind(obj: str):
-    tmp = BIND + f".tmp{os.getpid()}"
+    path = BIND
+    tmp = path + f".tmp{os.getpid()}"
     subprocess.run(["g++", "-shared", obj, "-o", tmp, "-L", BUILD, "-l:libpkv.so", "-Wl,-rpath,$ORIGIN",
                     "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
                    check=True)
-    os.replace(tmp, BIND)
+    os.replace(tmp, path)
+
+
+_bind_failed = False  # not tried again in this process
 
 
 def build(force: bool = False) -> str:
-    if not force and up_to_date():
+    """Build what is missing or older than its sources; returns the library's path.  The library comes
+    first: an extension that cannot be built costs a warning, not the library."""
+    global _bind_failed
+    lib_due = force or not _fresh(LIB)
+    bind_due = force or lib_due or not (_bind_failed or _fresh(BIND))
+    if not lib_due and not bind_due:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        bind = ex.submit(_compile_bind)
-        objs = list(ex.map(_compile, SOURCES))
-        bind_obj = bind.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    subprocess.run([nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "static"], check=True)
-    os.replace(tmp, LIB)
-    _link_bind(bind_obj)
+        bind = ex.submit(_compile_bind) if bind_due else None
+        objs = list(ex.map(_compile, SOURCES)) if lib_due else []
+    if lib_due:
+        tmp = LIB + f".tmp{os.getpid()}"
+        subprocess.run([nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "static"], check=True)
+        os.replace(tmp, LIB)
+    if bind_due:
+        try:
+            _link_bind(bind.result())
+            _bind_failed = False
+        except (OSError, RuntimeError, subprocess.CalledProcessError) as e:
+            _bind_failed = True
+            warnings.warn(f"{LIB} is built, but not its Python extension, which the 8-bit cache's calls need: {e}")
     return LIB
 
 

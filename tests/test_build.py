@@ -1,0 +1,42 @@
+"""The build on the CPU: the library does not hang on its Python extension."""
+import os
+import subprocess
+
+import pytest
+
+from paged_kv_cache_276_gb300 import build, native
+
+
+@pytest.fixture
+def scratch(tmp_path, monkeypatch):
+    """A build folder of its own, in which every source compiles to an empty object."""
+    def empty_object(src):
+        obj = str(tmp_path / (src + ".o"))
+        subprocess.run(["g++", "-c", "-x", "c++", "-fPIC", "/dev/null", "-o", obj], check=True)
+        return obj
+
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libpkv.so"))
+    monkeypatch.setattr(build, "_compile", empty_object)
+    return tmp_path
+
+
+@pytest.mark.parametrize("error", [subprocess.CalledProcessError(1, "g++"), FileNotFoundError("g++"), RuntimeError("nvcc")])
+def test_the_library_is_built_where_the_extension_cannot_be(scratch, monkeypatch, error):
+    calls = []
+
+    def no_headers():
+        calls.append(1)
+        raise error
+
+    monkeypatch.setattr(build, "_compile_bind", no_headers)
+    monkeypatch.setattr(build, "BIND", str(scratch / "_bind.so"))
+    monkeypatch.setattr(native, "BIND_PATH", build.BIND)
+    monkeypatch.setattr(build, "_bind_failed", False)
+    with pytest.warns(UserWarning, match="Python extension"):
+        assert build.build() == build.LIB
+    assert os.path.exists(build.LIB) and not os.path.exists(build.BIND)
+    assert build.build() == build.LIB and len(calls) == 1  # one try in a process
+    monkeypatch.setattr(native, "_bind_module", None)
+    with pytest.raises(RuntimeError, match="is missing"):
+        native._bind()
