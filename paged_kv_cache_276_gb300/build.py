@@ -1,5 +1,5 @@
 """Build the native library libpkv.so (CUDA kernels for sm_103a + host allocator)
-and the extension _bind.so, the Python entry of its shortest calls.
+and the extension _bind-*.so, the Python entry of its shortest calls.
 
 Usage: python -m paged_kv_cache_276_gb300.build [--force]
 
@@ -9,7 +9,8 @@ runtime is linked statically, so the library only needs the driver at run time.
 The extension beside it is compiled against Python's and a CUDA PyTorch's C++
 headers, which the library does not need: where they are missing the library is
 built all the same, with a warning, and the calls that go through the extension
-raise.
+raise.  Its file name carries the PyTorch and Python that it was built for
+(native.bind_path), so another one's is never loaded.
 """
 from __future__ import annotations
 
@@ -21,13 +22,14 @@ import sys
 import sysconfig
 import warnings
 
+from . import native
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
-BIND = os.path.join(BUILD, "_bind.so")
 
 SOURCES = ["decode.cu", "chunk_tc.cu", "cache_ops.cu", "quant_ops.cu", "decode_quant.cu", "alloc.cpp", "step.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -55,7 +57,7 @@ def _fresh(path: str) -> bool:
 
 
 def up_to_date() -> bool:
-    return _fresh(LIB) and _fresh(BIND)
+    return _fresh(LIB) and _fresh(native.bind_path())
 
 
 def _compile(src: str) -> str:
@@ -87,7 +89,7 @@ def _compile_bind() -> str:
 
 
 def _link_bind(obj: str):
-    path = BIND
+    path = native.bind_path()
     tmp = path + f".tmp{os.getpid()}"
     subprocess.run(["g++", "-shared", obj, "-o", tmp, "-L", BUILD, "-l:libpkv.so", "-Wl,-rpath,$ORIGIN",
                     "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
@@ -103,7 +105,7 @@ def build(force: bool = False) -> str:
     first: an extension that cannot be built costs a warning, not the library."""
     global _bind_failed
     lib_due = force or not _fresh(LIB)
-    bind_due = force or lib_due or not (_bind_failed or _fresh(BIND))
+    bind_due = force or lib_due or not (_bind_failed or _fresh(native.bind_path()))
     if not lib_due and not bind_due:
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -1,6 +1,6 @@
 """ctypes binding of libpkv.so: the C ABI declared in include/pkv.h, one Python
 function per C entry point with the same name (the 8-bit cache's calls go through
-a small extension, _bind.so, for their host time).
+a small extension, _bind-*.so, for their host time).
 
 Argument marshalling only: shapes are read off the tensors, pointers and the
 current CUDA stream are passed through, return codes become exceptions.  Every
@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import sysconfig
 import threading
 
 import torch
@@ -519,13 +520,17 @@ def paged_attention_decode_static_scratch(q, k_cache, v_cache, block_tables, seq
 
 # ------------------------------------------------------- the cache in 8 bits
 # These calls take less time on the GPU than a marshalling through ctypes takes
-# on the host, so they go through _bind.so, which checks the tensors and calls
+# on the host, so they go through an extension (bind.cpp), which checks the tensors and calls
 # the C ABI.  It answers _RECHECK for arguments that the call does not take;
 # they are then gone through here for the message.
 _BF16, _F8, _U8, _I32, _I64 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64
 _RECHECK = 1
-BIND_PATH = os.path.join(_HERE, "_build", "_bind.so")
 _bind_module = None
+
+
+def bind_path():
+    """The extension's file.  It uses PyTorch's C++ tensors and CPython's ABI: its name carries both versions."""
+    return os.path.join(_HERE, "_build", f"_bind-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _bind():
@@ -535,10 +540,11 @@ def _bind():
         lib()
         with _lock:
             if _bind_module is None:
-                if not os.path.exists(BIND_PATH):
+                path = bind_path()
+                if not os.path.exists(path):
                     raise RuntimeError(
-                        f"{BIND_PATH} is missing: build it with `python -m paged_kv_cache_276_gb300.build`")
-                spec = importlib.util.spec_from_file_location(f"{__package__}._bind", BIND_PATH)
+                        f"{path} is missing: build it with `python -m paged_kv_cache_276_gb300.build`")
+                spec = importlib.util.spec_from_file_location(f"{__package__}._bind", path)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)
                 _bind_module = module

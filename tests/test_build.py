@@ -1,8 +1,11 @@
-"""The build on the CPU: the library does not hang on its Python extension."""
+"""The build on the CPU: the library does not hang on its Python extension, and an
+extension of another PyTorch or Python is neither kept nor loaded."""
 import os
 import subprocess
+import sysconfig
 
 import pytest
+import torch
 
 from paged_kv_cache_276_gb300 import build, native
 
@@ -30,13 +33,27 @@ def test_the_library_is_built_where_the_extension_cannot_be(scratch, monkeypatch
         raise error
 
     monkeypatch.setattr(build, "_compile_bind", no_headers)
-    monkeypatch.setattr(build, "BIND", str(scratch / "_bind.so"))
-    monkeypatch.setattr(native, "BIND_PATH", build.BIND)
+    monkeypatch.setattr(native, "bind_path", lambda: str(scratch / "_bind.so"))
     monkeypatch.setattr(build, "_bind_failed", False)
     with pytest.warns(UserWarning, match="Python extension"):
         assert build.build() == build.LIB
-    assert os.path.exists(build.LIB) and not os.path.exists(build.BIND)
+    assert os.path.exists(build.LIB) and not os.path.exists(native.bind_path())
     assert build.build() == build.LIB and len(calls) == 1  # one try in a process
     monkeypatch.setattr(native, "_bind_module", None)
     with pytest.raises(RuntimeError, match="is missing"):
         native._bind()
+
+
+def test_an_extension_of_another_torch_or_python_does_not_count(monkeypatch):
+    build.build()
+    assert build.up_to_date()
+    monkeypatch.setattr(native, "_bind_module", None)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1+other")
+        assert not build.up_to_date()
+        with pytest.raises(RuntimeError, match="is missing"):
+            native._bind()
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: ".cpython-300-other.so")
+        assert not build.up_to_date()
+    assert build.up_to_date() and native._bind() is not None
