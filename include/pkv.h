@@ -593,9 +593,14 @@ int pkv_read_quant(const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t
 /*
  * Bytes of device workspace paged_attention_decode_quant needs for these sizes
  * (0: none; also for invalid sizes, so check the decode call's return code).
- * It depends on the sequences' number and longest length only through how many
- * CTAs they can keep busy.  The library asks the current device for its number
- * of SMs.
+ * The size picks the schedule with them: batches whose runs (a sequence's keys
+ * of one KV head) are not split between CTAs need none, and one sequence or one
+ * token more can take the need from 0 to the full size (two pieces per CTA: on
+ * 152 SMs 1.3 MB at head_dim 128 with up to 8 query heads per KV head, 2.5 MB
+ * with more, half that at head_dim 64).  It never shrinks as num_seqs or max_seq_len grows, so a
+ * buffer that serves several batches is sized for the largest num_seqs and
+ * max_seq_len that will be passed.  The number of SMs is taken once in a process,
+ * from the device that is current at the first call that needs it.
  */
 size_t paged_attention_decode_quant_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
                                                    int head_dim, int max_seq_len);
@@ -623,9 +628,17 @@ size_t paged_attention_decode_quant_workspace_size(int num_seqs, int num_q_heads
  *                 be NULL when that is 0); its contents need not be
  *                 initialised and are not preserved.  Calls that may overlap
  *                 on the GPU need a workspace each.
+ * Scores and sums are held in fp32.  For its product with the values a weight
+ * (times its value row's scale) is rounded to fp16: by 2^-11 of itself at most,
+ * or by 2^-32 of the largest where it is 2^21 times smaller and more; the sum of
+ * the weights takes them unrounded.  An output can so differ in its last bf16
+ * place from one over fp32 weights (paged_attention_decode rounds its weights to
+ * bf16).
  * Slots past a sequence's end never contribute, whatever bytes they hold.  A
  * NaN stored at a visible key or value makes the outputs that use it NaN, and
- * so does a query value that is not finite (its head's outputs).
+ * so does a query value that is not finite (its head's outputs), also where all
+ * the head's scores are -inf: 0 / 0, for which paged_attention_decode answers
+ * zeros.
  * Block ids outside [0, num_blocks) set PKV_STATUS_BAD_BLOCK; the block's keys
  * and values read as zeros.  Exponent bytes outside [96, 158] (which
  * pkv_write_quant never stores) count as the nearer bound.

@@ -139,6 +139,21 @@ def test_workspace_size_of_invalid_sizes_is_zero(native):
         assert f(*bad) == 0, bad
 
 
+def test_workspace_size_never_shrinks_and_may_jump(native):
+    """A buffer sized for the largest batch and bound serves every smaller one; one sequence or token
+    more may take the need from none to the full size."""
+    f = native.paged_attention_decode_quant_workspace_size
+    batches = [1, 2, 7, 18, 19, 20, 21, 76, 77, 152, 153, 154, 400, 1672, 1673, 13000, 13377, 65535]
+    bounds = [0, 1, 32, 33, 64, 65, 128, 129, 350, 352, 353, 384, 385, 704, 705, 768, 769, 1536, 1537, 5000, 100000]
+    for d, Hkv, G in [(128, 8, 4), (128, 1, 8), (128, 2, 16), (64, 3, 1), (64, 4, 12), (64, 16, 8)]:
+        size = np.array([[f(b, Hkv * G, Hkv, d, n) for n in bounds] for b in batches], dtype=np.int64)
+        assert (np.diff(size, axis=0) >= 0).all() and (np.diff(size, axis=1) >= 0).all()
+        assert size[0, 0] == 0
+    assert f(400, 32, 8, 128, 352) == 0 and f(400, 32, 8, 128, 353) > 1 << 20
+    assert f(152, 8, 1, 128, 704) == 0 and f(153, 8, 1, 128, 704) > 0
+    assert f(400, 32, 8, 128, 9000) < 1.3e6 < 2.5e6 < f(400, 128, 8, 128, 9000) < 2.6e6
+
+
 def cpu_cache(NB=4, Hkv=2, bs=16, d=64):
     c = lambda: torch.zeros((NB, Hkv, bs, d), dtype=torch.uint8).view(torch.float8_e4m3fn)  # noqa: E731
     e = lambda: torch.zeros((NB, Hkv, bs), dtype=torch.uint8)  # noqa: E731
