@@ -962,3 +962,41 @@ def test_calls_behind_an_overlapped_decode_without_items_wait_for_the_work_ahead
         torch.cuda.synchronize()
         assert all(np.array_equal(bits(a), bits(b)) for a, b in zip((q, out), want))
     assert (dout == 3.0).all() and st.item() == 0
+
+
+# how k and v lie: (elements before the first token's rows, tokens' distance less the rows' width)
+LIES = {"both 32": ((16, 32), (32, 32)), "k on 16, v on 32": ((8, 32), (0, 32)), "k on 32, v on 16": ((0, 32), (24, 32)),
+        "distance of k 8 mod 16": ((0, 24), (16, 32)), "distance of v 8 mod 16": ((16, 32), (0, 40)),
+        "k dense, v apart": (None, (16, 48)), "k apart, v dense": ((0, 64), None), "far apart": ((16, 4096), (0, 160))}
+
+
+@pytest.mark.parametrize("lie", LIES)
+@pytest.mark.parametrize("T,Hkv,d", [(301, 2, 64), (40, 3, 48), (130, 8, 128)])
+def test_write_of_rows_that_lie_differently(T, Hkv, d, lie):
+    """Keys and values in buffers of their own, at other alignments and other distances between tokens:
+    32-byte loads where both allow them, 16-byte ones otherwise, bit for bit the same codes."""
+    rng = np.random.default_rng(T + d + len(lie))
+    bs, width = 16, Hkv * d
+    NB = -(-T // bs) + 2
+    slots = inputs.distinct_slots(T, NB * bs, rng, skip_fraction=0.1)
+    host = random_cache(NB, Hkv, bs, d, rng, fill=0xAB)
+    cache = cache_on_gpu(*[a.copy() for a in host])
+    rows = [awkward_rows(T, Hkv, d, rng) for _ in range(2)]
+    placed = []
+    for b, where in zip(rows, LIES[lie]):
+        if where is None:
+            placed.append(gpu_bf16(b))
+            continue
+        start, more = where
+        buf = torch.full((start + T * (width + more),), float("nan"), dtype=torch.bfloat16, device="cuda")
+        assert buf.data_ptr() % 32 == 0
+        t = buf[start:].view(T, width + more)[:, :width].view(T, Hkv, d)
+        t.copy_(gpu_bf16(b))
+        assert t.stride(0) == width + more and t.data_ptr() % 32 == (16 if start % 16 else 0)
+        placed.append(t)
+    OQ.write(*rows, slots, *host)
+    st = status_tensor()
+    native.pkv_write_quant(*placed, dev(slots, torch.int64), *cache, st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    assert all(np.array_equal(u8(got), want) for got, want in zip(cache, host))
