@@ -129,8 +129,8 @@ __device__ __forceinline__ int lds_u8(uint32_t a) {
   return static_cast<int>(r);
 }
 
-// 16 bytes global -> shared by this thread, asynchronously, past L1 (which may
-// hold the line from before the newest tokens were written).
+// 16 bytes global -> shared by this thread, asynchronously, past L1: the bytes
+// are read once and need no line there.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
