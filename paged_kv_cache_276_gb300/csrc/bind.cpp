@@ -2,8 +2,8 @@
 //
 // These calls take a few microseconds on the GPU, less than checking their
 // tensors one attribute at a time in Python takes on the host (a decode step's
-// write: 2.1 us on the GPU; 8.9 us a call through ctypes, 3.2 through this
-// module).  Every function checks its tensors (type, device, density, shape),
+// write: 2.1 us on the GPU; 8.9 us a call through ctypes, 3.2 to 3.7 through
+// this module).  Every function checks its tensors (type, device, density, shape),
 // reads their addresses, and calls the C ABI on the given stream or the current
 // one.  It returns the C ABI's code, or kRecheck for arguments that are not what
 // the call takes: the Python side then goes through them for its message.

@@ -28,10 +28,11 @@
 // second kernel.  Joins take the pieces in an order that the sizes fix: results
 // repeat bit for bit.
 //
-// Measured (both kernels, back to back in a graph): 16 x 32768 tokens, 64 q / 8
-// KV heads of 128, block 32: 173 us, 6.3 TB/s of 6.78 for a plain copy; 256
-// mixed lengths, 32 / 8, block 16: 75.5 us, 5.9 TB/s; one sequence of 32768:
-// 20.3 us, of which the copies take 12.6, start and joins the rest.  Units of
+// Measured (both kernels, back to back in a graph; in brackets per call in a row
+// of calls): 16 x 32768 tokens, 64 q / 8 KV heads of 128, block 32: 174 us (176),
+// 6.2 TB/s of 6.78 for a plain copy; 256 mixed lengths, 32 / 8, block 16: 76.5 us
+// (78.4), 5.8 TB/s; one sequence of 32768: 20.2 us (20.5), of which the copies
+// take 12.6, start and joins the rest.  Units of
 // half or twice the size, or more stages with fewer warps, were 1 % faster on
 // the first at best and 7 to 28 % slower on the second.
 #include <cuda.h>

@@ -9,7 +9,7 @@
 // loop: a CTA per few rows lets the hardware balance a ragged end (with a grid
 // of 8 CTAs per SM that walks the rows, read-back took 41.8 us instead of 32.2).
 // Measured at 32768 tokens x 8 KV heads x 128: write 31.0 us (6.5 TB/s),
-// read-back 31.6 us (6.4 TB/s), of 6.78 TB/s for a plain copy; the 256 tokens of
+// read-back 31.7 us (6.4 TB/s), of 6.78 TB/s for a plain copy; the 256 tokens of
 // a decode step 2.1 us, a launch's latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
