@@ -22,8 +22,6 @@ import sys
 import sysconfig
 import warnings
 
-from . import native
-
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -56,8 +54,23 @@ def _fresh(path: str) -> bool:
     return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in _deps())
 
 
+def _bind_path() -> str:
+    """The extension's file; its name takes PyTorch, which the library builds without."""
+    if ROOT not in sys.path:
+        sys.path.append(ROOT)
+    from paged_kv_cache_276_gb300 import native
+    return native.bind_path()
+
+
+def _bind_fresh() -> bool:
+    try:
+        return _fresh(_bind_path())
+    except ImportError:
+        return False
+
+
 def up_to_date() -> bool:
-    return _fresh(LIB) and _fresh(native.bind_path())
+    return _fresh(LIB) and _bind_fresh()
 
 
 def _compile(src: str) -> str:
@@ -89,7 +102,7 @@ def _compile_bind() -> str:
 
 
 def _link_bind(obj: str):
-    path = native.bind_path()
+    path = _bind_path()
     tmp = path + f".tmp{os.getpid()}"
     subprocess.run(["g++", "-shared", obj, "-o", tmp, "-L", BUILD, "-l:libpkv.so", "-Wl,-rpath,$ORIGIN",
                     "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
@@ -105,7 +118,7 @@ def build(force: bool = False) -> str:
     first: an extension that cannot be built costs a warning, not the library."""
     global _bind_failed
     lib_due = force or not _fresh(LIB)
-    bind_due = force or lib_due or not (_bind_failed or _fresh(native.bind_path()))
+    bind_due = force or lib_due or not (_bind_failed or _bind_fresh())
     if not lib_due and not bind_due:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -120,7 +133,7 @@ def build(force: bool = False) -> str:
         try:
             _link_bind(bind.result())
             _bind_failed = False
-        except (OSError, RuntimeError, subprocess.CalledProcessError) as e:
+        except (ImportError, OSError, RuntimeError, subprocess.CalledProcessError) as e:
             _bind_failed = True
             warnings.warn(f"{LIB} is built, but not its Python extension, which the 8-bit cache's calls need: {e}")
     return LIB

@@ -2,6 +2,7 @@
 extension of another PyTorch or Python is neither kept nor loaded."""
 import os
 import subprocess
+import sys
 import sysconfig
 
 import pytest
@@ -57,3 +58,15 @@ def test_an_extension_of_another_torch_or_python_does_not_count(monkeypatch):
         m.setattr(sysconfig, "get_config_var", lambda name: ".cpython-300-other.so")
         assert not build.up_to_date()
     assert build.up_to_date() and native._bind() is not None
+
+
+@pytest.mark.parametrize("torch_there", [True, False])
+def test_the_build_runs_as_a_script_and_without_torch(tmp_path, torch_there):
+    build.build()
+    if not torch_there:
+        (tmp_path / "torch.py").write_text("raise ImportError('no torch here')\n")
+    done = subprocess.run([sys.executable, build.__file__], cwd=tmp_path, capture_output=True, text=True,
+                          env={**os.environ, "PYTHONPATH": str(tmp_path)})
+    assert done.returncode == 0, done.stderr
+    assert done.stdout.strip() == build.LIB
+    assert ("Python extension" in done.stderr) is not torch_there
