@@ -597,10 +597,11 @@ int pkv_read_quant(const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t
  * of one KV head) are not split between CTAs need none, and one sequence or one
  * token more can take the need from 0 to the full size (two pieces per CTA: on
  * 152 SMs 1.3 MB at head_dim 128 with up to 8 query heads per KV head, 2.5 MB
- * with more, half that at head_dim 64).  It never shrinks as num_seqs or max_seq_len grows, so a
- * buffer that serves several batches is sized for the largest num_seqs and
- * max_seq_len that will be passed.  The number of SMs is taken once in a process,
- * from the device that is current at the first call that needs it.
+ * with more, half that at head_dim 64).  It never shrinks as num_seqs or
+ * max_seq_len grows, so a buffer that serves several batches is sized for the
+ * largest num_seqs and max_seq_len that will be passed.  The number of SMs is
+ * taken once in a process, from the device that is current at the first call
+ * that needs it.
  */
 size_t paged_attention_decode_quant_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
                                                    int head_dim, int max_seq_len);

@@ -32,9 +32,9 @@
 // of calls): 16 x 32768 tokens, 64 q / 8 KV heads of 128, block 32: 174 us (176),
 // 6.2 TB/s of 6.78 for a plain copy; 256 mixed lengths, 32 / 8, block 16: 76.5 us
 // (78.4), 5.8 TB/s; one sequence of 32768: 20.2 us (20.5), of which the copies
-// take 12.6, start and joins the rest.  Units of
-// half or twice the size, or more stages with fewer warps, were 1 % faster on
-// the first at best and 7 to 28 % slower on the second.
+// take 12.6, start and joins the rest.  Units of half or twice the size, or more
+// stages with fewer warps, were 1 % faster on the first at best and 7 to 28 %
+// slower on the second.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

@@ -520,9 +520,9 @@ def paged_attention_decode_static_scratch(q, k_cache, v_cache, block_tables, seq
 
 # ------------------------------------------------------- the cache in 8 bits
 # These calls take less time on the GPU than a marshalling through ctypes takes
-# on the host, so they go through an extension (bind.cpp), which checks the tensors and calls
-# the C ABI.  It answers _RECHECK for arguments that the call does not take;
-# they are then gone through here for the message.
+# on the host, so they go through an extension (bind.cpp), which checks the
+# tensors and calls the C ABI.  It answers _RECHECK for arguments that the call
+# does not take; they are then gone through here for the message.
 _BF16, _F8, _U8, _I32, _I64 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64
 _RECHECK = 1
 _bind_module = None
