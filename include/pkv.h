@@ -66,6 +66,7 @@ typedef uint16_t pkv_bf16;
 #define PKV_STATUS_TIMEOUT    8  /* a bounded on-chip wait gave up               */
 #define PKV_STATUS_BAD_QSTART 16 /* prefill: q_start entry out of order or range */
 #define PKV_STATUS_BAD_ITEM   32 /* decode work list: item out of range, or built for other lengths / tables */
+#define PKV_STATUS_BAD_POS    64 /* rotary append: position outside its table         */
 
 /* Human-readable name of a return code (static storage). */
 const char *pkv_error_string(int code);
@@ -657,6 +658,140 @@ int paged_attention_decode_quant(const pkv_bf16 *q, const uint8_t *k_codes, cons
                                  int num_kv_heads, int head_dim, int block_size, int num_blocks,
                                  float scale, pkv_bf16 *out, void *workspace, size_t workspace_bytes,
                                  int32_t *d_status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary append, windowed attention and tree attention.
+ *
+ * The pages have no counterpart to these calls.  They serve models whose keys
+ * are rotated by their position before they are cached, whose layers see a
+ * window of the context (with a few first tokens that stay visible), and whose
+ * next tokens are drafted as a tree and verified in one step.  The cache,
+ * tables, slots and allocator are those of the calls above.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * pkv_write_rope -- rotate the queries and keys of new tokens to their
+ * positions and append keys and values: pkv_write with the position rotation
+ * applied on the way.
+ *
+ * For every token t < num_tokens with p = positions[t], and every pair j < R / 2
+ * (R = rot_dim) with c = cos_sin[p][j] and s = cos_sin[p][R / 2 + j], the pair's
+ * values (a, b) of each query and key row become (a c - b s, b c + a s).  The
+ * pair is values (j, j + R / 2) of the row (interleaved = 0) or (2 j, 2 j + 1)
+ * (interleaved = 1); values R and above pass unchanged.  Each product and the
+ * sum are rounded to fp32, the result once to bf16.  Query rows go to q_out; key
+ * rows, and value rows as they are, to slot slot_mapping[t] as in pkv_write (a
+ * negative slot: they are not stored; the queries are rotated all the same).
+ *   q             device bf16 (read): token t's rows [num_q_heads][head_dim]
+ *                 start t * q_stride elements after the first token's; k and v
+ *                 likewise with num_kv_heads rows.  Strides are multiples of 8
+ *                 and at least the rows' width, so that q, k and v can be views
+ *                 of one projection's output
+ *   q_out         device bf16 (written), token stride q_out_stride; may be q
+ *                 itself with the same stride (rotated in place), or lie apart
+ *   positions     device, [num_tokens] int64
+ *   cos_sin       device, [max_positions][rot_dim] fp32: the R / 2 cosines of a
+ *                 position, then its R / 2 sines
+ *   slot_mapping, k_cache, v_cache, num_blocks, block_size, d_status: as pkv_write
+ * A position outside [0, max_positions) sets PKV_STATUS_BAD_POS, a slot >=
+ * num_blocks * block_size PKV_STATUS_BAD_SLOT; nothing of the first token is
+ * written, and of the second only its queries.  The non-negative slots of one
+ * call must be distinct.  num_q_heads = 0 (q and q_out may be NULL): keys and
+ * values only.  All tensors are 16-byte aligned.
+ * Supported: head_dim a multiple of 16 up to 512; rot_dim a multiple of 16 up to
+ * head_dim; any block_size >= 1.  Other sizes return PKV_ERR_UNSUPPORTED
+ * (rot_dim above head_dim: PKV_ERR_ARG).  num_tokens == 0 is a no-op.
+ */
+int pkv_write_rope(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, int64_t q_stride, int64_t k_stride,
+                   int64_t v_stride, const int64_t *positions, const float *cos_sin, int max_positions, int rot_dim,
+                   int interleaved, const int64_t *slot_mapping, int num_tokens, pkv_bf16 *q_out,
+                   int64_t q_out_stride, pkv_bf16 *k_cache, pkv_bf16 *v_cache, int num_blocks, int block_size,
+                   int num_q_heads, int num_kv_heads, int head_dim, int32_t *d_status, void *stream);
+
+/*
+ * pkv_write_rope_quant -- pkv_write_rope into the 8-bit cache: the rotated key
+ * rows (in fp32, with no rounding to bf16 between) and the value rows are
+ * quantised as pkv_write_quant's rows are.  Other arguments as pkv_write_rope
+ * and pkv_write_quant.
+ */
+int pkv_write_rope_quant(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v, int64_t q_stride, int64_t k_stride,
+                         int64_t v_stride, const int64_t *positions, const float *cos_sin, int max_positions,
+                         int rot_dim, int interleaved, const int64_t *slot_mapping, int num_tokens, pkv_bf16 *q_out,
+                         int64_t q_out_stride, uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_exps, uint8_t *v_exps,
+                         int num_blocks, int block_size, int num_q_heads, int num_kv_heads, int head_dim,
+                         int32_t *d_status, void *stream);
+
+/*
+ * paged_attention_window -- attention with a sliding window and a few first
+ * tokens that stay visible (sinks), for single tokens and for prompt chunks.
+ *
+ * Sequence i owns query rows q_start[i] .. q_start[i+1]-1, its newest
+ * c = q_start[i+1] - q_start[i] tokens, as in paged_attention_prefill; q_start
+ * = NULL: one row per sequence (total_q = num_seqs), a decode step.  With
+ * L = seq_lens[i], row q_start[i] + r stands at position p = L - c + r and sees
+ * the keys t <= p with t > p - window or t < sinks:
+ *   out = sum_t softmax_t(scale * q . k_t) v_t over those, per query head g with
+ * KV head g / (num_q_heads / num_kv_heads), rounded to bf16.  A row that sees
+ * nothing (p < 0) gives zeros.
+ *   window        >= 1 (a row's own token counts); at least the longest length:
+ *                 plain causal attention
+ *   sinks         >= 0
+ *   block_tables  as paged_attention_prefill; besides the entries past the
+ *                 sequence, those of blocks that no row of the call sees (between
+ *                 the sinks and the window of the sequence's first row) are never
+ *                 used, so such blocks may have been given back
+ *   max_seq_len   host upper bound of seq_lens (a larger length sets
+ *                 PKV_STATUS_BAD_LEN and is clamped)
+ *   workspace     device, 16-byte aligned, at least
+ *                 paged_attention_window_workspace_size(...) bytes (may be NULL
+ *                 when that is 0); its contents need not be initialised and are
+ *                 not preserved.  Calls that may overlap need one each
+ *   everything else as paged_attention_prefill
+ * Keys and values that a row does not see never reach its result, whatever they
+ * hold (NaN and infinities included).  A row whose visible scores are all -inf
+ * gives zeros, as paged_attention_decode.
+ * Supported: head_dim in {64, 128}; num_q_heads / num_kv_heads <= 16;
+ *   block_size in {16, 32, 64, 128}; num_seqs <= 1024 (65535 with q_start NULL);
+ *   max_blocks_per_seq * block_size and num_blocks * num_kv_heads * block_size
+ *   below 2^31 - 512.  Other sizes return PKV_ERR_UNSUPPORTED.
+ */
+size_t paged_attention_window_workspace_size(int num_seqs, int total_q, int num_q_heads, int num_kv_heads,
+                                             int head_dim, int max_seq_len, int window, int sinks);
+
+int paged_attention_window(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
+                           const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+                           const int32_t *q_start, int num_seqs, int total_q, int max_seq_len, int window, int sinks,
+                           int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                           float scale, pkv_bf16 *out, void *workspace, size_t workspace_bytes, int32_t *d_status,
+                           void *stream);
+
+/*
+ * paged_attention_tree -- attention of a tree of drafted tokens over the cache
+ * (the verification step of speculative decoding).
+ *
+ * Sequence i owns query rows q_start[i] .. q_start[i+1]-1: the nodes of its
+ * tree, c = q_start[i+1] - q_start[i] <= max_nodes of them.  Their keys and
+ * values are in the cache already, as its newest c tokens (node j at table
+ * position L - c + j, L = seq_lens[i]), whatever positions they were rotated to.
+ * Node r sees every key t < L - c of the context, and node j of its own tree iff
+ * bit j of tree_mask[q_start[i] + r] is set (normally its ancestors and itself;
+ * bits c and above are ignored).  A node that sees nothing gives zeros; nodes
+ * before the sequence's start (c > L) do not exist.
+ *   tree_mask     device, [total_q] uint64
+ *   max_nodes     host upper bound of a tree's nodes, 1 .. 64; a sequence with
+ *                 more rows sets PKV_STATUS_BAD_QSTART and gets none
+ *   everything else as paged_attention_window
+ * Supported: as paged_attention_window, num_seqs <= 1024.
+ */
+size_t paged_attention_tree_workspace_size(int num_seqs, int total_q, int max_nodes, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int max_seq_len);
+
+int paged_attention_tree(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
+                         const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+                         const int32_t *q_start, const uint64_t *tree_mask, int num_seqs, int total_q, int max_nodes,
+                         int max_seq_len, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                         int num_blocks, float scale, pkv_bf16 *out, void *workspace, size_t workspace_bytes,
+                         int32_t *d_status, void *stream);
 
 /* ------------------------------------------------------------------------
  * Host block allocator: pool, block tables, refcounts, copy-on-write.

@@ -1,6 +1,7 @@
 """ctypes binding of libpkv.so: the C ABI declared in include/pkv.h, one Python
-function per C entry point with the same name (the 8-bit cache's calls go through
-a small extension, _bind-*.so, for their host time).
+function per C entry point with the same name (the 8-bit cache's calls, the rotary
+append and the windowed and tree attention go through a small extension,
+_bind-*.so, for their host time).
 
 Argument marshalling only: shapes are read off the tensors, pointers and the
 current CUDA stream are passed through, return codes become exceptions.  Every
@@ -36,6 +37,7 @@ PKV_STATUS_BAD_LEN = 4
 PKV_STATUS_TIMEOUT = 8
 PKV_STATUS_BAD_QSTART = 16
 PKV_STATUS_BAD_ITEM = 32
+PKV_STATUS_BAD_POS = 64
 
 PKV_DECODE_OVERLAP = 1
 
@@ -117,6 +119,18 @@ SIGNATURES = {
     "paged_attention_decode_quant": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_int,
                                               _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_ptr,
                                               _c_ptr, _c_size, _c_ptr, _c_ptr]),
+    "pkv_write_rope": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_int, _c_int, _c_int,
+                                _c_ptr, _c_int, _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                _c_ptr, _c_ptr]),
+    "pkv_write_rope_quant": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_int, _c_int,
+                                      _c_int, _c_ptr, _c_int, _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int,
+                                      _c_int, _c_int, _c_int, _c_int, _c_ptr, _c_ptr]),
+    "paged_attention_window_workspace_size": (_c_size, [_c_int] * 8),
+    "paged_attention_window": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr] + [_c_int] * 10 +
+                               [_c_float, _c_ptr, _c_ptr, _c_size, _c_ptr, _c_ptr]),
+    "paged_attention_tree_workspace_size": (_c_size, [_c_int] * 7),
+    "paged_attention_tree": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_ptr] + [_c_int] * 9 +
+                             [_c_float, _c_ptr, _c_ptr, _c_size, _c_ptr, _c_ptr]),
     "pkv_seq_append_batch": (_c_int, [_c_ptr, _c_ptr, _c_int, _c_int, _c_ptr]),
     "pkv_seq_append_tokens": (_c_int, [_c_ptr, ctypes.c_int64, _c_ptr, _c_int, _c_ptr, ctypes.POINTER(_c_int)]),
     "pkv_prefix_cache_stats": (_c_int, [_c_ptr, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64)]),
@@ -643,6 +657,124 @@ def paged_attention_decode_quant(q, k_codes, v_codes, k_exps, v_exps, block_tabl
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         _refuse_rest(k_codes.device)
     _check(rc, "paged_attention_decode_quant")
+
+
+# ------------------------------- rotary append, windowed attention, tree attention
+# Through the extension too, as the 8-bit cache's calls.
+def _refuse_bf16_cache(k_cache, v_cache, d_status, *others):
+    """Raise for the first argument that is not what a call takes; returns the cache's shape."""
+    dev = k_cache.device if isinstance(k_cache, torch.Tensor) else None
+    for t, dtype, name in ((k_cache, _BF16, "k_cache"), (v_cache, _BF16, "v_cache")) + others:
+        _need(t, dtype, name, dev)
+    if d_status is not None and (not isinstance(d_status, torch.Tensor) or d_status.dtype != _I32
+                                 or d_status.device != dev):
+        raise TypeError("d_status must be a torch.int32 tensor on the cache's device")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch: caches [NB, Hkv, bs, d] expected")
+    return k_cache.shape
+
+
+def _refuse_rope(q, k, v, positions, cos_sin, slot_mapping, q_out, shape, dev):
+    if slot_mapping.dim() != 1 or positions.shape != slot_mapping.shape:
+        raise ValueError("slot_mapping and positions: [T] expected")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin: [max_positions, rot_dim] expected")
+    T, (_, Hkv, _, d) = slot_mapping.shape[0], shape
+    for t, name in ((k, "k"), (v, "v")):
+        _refuse_token_rows(t, name, (T, Hkv, d), dev)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out: both, or neither")
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[1] < 1:
+            raise ValueError("q: a tensor [T, Hq, d] expected")
+        for t, name in ((q, "q"), (q_out, "q_out")):
+            _refuse_token_rows(t, name, (T, q.shape[1], d), dev)
+    _refuse_rest(dev)
+
+
+def pkv_write_rope(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, interleaved=False,
+                   d_status=None, stream=None):
+    """Rotate new tokens' queries and keys to their positions, append keys and values.  q, q_out: [T, Hq, d] bf16
+    (or both None), k, v: [T, Hkv, d] bf16, each token's rows dense (views of a fused projection's output are fine;
+    q_out may be q); positions: [T] int64; cos_sin: [max_positions, rot_dim] fp32, cosines then sines; slot_mapping:
+    [T] int64, negative: not stored; caches [NB, Hkv, bs, d] bf16 (device).  interleaved: pairs (2j, 2j + 1), else
+    (j, j + rot_dim / 2).  d and rot_dim: multiples of 16."""
+    rc = _bind().write_rope(q, k, v, positions, cos_sin, slot_mapping, q_out, bool(interleaved), d_status,
+                            _handle(stream), k_cache, v_cache)
+    if rc == _RECHECK:
+        shape = _refuse_bf16_cache(k_cache, v_cache, d_status, (positions, _I64, "positions"),
+                                   (cos_sin, torch.float32, "cos_sin"), (slot_mapping, _I64, "slot_mapping"))
+        _refuse_rope(q, k, v, positions, cos_sin, slot_mapping, q_out, shape, k_cache.device)
+    _check(rc, "pkv_write_rope")
+
+
+def pkv_write_rope_quant(q, k, v, positions, cos_sin, slot_mapping, q_out, k_codes, v_codes, k_exps, v_exps,
+                         interleaved=False, d_status=None, stream=None):
+    """``pkv_write_rope`` into an 8-bit cache (laid out as in ``pkv_write_quant``)."""
+    rc = _bind().write_rope_quant(q, k, v, positions, cos_sin, slot_mapping, q_out, bool(interleaved), d_status,
+                                  _handle(stream), k_codes, v_codes, k_exps, v_exps)
+    if rc == _RECHECK:
+        shape = _refuse_cache(k_codes, v_codes, k_exps, v_exps, d_status, (positions, _I64, "positions"),
+                              (cos_sin, torch.float32, "cos_sin"), (slot_mapping, _I64, "slot_mapping"))
+        _refuse_rope(q, k, v, positions, cos_sin, slot_mapping, q_out, shape, k_codes.device)
+    _check(rc, "pkv_write_rope_quant")
+
+
+def _refuse_spans(q, k_cache, v_cache, block_tables, seq_lens, q_start, out, workspace, d_status, *others):
+    start = () if q_start is None else ((q_start, _I32, "q_start"),)
+    d = _refuse_bf16_cache(k_cache, v_cache, d_status, (q, _BF16, "q"), (out, _BF16, "out"),
+                           (block_tables, _I32, "block_tables"), (seq_lens, _I32, "seq_lens"), *start, *others)[3]
+    if q.dim() != 3 or q.shape[2] != d or out.shape != q.shape or block_tables.dim() != 2 or seq_lens.dim() != 1 \
+            or block_tables.shape[0] != seq_lens.shape[0] \
+            or (q.shape[:1] != seq_lens.shape if q_start is None else q_start.shape != (seq_lens.shape[0] + 1,)) \
+            or any(t.shape != q.shape[:1] for t, _, _ in others):
+        raise ValueError("shape mismatch")
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.device != k_cache.device
+                                  or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    _refuse_rest(k_cache.device)
+
+
+def paged_attention_window_workspace_size(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, max_seq_len, window,
+                                          sinks):
+    return int(lib().paged_attention_window_workspace_size(int(num_seqs), int(total_q), int(num_q_heads),
+                                                           int(num_kv_heads), int(head_dim), int(max_seq_len),
+                                                           int(window), int(sinks)))
+
+
+def paged_attention_window(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, window, sinks, scale, out,
+                           q_start=None, workspace=None, d_status=None, stream=None):
+    """Attention of each sequence's newest tokens over a sliding window and the first ``sinks`` tokens: q, out
+    [total_q, Hq, d] bf16; q_start [B + 1] int32, or None for one row per sequence; caches [NB, Hkv, bs, d]; tables
+    [B, max_blocks] int32 (entries of blocks that no row sees may hold anything); lens [B] int32; workspace: a device
+    buffer of ``paged_attention_window_workspace_size`` bytes (one per call that may overlap)."""
+    rc = _bind().spans(q, k_cache, v_cache, block_tables, seq_lens, q_start, None, int(window), int(sinks),
+                       int(max_seq_len), float(scale), out, workspace, d_status, _handle(stream))
+    if rc == _RECHECK:
+        _refuse_spans(q, k_cache, v_cache, block_tables, seq_lens, q_start, out, workspace, d_status)
+    _check(rc, "paged_attention_window")
+
+
+def paged_attention_tree_workspace_size(num_seqs, total_q, max_nodes, num_q_heads, num_kv_heads, head_dim,
+                                        max_seq_len):
+    return int(lib().paged_attention_tree_workspace_size(int(num_seqs), int(total_q), int(max_nodes), int(num_q_heads),
+                                                         int(num_kv_heads), int(head_dim), int(max_seq_len)))
+
+
+def paged_attention_tree(q, k_cache, v_cache, block_tables, seq_lens, q_start, tree_mask, max_nodes, max_seq_len,
+                         scale, out, workspace=None, d_status=None, stream=None):
+    """Attention of drafted trees over the cache: q, out [total_q, Hq, d] bf16, the nodes of sequence i in rows
+    q_start[i] .. q_start[i + 1] - 1 (at most ``max_nodes`` <= 64, its newest tokens in the cache); tree_mask [total_q]
+    int64: bit j set where the node sees node j of its tree; every node sees the whole context.  The rest as in
+    ``paged_attention_window``."""
+    rc = _RECHECK if q_start is None or tree_mask is None else _bind().spans(
+        q, k_cache, v_cache, block_tables, seq_lens, q_start, tree_mask, int(max_nodes), 0, int(max_seq_len),
+        float(scale), out, workspace, d_status, _handle(stream))
+    if rc == _RECHECK:
+        _need(q_start, _I32, "q_start")
+        _refuse_spans(q, k_cache, v_cache, block_tables, seq_lens, q_start, out, workspace, d_status,
+                      (tree_mask, _I64, "tree_mask"))
+    _check(rc, "paged_attention_tree")
 
 
 # ------------------------------------------------------------- allocator
