@@ -16,11 +16,11 @@
 #include "launch.cuh"
 #include "pkv.h"
 #include "ptx.cuh"
+#include "spans.cuh"
 
 namespace pkv {
+namespace spans {
 namespace {
-
-constexpr int kMaxNodes = 64;
 
 struct SpanParams {
   const __nv_bfloat16 *q, *k_cache, *v_cache;
@@ -121,32 +121,19 @@ __global__ void __launch_bounds__(128) spans_kernel(const SpanParams p) {
   for (int i = 0; i < PER; ++i) p.out[w * D + lane * PER + i] = __float2bfloat16_rn(o[i] * inv);
 }
 
-struct SpanCall {
-  const pkv_bf16 *q, *k_cache, *v_cache;
-  const int32_t *block_tables;
-  int max_blocks;
-  const int32_t *seq_lens, *q_start;
-  int num_seqs, total_q, max_seq_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
-  float scale;
-  pkv_bf16 *out;
-  void *workspace;
-  size_t workspace_bytes;
-  int32_t *status;
-  void *stream;
-};
-
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Sizes and pointers; *work: there is something to do.
-int check(const SpanCall &a, bool single, bool *work) {
+int check(const Call &a, bool *work) {
   *work = false;
+  const bool single = !a.q_start;
   if (a.num_seqs < 0 || a.total_q < 0 || a.max_blocks < 0 || a.max_seq_len < 0 || a.num_q_heads < 1 ||
       a.num_kv_heads < 1 || a.num_blocks < 0 || !std::isfinite(a.scale) || a.num_q_heads % a.num_kv_heads != 0)
     return PKV_ERR_ARG;
   if ((a.head_dim != 64 && a.head_dim != 128) || a.num_q_heads / a.num_kv_heads > 16) return PKV_ERR_UNSUPPORTED;
   if (a.block_size != 16 && a.block_size != 32 && a.block_size != 64 && a.block_size != 128)
     return PKV_ERR_UNSUPPORTED;
-  if (a.num_seqs > (single ? 65535 : 1024)) return PKV_ERR_UNSUPPORTED;
+  if (a.num_seqs > (single ? 65535 : kMaxSeqs)) return PKV_ERR_UNSUPPORTED;
   constexpr long long kLimit = (1ll << 31) - 512;
   if (static_cast<long long>(a.max_blocks) * a.block_size >= kLimit ||
       static_cast<long long>(a.num_blocks) * a.num_kv_heads * a.block_size >= kLimit)
@@ -161,7 +148,7 @@ int check(const SpanCall &a, bool single, bool *work) {
   return PKV_OK;
 }
 
-int launch(const SpanCall &a, SpanParams p) {
+int launch(const Call &a, SpanParams p) {
   p.q = reinterpret_cast<const __nv_bfloat16 *>(a.q);
   p.k_cache = reinterpret_cast<const __nv_bfloat16 *>(a.k_cache);
   p.v_cache = reinterpret_cast<const __nv_bfloat16 *>(a.v_cache);
@@ -179,6 +166,8 @@ int launch(const SpanCall &a, SpanParams p) {
   p.group = a.num_q_heads / a.num_kv_heads;
   p.num_blocks = a.num_blocks;
   p.block_size = a.block_size;
+  p.window = a.window;
+  p.sinks = a.sinks;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   const long long grid = (static_cast<long long>(a.total_q) * a.num_q_heads + 3) / 4;
   if (grid > 0x7fffffffll) return PKV_ERR_UNSUPPORTED;
@@ -189,14 +178,54 @@ int launch(const SpanCall &a, SpanParams p) {
   return e == cudaSuccess ? PKV_OK : (set_cuda_error(e), PKV_ERR_CUDA);
 }
 
+// The sizes that both calls' workspaces depend on; false: not sizes of a call that
+// would run.
+bool sizes(Call *a, int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim, int max_seq_len) {
+  a->num_seqs = num_seqs;
+  a->total_q = total_q;
+  a->num_q_heads = num_q_heads;
+  a->num_kv_heads = num_kv_heads;
+  a->head_dim = head_dim;
+  a->max_seq_len = max_seq_len;
+  return num_seqs > 0 && total_q > 0 && num_q_heads > 0 && num_kv_heads > 0 && num_q_heads % num_kv_heads == 0 &&
+         num_q_heads / num_kv_heads <= 16 && (head_dim == 64 || head_dim == 128) && max_seq_len >= 0;
+}
+
+int run(const Call &a) {
+  bool work;
+  const int rc = check(a, &work);
+  if (rc != PKV_OK || !work) return rc;
+  return a.q_start ? tc_launch(a) : launch(a, SpanParams{});
+}
+
 }  // namespace
+}  // namespace spans
 }  // namespace pkv
 
 extern "C" {
 
-size_t paged_attention_window_workspace_size(int, int, int, int, int, int, int, int) { return 0; }
+size_t paged_attention_window_workspace_size(int num_seqs, int total_q, int num_q_heads, int num_kv_heads,
+                                             int head_dim, int max_seq_len, int window, int sinks) {
+  pkv::spans::Call a{};
+  if (window < 1 || sinks < 0 ||
+      !pkv::spans::sizes(&a, num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, max_seq_len))
+    return 0;
+  a.window = window;
+  a.sinks = sinks;
+  return pkv::spans::tc_workspace_size(a);
+}
 
-size_t paged_attention_tree_workspace_size(int, int, int, int, int, int, int) { return 0; }
+size_t paged_attention_tree_workspace_size(int num_seqs, int total_q, int max_nodes, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int max_seq_len) {
+  pkv::spans::Call a{};
+  if (max_nodes < 1 || max_nodes > pkv::spans::kMaxNodes ||
+      !pkv::spans::sizes(&a, num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, max_seq_len))
+    return 0;
+  static const uint64_t some = 0;  // a tree's call is one with a mask
+  a.mask = &some;
+  a.max_nodes = max_nodes;
+  return pkv::spans::tc_workspace_size(a);
+}
 
 int paged_attention_window(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
                            const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
@@ -205,16 +234,9 @@ int paged_attention_window(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv
                            float scale, pkv_bf16 *out, void *workspace, size_t workspace_bytes, int32_t *d_status,
                            void *stream) {
   if (window < 1 || sinks < 0 || (!q_start && total_q != num_seqs)) return PKV_ERR_ARG;
-  const pkv::SpanCall a{q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, q_start, num_seqs, total_q,
-                        max_seq_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, out,
-                        workspace, workspace_bytes, d_status, stream};
-  bool work;
-  const int rc = pkv::check(a, !q_start, &work);
-  if (rc != PKV_OK || !work) return rc;
-  pkv::SpanParams p{};
-  p.window = window;
-  p.sinks = sinks;
-  return pkv::launch(a, p);
+  return pkv::spans::run({q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, q_start, nullptr, num_seqs,
+                          total_q, max_seq_len, window, sinks, 0, num_q_heads, num_kv_heads, head_dim, block_size,
+                          num_blocks, scale, out, workspace, workspace_bytes, d_status, stream});
 }
 
 int paged_attention_tree(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
@@ -223,18 +245,12 @@ int paged_attention_tree(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_b
                          int max_seq_len, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                          int num_blocks, float scale, pkv_bf16 *out, void *workspace, size_t workspace_bytes,
                          int32_t *d_status, void *stream) {
-  if (max_nodes < 1 || max_nodes > pkv::kMaxNodes) return PKV_ERR_ARG;
-  const pkv::SpanCall a{q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, q_start, num_seqs, total_q,
-                        max_seq_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, out,
-                        workspace, workspace_bytes, d_status, stream};
-  bool work;
-  const int rc = pkv::check(a, false, &work);
-  if (rc != PKV_OK || !work) return rc;
-  if (!q_start || !tree_mask || (reinterpret_cast<uintptr_t>(tree_mask) & 7u)) return PKV_ERR_ARG;
-  pkv::SpanParams p{};
-  p.mask = tree_mask;
-  p.max_nodes = max_nodes;
-  return pkv::launch(a, p);
+  if (max_nodes < 1 || max_nodes > pkv::spans::kMaxNodes) return PKV_ERR_ARG;
+  if (num_seqs > 0 && total_q > 0 && (!q_start || !tree_mask || (reinterpret_cast<uintptr_t>(tree_mask) & 7u)))
+    return PKV_ERR_ARG;
+  return pkv::spans::run({q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, q_start, tree_mask,
+                          num_seqs, total_q, max_seq_len, 0, 0, max_nodes, num_q_heads, num_kv_heads, head_dim,
+                          block_size, num_blocks, scale, out, workspace, workspace_bytes, d_status, stream});
 }
 
 }  // extern "C"

@@ -1,0 +1,1011 @@
+// Windowed attention of query chunks and attention of drafted trees on the
+// 5th-generation tensor cores.
+//
+// For one KV head, a query tile of 128 rows holds up to 128 / G tokens x the G
+// query heads of the group (row r = token r / G, head r % G).  Over each tile of
+// 128 keys that some row sees:
+//     S  = Q K^T                     tcgen05.mma, M 128 x N 128 x K d -> TMEM
+//     P  = exp2(S * scale*log2e - m)  softmax warps, one query row per thread,
+//                                    bf16 in TMEM
+//     O += P V                       tcgen05.mma, M 128 x N d x K 128 -> TMEM
+// with the running max / sum of the online softmax.  What a row sees of a tile is
+// two 64-bit words, from the window's bounds or from the tree's mask: a key whose
+// bit is clear gets the score -inf.
+//
+// Runs and ranges.  A run is one (sequence, KV head, query tile or pair of query
+// tiles) with the key tiles it needs: of a tree every tile of the sequence, of a
+// window those between its first row's window and its last row's position, and
+// the sinks' before them.  The runs of the batch are laid end to end, each with a
+// weight of its keys plus kRunCost, and every CTA of a persistent grid (one per
+// SM) takes an equal, contiguous range of the weight: a border inside a run falls
+// on a key tile, or on the run's end if that is near.  So all SMs end together
+// whatever the lengths are, with no host-built list.  The weights have closed
+// forms, so a CTA finds its first run by three searches.  A run that lies in one
+// range is written at once; the pieces of one that does not (at most two per CTA:
+// the first and the last of its range) go to the workspace as (max, sum,
+// unnormalised O), and a second kernel joins them in the order of the CTAs:
+// results repeat bit for bit.
+//
+// Both query tiles of a pair are multiplied against each key and value tile: half
+// the traffic per product.  A query tile goes to one of two slots in turn (its
+// queries' buffer, its softmax warps, its accumulator), so that with runs of one
+// tile the next run starts in the other slot while this one is written out.
+//
+// Values that a row does not see must not reach it, and 0 times NaN or infinity is
+// NaN: in a tile that is not seen whole, values no row of the run sees are
+// zeroed in shared memory and those that are not finite are zeroed and noted; the
+// rows that do see one add it when they are written out (rare).
+//
+// Warp roles: 0-3 and 4-7 softmax of slot 0 and 1 (thread = row), 8 TMA producer of
+// queries and keys, 9 score-product issuer (one lane) and tensor-memory owner, 10
+// P V product issuer (one lane), 11 TMA producer of values.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "launch.cuh"
+#include "pkv.h"
+#include "ptx.cuh"
+#include "spans.cuh"
+#include "tc.cuh"
+#include "tc_softmax.cuh"
+
+namespace pkv {
+namespace spans {
+namespace {
+
+constexpr int kRows = 128;       // query rows per tile
+constexpr int kTK = 128;         // keys per tile
+constexpr int kTmemCols = 512;
+constexpr int kKWarp = 8, kMmaWarp = 9, kPvWarp = 10, kVWarp = 11;
+constexpr int kThreads = 12 * 32;
+constexpr float kSlack = 8.f;    // lazy rescale threshold (log2 units)
+constexpr int kRunCost = 256;    // a run's start and end, in keys
+constexpr int kMinRange = 512;   // least weight of a CTA's range, in keys
+constexpr int kMinPiece = 2;     // key tiles that a border leaves on either side
+constexpr int kJoinThreads = 256;
+
+template <int D>
+struct Layout {
+  static_assert(D == 64 || D == 128, "head dim");
+  static constexpr int kHalves = D / 64;            // 64-column (128-byte) halves of a row
+  static constexpr int kHalf = kRows * 128;         // one half of a tile of 128 rows
+  static constexpr int kTile = kHalves * kHalf;     // [half][128 rows][128 B]
+  static constexpr int kStages = D == 128 ? 2 : 4;  // of keys, and of values
+  static constexpr int kSmemK = 2 * kTile;          // after two query tiles
+  static constexpr int kSmemV = kSmemK + kStages * kTile;
+  static constexpr int kSmemBars = kSmemV + kStages * kTile;
+  // tensor memory: accumulators at 0 and D, scores, then each slot's P
+  static constexpr int kTmemS = 2 * D, kTmemP = kTmemS + kTK;
+  static_assert(kTmemP + 2 * (kTK / 2) <= kTmemCols, "tensor memory");
+};
+
+// barrier indices (8 bytes each)
+template <int ST>
+struct Bar {
+  static constexpr int kQFull = 0, kQFree = 2, kOFull = 4, kOFree = 6, kSFull = 8, kPFull = 10, kPLo = 12, kPvDone = 14,
+                       kSFree = 16, kKFull = 17, kKEmpty = kKFull + ST, kVFull = kKEmpty + ST, kVEmpty = kVFull + ST,
+                       kCount = kVEmpty + ST;
+};
+
+template <int D>
+constexpr size_t smem_bytes(int num_seqs) {
+  using Lay = Layout<D>;
+  return 1024 + Lay::kSmemBars + Bar<Lay::kStages>::kCount * 8 + 16 + static_cast<size_t>(num_seqs + 1) * 8 +
+         static_cast<size_t>(num_seqs) * 12;
+}
+static_assert(smem_bytes<128>(kMaxSeqs) <= 227 * 1024, "shared memory");
+
+struct Params {
+  const int32_t *block_tables, *seq_lens, *q_start;
+  const uint64_t *mask;        // tree; NULL: window
+  const __nv_bfloat16 *v_cache;
+  __nv_bfloat16 *out;
+  float4 *ws_o;                // [2 grid][D / 4][piece_rows]
+  float2 *ws_ml;               // [2 grid][piece_rows]
+  int4 *ws_desc;               // [grid]: {sequence | KV head << 16, first token, flags, -} of each CTA's pieces
+  int32_t *status;
+  int num_seqs, max_blocks, num_q_heads, num_kv_heads, num_blocks, total_q, max_len, oob_row;
+  int group, tile_tok, span;   // tokens of a query tile (floor(128 / G) or the tree's) and of a run
+  int window, sinks, max_nodes, piece_rows;
+  float scale_log2;
+};
+
+// flags of a descriptor
+constexpr int kLeaves = 1;  // the CTA's last run goes on in the next CTA (piece 1 holds its start)
+constexpr int kEnds = 2;    // the run that the CTA goes on with (piece 0) ends here
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Per-sequence values kept in shared memory.
+struct SeqTab {
+  const long long *prefix;  // [B + 1] weight before each sequence
+  const int *lens, *qs, *qc;  // [B] clamped length, first query row, query tokens (0: none or a bad q_start)
+};
+
+// The weights of a sequence's runs (of one KV head), in keys: run i has
+//   i < bent:  base + span (i + 1)     (its window still reaches the first token)
+//   else       flat
+struct Weights {
+  long long base, flat, bent;
+  int span, runs;
+  __device__ Weights(const Params &p, int L, int c) {
+    span = p.span;
+    runs = ceil_div(c, span);
+    if (p.mask) {
+      bent = 0;
+      base = 0;
+      flat = kRunCost + max(L, 1);
+    } else {
+      const long long ctx = max(0, L - c);
+      const long long reach = static_cast<long long>(p.window) - 1 + (static_cast<long long>(p.sinks) + kTK - 1) / kTK * kTK;
+      bent = ctx > reach ? 0 : min(static_cast<long long>(runs), (reach - ctx) / span + 1);
+      base = kRunCost + ctx;
+      flat = kRunCost + span + reach;
+    }
+  }
+  __device__ long long of(int i) const { return i < bent ? base + static_cast<long long>(span) * (i + 1) : flat; }
+  __device__ long long sum(long long m) const {  // of the first m runs
+    const long long b = min(m, bent);
+    return b * base + span * (b * (b + 1) / 2) + (m - b) * flat;
+  }
+  // the run that holds weight x, 0 <= x < sum(runs)
+  __device__ int find(long long x) const {
+    const long long s = sum(bent);
+    if (x >= s) return static_cast<int>(bent + (x - s) / flat);
+    long long lo = 0, hi = bent;
+    while (hi - lo > 1) {
+      const long long mid = (lo + hi) >> 1;
+      if (sum(mid) <= x) lo = mid; else hi = mid;
+    }
+    return static_cast<int>(lo);
+  }
+};
+
+// A CTA's piece of a run: key tiles [t0, t1) of its n.  Tile v starts at key
+// 128 v (the sinks', v < ns) or 128 (v - ns + t_lo).
+struct Run {
+  int seq, head, r0, ntq;  // first query token, query tiles
+  int lo, hi, sink_end;    // the run sees nothing outside [lo, hi) and [0, sink_end)
+  int ns, t_lo, n, t0, t1;
+  __device__ bool whole() const { return t0 == 0 && t1 == n; }
+  __device__ int key0(int v) const { return kTK * (v < ns ? v : v - ns + t_lo); }
+};
+
+// The runs of this CTA in order (every role walks the same sequence).
+struct Sched {
+  long long xa, xb, s;  // the CTA's range; the current run's start
+  int seq, head, i;
+  bool done;
+  Run x;
+
+  // true: there is a first run
+  __device__ bool begin(const Params &p, const SeqTab &t, int ctas) {
+    const long long total = t.prefix[p.num_seqs];
+    xa = xb = 0;
+    if (static_cast<int>(blockIdx.x) < ctas) {
+      xa = total * blockIdx.x / ctas;
+      xb = total * (blockIdx.x + 1) / ctas;
+    }
+    done = xa >= xb;
+    if (done) return false;
+    int lo = 0, hi = p.num_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (t.prefix[mid] <= xa) lo = mid; else hi = mid;
+    }
+    seq = lo;
+    const Weights w(p, t.lens[seq], t.qc[seq]);
+    const long long per_head = w.sum(w.runs), off = xa - t.prefix[seq];
+    head = static_cast<int>(off / per_head);
+    i = w.find(off - head * per_head);
+    s = t.prefix[seq] + head * per_head + w.sum(i);
+    return settle(p, t);
+  }
+  // the next run of the CTA; false: there is none
+  __device__ bool next(const Params &p, const SeqTab &t) {
+    step(p, t);
+    return settle(p, t);
+  }
+
+ private:
+  __device__ void step(const Params &p, const SeqTab &t) {
+    const Weights w(p, t.lens[seq], t.qc[seq]);
+    s += w.of(i);
+    if (++i < w.runs) return;
+    i = 0;
+    if (++head < p.num_kv_heads) return;
+    head = 0;
+    do ++seq;
+    while (seq < p.num_seqs && t.qc[seq] == 0);
+  }
+  // from the current run on: the first that this CTA has a piece of
+  __device__ bool settle(const Params &p, const SeqTab &t) {
+    for (; s < xb && seq < p.num_seqs; step(p, t)) {
+      const int L = t.lens[seq], c = t.qc[seq];
+      geometry(p, L, c);
+      const long long w = Weights(p, L, c).of(i);
+      x.t0 = xa <= s ? 0 : border(xa - s, w);
+      x.t1 = xb >= s + w ? x.n : border(xb - s, w);
+      // a run without keys belongs to the CTA that holds its start; a range
+      // inside a tile is an empty piece, which the join expects
+      const bool mine = x.n == 0 ? xa <= s : x.t0 < x.t1 || (x.t0 > 0 && x.t0 < x.n);
+      if (mine) return true;
+    }
+    done = true;
+    return false;
+  }
+  __device__ int border(long long at, long long w) const {
+    const int o = static_cast<int>(at * x.n / w);
+    return o < kMinPiece ? 0 : o > x.n - kMinPiece ? x.n : o;
+  }
+  __device__ void geometry(const Params &p, int L, int c) {
+    x.seq = seq;
+    x.head = head;
+    x.r0 = i * p.span;
+    const int ctx = L - c, end = min(c, x.r0 + p.span);
+    x.ntq = end - x.r0 > p.tile_tok ? 2 : 1;
+    if (p.mask) {
+      x.lo = 0;
+      x.hi = L;
+      x.sink_end = 0;
+    } else {
+      x.hi = max(0, ctx + end);
+      x.lo = max(0, max(0, ctx + x.r0) - p.window + 1);
+      x.sink_end = min(p.sinks, x.lo);
+    }
+    x.t_lo = x.lo / kTK;
+    x.ns = min(ceil_div(x.sink_end, kTK), x.t_lo);
+    x.n = x.hi > 0 ? x.ns + ceil_div(x.hi, kTK) - x.t_lo : 0;
+  }
+};
+
+// CTAs that get a range.
+__device__ __forceinline__ int active_ctas(long long total) {
+  const long long most = total / kMinRange;
+  return most < 1 ? 1 : most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+}
+
+// Bits below x of a 64-bit word.
+__device__ __forceinline__ uint64_t below(int x) { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1; }
+
+// What a row sees of 64 keys from h0 on.
+struct RowSight {
+  int lo, hi, sinks;   // window: [lo, hi) and [0, sinks)
+  int ctx;             // tree: [0, ctx) and bit j of word for key ctx + j
+  uint64_t word;
+  bool tree;
+  __device__ __forceinline__ uint64_t of(int h0) const {
+    if (!tree) return (below(hi - h0) & ~below(lo - h0)) | below(sinks - h0);
+    const int sh = ctx - h0;
+    const uint64_t own = sh >= 64 || sh <= -64 ? 0ull : sh >= 0 ? word << sh : word >> -sh;
+    return below(sh) | own;
+  }
+};
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t two_bf16) {
+  const uint32_t m = two_bf16 & 0x7F807F80u;
+  return (m & 0x7F80u) == 0x7F80u || (m >> 16) == 0x7F80u;
+}
+
+template <int BS, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    spans_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                    const __grid_constant__ CUtensorMap tmv, const Params p) {
+  using Lay = Layout<D>;
+  constexpr int kStages = Lay::kStages, kHalves = Lay::kHalves, kTile = Lay::kTile;
+  using BI = Bar<kStages>;
+  // one TMA box per block of the tile
+  constexpr int kBoxes = kTK / BS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kSmemBars);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + BI::kCount);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  int *odd_tile = reinterpret_cast<int *>(tmem_slot + 2);  // 1 + the last key tile (counted over the CTA) whose values are not all finite
+  long long *prefix = reinterpret_cast<long long *>(bars + BI::kCount + 2);  // [B + 1]
+  int *lens = reinterpret_cast<int *>(prefix + p.num_seqs + 1);              // [B]
+  int *qs = lens + p.num_seqs, *qc = qs + p.num_seqs;                        // [B] each
+  const SeqTab tab{prefix, lens, qs, qc};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int B = p.num_seqs, hkv = p.num_kv_heads;
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  if (warp == 0) {  // weight per sequence -> exclusive prefix
+    const int per = (B + 31) / 32;
+    const int lo = min(B, lane * per), hi = min(B, lo + per);
+    const int cap = min(p.max_blocks * BS, p.max_len);
+    long long sum = 0;
+    for (int i = lo; i < hi; ++i) {
+      int L = p.seq_lens[i];
+      if (L < 0 || L > cap) {
+        if (blockIdx.x == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_LEN);
+        L = L < 0 ? 0 : cap;
+      }
+      const int a = p.q_start[i], b = p.q_start[i + 1];
+      int c = b - a;
+      if (a < 0 || b < a || b > p.total_q || (p.mask && c > p.max_nodes)) {
+        if (blockIdx.x == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_QSTART);
+        c = 0;
+      }
+      lens[i] = L;
+      qs[i] = a;
+      qc[i] = c;
+      const Weights w(p, L, c);
+      sum += w.sum(w.runs) * hkv;
+      prefix[i + 1] = sum;  // within the lane's stretch
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    for (int i = lo; i < hi; ++i) prefix[i + 1] += incl - sum;
+    if (lane == 0) prefix[0] = 0;
+  }
+  if (threadIdx.x == 32 * kKWarp) {
+    for (int i = 0; i < 2; ++i) {  // one per slot
+      mbar_init(bar(BI::kQFull + i), 1);
+      mbar_init(bar(BI::kQFree + i), 1);
+      mbar_init(bar(BI::kOFull + i), 1);
+      mbar_init(bar(BI::kOFree + i), kRows);
+      mbar_init(bar(BI::kSFull + i), 1);
+      mbar_init(bar(BI::kPFull + i), kRows);
+      mbar_init(bar(BI::kPLo + i), kRows);
+      mbar_init(bar(BI::kPvDone + i), 1);
+    }
+    mbar_init(bar(BI::kSFree), kRows);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(BI::kKFull + s), 1);
+      mbar_init(bar(BI::kKEmpty + s), 1);
+      mbar_init(bar(BI::kVFull + s), 1);
+      mbar_init(bar(BI::kVEmpty + s), 1);
+    }
+    *abort_flag = 0;
+    *odd_tile = 0;
+    mbar_init_fence();
+  }
+  if (warp == kMmaWarp) {
+    tc::alloc(smem_u32(tmem_slot), kTmemCols);
+    tc::relinquish();
+  }
+  if (p.tile_tok * p.group < kRows) {
+    // the loads fill the tile's first tile_tok * G rows only: the rest stay zero
+    for (int i = threadIdx.x; i < 2 * kTile / 16; i += kThreads)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_u32(smem) + i * 16), "r"(0u) : "memory");
+    fence_proxy_async_shared();
+  }
+  if (threadIdx.x == 32 * kKWarp + 1) {
+    tma_prefetch_desc(&tmq);
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + Lay::kSmemK), sV = smem_u32(smem + Lay::kSmemV);
+  const uint32_t tS = tmem + Lay::kTmemS, tP = tmem + Lay::kTmemP;
+  const int ctas = active_ctas(prefix[B]);
+  Sched sc;
+  sc.begin(p, tab, ctas);
+  auto timed_out = [&] {
+    if (p.status) atomicOr(p.status, PKV_STATUS_TIMEOUT);
+    *abort_flag = 1;
+  };
+
+  if (!sc.done) {
+    if (warp == kKWarp || warp == kVWarp) {
+      // ------------------------------------------- producers: K (+ Q), V
+      const bool is_v = warp == kVWarp;
+      const CUtensorMap *tm = is_v ? &tmv : &tmk;
+      const uint32_t ring = is_v ? sV : sK;
+      const int full0 = is_v ? BI::kVFull : BI::kKFull, empty0 = is_v ? BI::kVEmpty : BI::kKEmpty;
+      // a tree of one run per KV head reads every key once; other runs share theirs
+      const uint64_t pol = p.mask && p.max_nodes <= p.span ? l2_policy_evict_first() : l2_policy_evict_normal();
+      int g = 0, nq = 0;  // key tiles and query tiles so far
+      int tw_seq = -1, tw_base = 0, tw_val = -1;
+      for (; !sc.done && !*abort_flag; sc.next(p, tab)) {
+        const Run &x = sc.x;
+        if (x.t0 >= x.t1) continue;
+        if (!is_v) {
+          bool ok = true;
+          for (int q = 0; q < x.ntq && ok; ++q, ++nq) {
+            const int slot = nq & 1, use = nq >> 1;
+            if (use > 0 && !wait_warp(bar(BI::kQFree + slot), (use - 1) & 1)) ok = false;
+            if (ok && lane == 0) {
+              mbar_arrive_expect_tx(bar(BI::kQFull + slot), p.tile_tok * p.group * D * 2);  // the boxes' bytes
+              for (int hf = 0; hf < kHalves; ++hf)
+                asm volatile(
+                    "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                    " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(sQ + slot * kTile + hf * Lay::kHalf),
+                    "l"(reinterpret_cast<uint64_t>(&tmq)), "r"(hf * 64), "r"(x.head * p.group),
+                    "r"(qs[x.seq] + x.r0 + q * p.tile_tok), "r"(bar(BI::kQFull + slot))
+                    : "memory");
+            }
+          }
+          if (!ok) {
+            if (lane == 0) timed_out();
+            break;
+          }
+        }
+        for (int t = x.t0; t < x.t1; ++t, ++g) {
+          const int s = g % kStages;
+          if (g >= kStages && !wait_warp(bar(empty0 + s), ((g / kStages) - 1) & 1)) {
+            if (lane == 0) timed_out();
+            break;
+          }
+          const int k0 = x.key0(t), blk = k0 / BS;
+          if (x.seq != tw_seq || blk < tw_base || blk + kBoxes > tw_base + 32) {
+            tw_seq = x.seq;
+            tw_base = blk;
+            const int e = blk + lane;
+            tw_val = e < p.max_blocks ? p.block_tables[static_cast<size_t>(x.seq) * p.max_blocks + e] : -1;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), kTile);
+          // one lane per (box, half): the box copies go out in parallel
+          const int j = lane / kHalves, hf = lane % kHalves;
+          const int b = __shfl_sync(0xffffffffu, tw_val, (blk + min(j, kBoxes - 1) - tw_base) & 31);
+          if (j < kBoxes) {
+            const int kb = k0 + j * BS;  // the block's first key
+            const bool seen = kb < x.hi && (kb + BS > x.lo || kb < x.sink_end);
+            int row = p.oob_row;  // no row of the run sees the block, or a bad id: zeros
+            if (seen && b >= 0 && b < p.num_blocks) row = (b * hkv + x.head) * BS;
+            else if (seen && p.status && !is_v && hf == 0) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
+            tma_load_2d(ring + s * kTile + hf * Lay::kHalf + j * BS * 128, tm, hf * 64, row, bar(full0 + s), pol);
+          }
+        }
+      }
+      // never leave a copy in flight into this CTA's shared memory
+      if (lane == 0) {
+        for (int y = g > kStages ? g - kStages : 0; y < g; ++y)
+          mbar_wait_sleep(bar(full0 + (y % kStages)), (y / kStages) & 1);
+        if (!is_v)
+          for (int y = nq > 2 ? nq - 2 : 0; y < nq; ++y) mbar_wait_sleep(bar(BI::kQFull + (y & 1)), (y >> 1) & 1);
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------- S = Q K^T issuer
+      // The slots share one S buffer: a product goes out once the previous one has
+      // been read (the weights have their own columns), so the next product runs
+      // while the softmax of this one is computed.
+      if (lane == 0) {
+        constexpr uint32_t kIdS = tc::idesc_bf16(kRows, kTK, false, false);
+        int g = 0, nq = 0, np = 0;  // key tiles, query tiles, products so far
+        bool ok = true;
+        for (; !sc.done && ok; sc.next(p, tab)) {
+          const Run &x = sc.x;
+          if (x.t0 >= x.t1) continue;
+          for (int t = x.t0; t < x.t1 && ok; ++t, ++g) {
+            const int s = g % kStages;
+            if (!mbar_wait(bar(BI::kKFull + s), (g / kStages) & 1)) { ok = false; break; }
+            const uint32_t kb = sK + s * kTile;
+            for (int q = 0; q < x.ntq; ++q) {
+              const int slot = (nq + q) & 1;
+              if (t == x.t0 && !mbar_wait(bar(BI::kQFull + slot), ((nq + q) >> 1) & 1)) { ok = false; break; }
+              if (np > 0 && !mbar_wait(bar(BI::kSFree), (np - 1) & 1)) { ok = false; break; }
+              tc::fence_after();
+              const uint32_t sq = sQ + slot * kTile;
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks)
+                tc::mma(tS, tc::desc_sw128(sq + (ks >> 2) * Lay::kHalf + (ks & 3) * 32, 16, 1024),
+                        tc::desc_sw128(kb + (ks >> 2) * Lay::kHalf + (ks & 3) * 32, 16, 1024), kIdS, ks > 0);
+              tc::commit(bar(BI::kSFull + slot));
+              if (t == x.t1 - 1) tc::commit(bar(BI::kQFree + slot));
+              ++np;
+            }
+            if (ok) tc::commit(bar(BI::kKEmpty + s));  // the keys are read by these products only
+          }
+          nq += x.ntq;
+        }
+        if (!ok) timed_out();
+      }
+    } else if (warp == kPvWarp) {
+      // ------------------------------------------------ O += P V issuer
+      // Per key tile the run's first query tile, then its second (whose product so
+      // follows the first one's clearing of the value rows).
+      if (lane == 0) {
+        constexpr uint32_t kIdO = tc::idesc_bf16(kRows, D, false, true);
+        constexpr int kSteps = kTK / 16;  // 16 keys = 8 packed columns of P
+        int g = 0, nq = 0, n[2] = {0, 0};  // key tiles, query tiles, each slot's products
+        bool ok = true;
+        for (; !sc.done && ok; sc.next(p, tab)) {
+          const Run &x = sc.x;
+          if (x.t0 >= x.t1) continue;
+          for (int t = x.t0; t < x.t1 && ok; ++t, ++g) {
+            const int vs = g % kStages;
+            if (!mbar_wait(bar(BI::kVFull + vs), (g / kStages) & 1)) { ok = false; break; }
+            const uint32_t vb = sV + vs * kTile;
+            for (int q = 0; q < x.ntq; ++q) {
+              const int slot = (nq + q) & 1, use = (nq + q) >> 1;
+              int &done = slot ? n[1] : n[0];
+              if (!mbar_wait(bar(BI::kPFull + slot), done & 1)) { ok = false; break; }
+              // the first product overwrites the accumulator: its last run must have been written out
+              if (t == x.t0 && use > 0 && !mbar_wait(bar(BI::kOFree + slot), (use - 1) & 1)) { ok = false; break; }
+              tc::fence_after();
+              const uint32_t pa = tP + slot * (kTK / 2), acc = tmem + slot * D;
+              // keys 64.. first (kPFull), keys 0.. once weighted (kPLo)
+#pragma unroll
+              for (int ks = kSteps / 2; ks < kSteps; ++ks)
+                tc::mma_ta(acc, pa + ks * 8, tc::desc_sw128(vb + ks * 2048, Lay::kHalf, 1024), kIdO,
+                           !(t == x.t0 && ks == kSteps / 2));
+              if (!mbar_wait(bar(BI::kPLo + slot), done & 1)) { ok = false; break; }
+              tc::fence_after();
+#pragma unroll
+              for (int ks = 0; ks < kSteps / 2; ++ks)
+                tc::mma_ta(acc, pa + ks * 8, tc::desc_sw128(vb + ks * 2048, Lay::kHalf, 1024), kIdO, true);
+              tc::commit(bar(BI::kPvDone + slot));
+              if (t == x.t1 - 1) tc::commit(bar(BI::kOFull + slot));
+              ++done;
+            }
+            if (ok) tc::commit(bar(BI::kVEmpty + vs));
+          }
+          nq += x.ntq;
+        }
+        if (!ok) timed_out();
+      }
+    } else {
+      // ------------------------------------------------------ softmax warps
+      const int slot = warp >> 2;
+      const int r = threadIdx.x & (kRows - 1);  // query row = TMEM lane
+      const int tok = r / p.group, gh = r - tok * p.group;
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t tO = tmem + slot * D + lane_off, tSr = tS + lane_off, tPr = tP + slot * (kTK / 2) + lane_off;
+      const bool neg = p.scale_log2 < 0.f;  // a negative scale turns the largest score into the smallest
+      const uint32_t masked = __float_as_uint(neg ? INFINITY : -INFINITY);
+      int g = 0, nq = 0, n_tiles = 0;  // key tiles and query tiles of the CTA, key tiles of this slot
+      bool ok = true;
+      for (; !sc.done && ok; sc.next(p, tab)) {
+        const Run &x = sc.x;
+        const bool any = x.t0 < x.t1;
+        // the run's query tile in this slot: without keys (nothing goes through the
+        // slots) tile `slot` of the run
+        const int q = any ? (slot - nq) & 1 : slot, use = (nq + q) >> 1;
+        if (any) nq += x.ntq;
+        if (q >= x.ntq) {
+          g += x.t1 - x.t0;
+          continue;
+        }
+        const int L = lens[x.seq], c = qc[x.seq], ctx = L - c;
+        const int token = x.r0 + q * p.tile_tok + tok;
+        const bool row_valid = tok < p.tile_tok && token < c;
+        RowSight sight;
+        sight.tree = p.mask != nullptr;
+        sight.ctx = ctx;
+        sight.word = 0;
+        sight.lo = sight.hi = sight.sinks = 0;
+        if (sight.tree) {
+          if (row_valid) sight.word = p.mask[qs[x.seq] + token] & below(c);
+          else sight.ctx = 0;
+        } else if (row_valid) {
+          sight.hi = max(0, ctx + token + 1);
+          sight.lo = max(0, sight.hi - p.window);
+          sight.sinks = min(p.sinks, sight.hi);
+        }
+        // every row of the run sees keys [all_lo, all_hi) and [0, all_sinks)
+        const int last = min(c, x.r0 + p.span) - 1;
+        const int all_hi = sight.tree ? ctx : ctx + x.r0 + 1;
+        const int all_lo = sight.tree ? 0 : max(0, ctx + last - p.window + 1), all_sinks = sight.tree ? 0 : min(p.sinks, all_hi);
+        float m = -INFINITY, l = 0.f;
+        const int g0 = g;
+        for (int t = x.t0; t < x.t1; ++t, ++g) {
+          const int k0 = x.key0(t);
+          const bool full = (k0 >= all_lo && k0 + kTK <= all_hi) || k0 + kTK <= all_sinks;
+          const uint64_t all = row_valid ? ~0ull : 0ull;  // spare rows see nothing
+          const uint64_t see_lo = full ? all : sight.of(k0), see_hi = full ? all : sight.of(k0 + 64);
+          const bool first = t == x.t0;
+          if (!wait_warp(bar(BI::kSFull + slot), n_tiles & 1)) { ok = false; break; }
+          ++n_tiles;
+          bool scale_o = false;
+          float alpha = 1.f;
+          // move the reference max only when a score passes it by more than kSlack
+          // (rare after a run's first tile); exact, since O and l share it
+          auto new_reference = [&](float rm) {
+            const float bm = rm * p.scale_log2;
+            const bool move = bm > m + kSlack;
+            scale_o = move && !first && m != -INFINITY;
+            alpha = scale_o ? fast_exp2(m - bm) : 1.f;
+            if (move) {
+              l = m == -INFINITY ? 0.f : l * exp2f(m - bm);
+              m = bm;
+            }
+            return m == -INFINITY ? 0.f : m;
+          };
+          auto mask = [&](uint32_t(&sv)[64], uint64_t see) {
+            const uint32_t a = static_cast<uint32_t>(see), b = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              if (!(a & (1u << k))) sv[k] = masked;
+              if (!(b & (1u << k))) sv[32 + k] = masked;
+            }
+          };
+          auto rescale_o = [&]() {
+            if (__any_sync(0xffffffffu, scale_o)) {  // warp-uniform: tcgen05.ld/st are warp-wide
+#pragma unroll
+              for (int ch = 0; ch < D / 32; ++ch) {
+                uint32_t ov[32];
+                tc::ld32(tO + ch * 32, ov);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+                tc::st32(tO + ch * 32, ov);
+              }
+            }
+          };
+          // Values of a tile that is not seen whole, by the run's first query tile
+          // (the other's product follows): clear what no row of the run sees, and
+          // what is not finite, noting the tile.
+          auto clear_values = [&]() {
+            if (full || q > 0) return true;
+            const int s = g % kStages;
+            if (!wait_warp(bar(BI::kVFull + s), (g / kStages) & 1)) return false;
+            const uint32_t vb = sV + s * kTile;
+            bool odd = false;
+#pragma unroll 4
+            for (int e = r; e < kTK * kHalves * 8; e += kRows) {  // 16-byte chunks
+              const int row = e / (kHalves * 8), rem = e % (kHalves * 8), key = k0 + row;
+              const uint32_t at = vb + (rem / 8) * Lay::kHalf + row * 128 + (rem % 8) * 16;
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                           : "r"(at));
+              const bool hidden = key >= x.hi || (key < x.lo && key >= x.sink_end);
+              const bool bad = not_finite(w[0]) || not_finite(w[1]) || not_finite(w[2]) || not_finite(w[3]);
+              if (hidden || bad) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (hidden || (w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u;
+                  if (hidden || (w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0x0000FFFFu;
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+                odd |= !hidden;
+              }
+            }
+            if (odd) atomicMax(odd_tile, g + 1);  // the other slot may be ahead, or behind
+            return true;
+          };
+          // make this thread's P (tensor memory) and cleared values (shared memory)
+          // visible to the P V issuer, then count in at barrier bi
+          auto publish = [&](int bi) {
+            tc::wait_st();
+            fence_proxy_async_shared();
+            tc::fence_before();
+            mbar_arrive(bar(bi));
+          };
+          // this slot's previous P V product must be complete before its weights'
+          // columns and its accumulator are written
+          auto previous_pv_done = [&]() {
+            if (n_tiles > 1 && !wait_warp(bar(BI::kPvDone + slot), (n_tiles - 2) & 1)) return false;
+            tc::fence_after();
+            return true;
+          };
+          tc::fence_after();
+          if (__all_sync(0xffffffffu, see_lo == 0 && see_hi == 0)) {  // no row of the warp sees any of the tile
+            tc::fence_before();
+            mbar_arrive(bar(BI::kSFree));
+            if (!previous_pv_done()) { ok = false; break; }
+            uint32_t z[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) z[k] = 0u;
+            tc::st32(tPr, z);
+            tc::st32(tPr + 32, z);
+            if (!clear_values()) { ok = false; break; }
+            publish(BI::kPFull + slot);
+            mbar_arrive(bar(BI::kPLo + slot));
+          } else {
+            // the row's 128 scores in one load round; once they are in registers the
+            // next score product may overwrite them
+            uint32_t sl[64], sh[64];
+            tc::ld32(tSr, *reinterpret_cast<uint32_t(*)[32]>(&sl[0]));
+            tc::ld32(tSr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sl[32]));
+            tc::ld32(tSr + 64, *reinterpret_cast<uint32_t(*)[32]>(&sh[0]));
+            tc::ld32(tSr + 96, *reinterpret_cast<uint32_t(*)[32]>(&sh[32]));
+            tc::wait_ld();
+            tc::fence_before();
+            mbar_arrive(bar(BI::kSFree));
+            if (!full) {
+              mask(sl, see_lo);
+              mask(sh, see_hi);
+            }
+            const float el = extreme64(sl, neg), eh = extreme64(sh, neg);
+            const float msub = new_reference(neg ? fminf(el, eh) : fmaxf(el, eh));
+            const uint64_t ks2 = f32x2_bits(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
+            const uint64_t nm2 = f32x2_bits(__float_as_uint(-msub), __float_as_uint(-msub));
+            // keys 64..127 first: their P V product starts while keys 0..63 are weighted
+            uint32_t pk[32];
+            float lsum = weights64(sh, ks2, nm2, pk);
+            if (!previous_pv_done()) { ok = false; break; }
+            tc::st32(tPr + 32, pk);
+            // none of this tile's P V products is issued before kPFull: the accumulator
+            // holds its final value and may be rescaled here
+            rescale_o();
+            if (!clear_values()) { ok = false; break; }
+            publish(BI::kPFull + slot);
+            lsum += weights64(sl, ks2, nm2, pk);
+            tc::st32(tPr, pk);
+            tc::wait_st();
+            tc::fence_before();
+            mbar_arrive(bar(BI::kPLo + slot));
+            l += lsum;
+          }
+        }
+        if (!ok) break;
+        // ---- end of the piece: normalise and store the rows, or store the partial
+        if (any) {
+          if (!wait_warp(bar(BI::kOFull + slot), use & 1)) { ok = false; break; }
+          tc::fence_after();
+        }
+        const float inv = any && l > 0.f ? 1.f / l : 0.f;
+        const bool whole = x.whole();
+        const size_t orow = (static_cast<size_t>(qs[x.seq]) + token) * p.num_q_heads + x.head * p.group + gh;
+        const size_t piece = 2 * static_cast<size_t>(blockIdx.x) + (x.t0 == 0 ? 1 : 0);
+        const int prow = q * kRows + r;
+        const bool odd = any && *reinterpret_cast<volatile int *>(odd_tile) > g0;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          __syncwarp();
+          uint32_t ov[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) ov[k] = 0u;
+          if (any) {
+            tc::ld32(tO + ch * 32, ov);
+            tc::wait_ld();
+          }
+          if (odd && row_valid) {
+            // add the values that were cleared because they are not finite, where this row sees them
+            for (int t = x.t0; t < x.t1; ++t) {
+              const int k0 = x.key0(t);
+              if ((k0 >= all_lo && k0 + kTK <= all_hi) || k0 + kTK <= all_sinks) continue;
+              for (int k = 0; k < kTK; ++k) {
+                if (!((sight.of(k0 + (k & 64)) >> (k & 63)) & 1)) continue;
+                const int b = p.block_tables[static_cast<size_t>(x.seq) * p.max_blocks + (k0 + k) / BS];
+                if (b < 0 || b >= p.num_blocks) continue;
+                const uint32_t *row = reinterpret_cast<const uint32_t *>(
+                    p.v_cache + ((static_cast<size_t>(b) * hkv + x.head) * BS + (k0 + k) % BS) * D + ch * 32);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const uint32_t w = row[i];
+                  if ((w & 0x7F80u) == 0x7F80u) ov[2 * i] = __float_as_uint(__uint_as_float(ov[2 * i]) + __uint_as_float(w << 16));
+                  if ((w & 0x7F800000u) == 0x7F800000u)
+                    ov[2 * i + 1] = __float_as_uint(__uint_as_float(ov[2 * i + 1]) + __uint_as_float(w & 0xFFFF0000u));
+                }
+              }
+            }
+          }
+          if (!row_valid) continue;
+          if (!whole) {
+#pragma unroll
+            for (int c4 = 0; c4 < 8; ++c4)
+              p.ws_o[(piece * (D / 4) + ch * 8 + c4) * p.piece_rows + prow] =
+                  make_float4(__uint_as_float(ov[c4 * 4]), __uint_as_float(ov[c4 * 4 + 1]), __uint_as_float(ov[c4 * 4 + 2]),
+                              __uint_as_float(ov[c4 * 4 + 3]));
+            continue;
+          }
+          // a thread writes its own row: 32-byte stores (when the output allows) halve the requests
+          __nv_bfloat16 *dst = p.out + orow * D + ch * 32;
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(__uint_as_float(ov[2 * k]) * inv, __uint_as_float(ov[2 * k + 1]) * inv);
+          if ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
+#pragma unroll
+            for (int h8 = 0; h8 < 2; ++h8) st_global_v8(dst + h8 * 16, &w[8 * h8]);
+          } else {
+#pragma unroll
+            for (int c8 = 0; c8 < 4; ++c8)
+              reinterpret_cast<uint4 *>(dst)[c8] = make_uint4(w[4 * c8], w[4 * c8 + 1], w[4 * c8 + 2], w[4 * c8 + 3]);
+          }
+        }
+        if (any) {
+          tc::fence_before();
+          mbar_arrive(bar(BI::kOFree + slot));
+        }
+        if (!whole && row_valid) p.ws_ml[piece * p.piece_rows + prow] = make_float2(m, l);
+      }
+      if (!ok) timed_out();
+    }
+  }
+  // this CTA's pieces, for the join
+  if (p.ws_desc && threadIdx.x == 32 * kVWarp) {
+    int4 d = make_int4(0, 0, 0, 0);
+    Sched w;
+    for (w.begin(p, tab, ctas); !w.done; w.next(p, tab)) {
+      const Run &x = w.x;
+      if (x.whole()) continue;
+      if (x.t0 > 0 && x.t1 == x.n) d.z |= kEnds;
+      if (x.t0 == 0) {
+        d.x = x.seq | (x.head << 16);
+        d.y = x.r0;
+        d.z |= kLeaves;
+      }
+    }
+    p.ws_desc[blockIdx.x] = d;
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::dealloc(tmem, kTmemCols);
+  }
+}
+
+// One block per CTA whose last run leaves it and per share of the head dim: the
+// exact merge of the run's pieces, a thread per query row.
+//   out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M),  M = max_p m_p
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) spans_join_kernel(const Params p, int grid) {
+  grid_launch_dependents();
+  grid_dependency_wait();  // the pieces come from the grid launched just before
+  const int4 d = p.ws_desc[blockIdx.x];
+  if (!(d.z & kLeaves)) return;
+  __shared__ int last_cta;
+  if (threadIdx.x < 32) {  // the first CTA after this one in which the run ends
+    int found = -1;
+    for (int base = blockIdx.x + 1; base < grid && found < 0; base += 32) {
+      const int c = base + threadIdx.x;
+      const unsigned ends = __ballot_sync(0xffffffffu, c < grid && (p.ws_desc[c].z & kEnds));
+      if (ends) found = base + __ffs(ends) - 1;
+    }
+    if (threadIdx.x == 0) last_cta = found;
+  }
+  __syncthreads();
+  if (last_cta < 0) return;  // only where a bounded wait gave up
+  const int seq = d.x & 0xffff, head = d.x >> 16;
+  const int a = p.q_start[seq], c = p.q_start[seq + 1] - a;
+  const int pieces = last_cta - static_cast<int>(blockIdx.x) + 1;
+  for (int prow = threadIdx.x; prow < p.piece_rows; prow += blockDim.x) {
+    const int q = prow / kRows, r = prow % kRows, tok = r / p.group, gh = r - tok * p.group;
+    const int token = d.y + q * p.tile_tok + tok;
+    if (tok >= p.tile_tok || token >= c || token >= d.y + p.span) continue;
+    // piece 1 of the first CTA, piece 0 of the others
+    auto slot = [&](int i) { return 2 * (static_cast<size_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
+    float M = -INFINITY;
+    for (int i = 0; i < pieces; ++i) M = fmaxf(M, p.ws_ml[slot(i) * p.piece_rows + prow].x);
+    constexpr int kCols = D / 4 / 8;  // float4 columns of this block (8 blocks share the head dim)
+    float4 acc[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+      const float2 ml = p.ws_ml[slot(i) * p.piece_rows + prow];
+      // an empty piece (max -inf) weighs nothing, and its O was not written
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      den += ml.y * f;
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) {
+        const float4 o = f != 0.f ? p.ws_o[(slot(i) * (D / 4) + blockIdx.y * kCols + k) * p.piece_rows + prow]
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        acc[k].x += f * o.x;
+        acc[k].y += f * o.y;
+        acc[k].z += f * o.z;
+        acc[k].w += f * o.w;
+      }
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    uint2 *dst = reinterpret_cast<uint2 *>(p.out + ((static_cast<size_t>(a) + token) * p.num_q_heads + head * p.group + gh) * D) +
+                 blockIdx.y * kCols;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+      dst[k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+  }
+}
+
+// ------------------------------------------------------------------ host
+struct Plan {
+  int group, tile_tok, span, piece_rows;
+  bool split;  // some run may be cut
+  size_t o_bytes, ml_bytes, desc_bytes;
+  size_t bytes() const { return split ? o_bytes + ml_bytes + desc_bytes : 0; }
+};
+
+Plan make_plan(const Call &a) {
+  Plan plan{};
+  plan.group = a.num_q_heads / a.num_kv_heads;
+  plan.tile_tok = kRows / plan.group;
+  const int longest = a.mask ? a.max_nodes : a.total_q;  // tokens of a chunk or tree, at most
+  plan.tile_tok = std::min(plan.tile_tok, std::max(1, longest));
+  plan.span = longest > plan.tile_tok ? 2 * plan.tile_tok : plan.tile_tok;
+  plan.piece_rows = plan.span > plan.tile_tok ? 2 * kRows : kRows;
+  // a run of fewer tiles than two least pieces is never cut
+  long long keys = a.max_seq_len;
+  if (!a.mask) {
+    const long long sunk = (static_cast<long long>(a.sinks) + kTK - 1) / kTK * kTK;
+    keys = std::min(keys, static_cast<long long>(a.window) + plan.span + 2 * kTK + sunk);
+  }
+  plan.split = (keys + kTK - 1) / kTK >= 2 * kMinPiece;
+  const size_t pieces = 2 * static_cast<size_t>(num_sms());
+  plan.o_bytes = pieces * plan.piece_rows * a.head_dim * sizeof(float);
+  plan.ml_bytes = pieces * plan.piece_rows * sizeof(float2);
+  plan.desc_bytes = static_cast<size_t>(num_sms()) * sizeof(int4);
+  return plan;
+}
+
+using KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Params);
+
+template <int D>
+KernelFn pick_kernel(int block_size) {
+  switch (block_size) {
+    case 16: return spans_tc_kernel<16, D>;
+    case 32: return spans_tc_kernel<32, D>;
+    case 64: return spans_tc_kernel<64, D>;
+    default: return spans_tc_kernel<128, D>;
+  }
+}
+
+template <int D>
+int launch(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const Params &p, int block_size,
+           bool split, cudaStream_t stream) {
+  const KernelFn kernel = pick_kernel<D>(block_size);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem_bytes<D>(kMaxSeqs)));
+  const unsigned grid = static_cast<unsigned>(num_sms());
+  if (e == cudaSuccess) e = launch_overlapped(kernel, grid, kThreads, smem_bytes<D>(p.num_seqs), stream, tmq, tmk, tmv, p);
+  if (e == cudaSuccess && split)
+    e = launch_overlapped(spans_join_kernel<D>, dim3(grid, 8), kJoinThreads, 0, stream, p, static_cast<int>(grid));
+  return e == cudaSuccess ? PKV_OK : (set_cuda_error(e), PKV_ERR_CUDA);
+}
+
+}  // namespace
+
+size_t tc_workspace_size(const Call &a) { return make_plan(a).bytes(); }
+
+int tc_launch(const Call &a) {
+  const Plan plan = make_plan(a);
+  if (plan.bytes() > 0 && (!a.workspace || a.workspace_bytes < plan.bytes() || !aligned16(a.workspace)))
+    return PKV_ERR_WORKSPACE;
+  const long long rows = static_cast<long long>(a.num_blocks) * a.num_kv_heads * a.block_size;
+  CUtensorMap tmq, tmk, tmv;
+  // q viewed as [total_q][Hq][d]: a box is 64 columns x G heads x the tile's tokens
+  if (!make_tensor_map_3d(&tmq, a.q, a.head_dim, a.num_q_heads, a.total_q, 64, plan.group, plan.tile_tok) ||
+      !make_tensor_map_2d(&tmk, a.k_cache, a.head_dim, rows, 64, a.block_size) ||
+      !make_tensor_map_2d(&tmv, a.v_cache, a.head_dim, rows, 64, a.block_size))
+    return PKV_ERR_CUDA;
+  Params p{};
+  p.block_tables = a.block_tables;
+  p.seq_lens = a.seq_lens;
+  p.q_start = a.q_start;
+  p.mask = a.mask;
+  p.v_cache = reinterpret_cast<const __nv_bfloat16 *>(a.v_cache);
+  p.out = reinterpret_cast<__nv_bfloat16 *>(a.out);
+  if (plan.split) {
+    char *ws = static_cast<char *>(a.workspace);
+    p.ws_o = reinterpret_cast<float4 *>(ws);
+    p.ws_ml = reinterpret_cast<float2 *>(ws + plan.o_bytes);
+    p.ws_desc = reinterpret_cast<int4 *>(ws + plan.o_bytes + plan.ml_bytes);
+  }
+  p.status = a.status;
+  p.num_seqs = a.num_seqs;
+  p.max_blocks = a.max_blocks;
+  p.num_q_heads = a.num_q_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.num_blocks = a.num_blocks;
+  p.total_q = a.total_q;
+  p.max_len = a.max_seq_len;
+  p.oob_row = static_cast<int>(rows);
+  p.group = plan.group;
+  p.tile_tok = plan.tile_tok;
+  p.span = plan.span;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.max_nodes = a.max_nodes;
+  p.piece_rows = plan.piece_rows;
+  p.scale_log2 = kernel_scale_log2(a.scale);
+  return a.head_dim == 64 ? launch<64>(tmq, tmk, tmv, p, a.block_size, plan.split, as_stream(a.stream))
+                          : launch<128>(tmq, tmk, tmv, p, a.block_size, plan.split, as_stream(a.stream));
+}
+
+}  // namespace spans
+}  // namespace pkv
