@@ -37,8 +37,10 @@
 // rows that do see one add it when they are written out (rare).
 //
 // Warp roles: 0-3 and 4-7 softmax of slot 0 and 1 (thread = row), 8 TMA producer of
-// queries and keys, 9 score-product issuer (one lane) and tensor-memory owner, 10
-// P V product issuer (one lane), 11 TMA producer of values.
+// queries and keys, which also finds the CTA's runs and hands them to the others
+// through a ring of descriptors in shared memory, 9 score-product issuer (one
+// lane) and tensor-memory owner, 10 P V product issuer (one lane), 11 TMA producer
+// of values.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -69,6 +71,11 @@ constexpr int kRunCost = 256;    // a run's start and end, in keys
 constexpr int kMinRange = 512;   // least weight of a CTA's range, in keys
 constexpr int kMinPiece = 2;     // key tiles that a border leaves on either side
 constexpr int kJoinThreads = 256;
+constexpr int kRunRing = 4;      // descriptors of runs ahead
+constexpr int kRunUsers = 11;    // arrivals that free one: 8 softmax warps, two issuers, the value producer
+// registers a thread of the softmax warps and of the others: 128 (2 x 200 + 104)
+// is what the block is launched with (384 x 168)
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 
 template <int D>
 struct Layout {
@@ -89,15 +96,18 @@ struct Layout {
 template <int ST>
 struct Bar {
   static constexpr int kQFull = 0, kQFree = 2, kOFull = 4, kOFree = 6, kSFull = 8, kPFull = 10, kPLo = 12, kPvDone = 14,
-                       kSFree = 16, kKFull = 17, kKEmpty = kKFull + ST, kVFull = kKEmpty + ST, kVEmpty = kVFull + ST,
+                       kSFree = 16, kRunFull = 17, kRunFree = kRunFull + kRunRing, kKFull = kRunFree + kRunRing, kKEmpty = kKFull + ST, kVFull = kKEmpty + ST, kVEmpty = kVFull + ST,
                        kCount = kVEmpty + ST;
 };
+
+// A run's descriptor: the fields of Run in this order.
+constexpr int kRunInts = 12;
 
 template <int D>
 constexpr size_t smem_bytes(int num_seqs) {
   using Lay = Layout<D>;
-  return 1024 + Lay::kSmemBars + Bar<Lay::kStages>::kCount * 8 + 16 + static_cast<size_t>(num_seqs + 1) * 8 +
-         static_cast<size_t>(num_seqs) * 12;
+  return 1024 + Lay::kSmemBars + Bar<Lay::kStages>::kCount * 8 + 16 + kRunRing * kRunInts * 4 +
+         static_cast<size_t>(num_seqs + 1) * 8 + static_cast<size_t>(num_seqs) * 12;
 }
 static_assert(smem_bytes<128>(kMaxSeqs) <= 227 * 1024, "shared memory");
 
@@ -134,6 +144,7 @@ struct SeqTab {
 struct Weights {
   long long base, flat, bent;
   int span, runs;
+  __device__ Weights() {}
   __device__ Weights(const Params &p, int L, int c) {
     span = p.span;
     runs = ceil_div(c, span);
@@ -170,22 +181,30 @@ struct Weights {
 // A CTA's piece of a run: key tiles [t0, t1) of its n.  Tile v starts at key
 // 128 v (the sinks', v < ns) or 128 (v - ns + t_lo).
 struct Run {
-  int seq, head, r0, ntq;  // first query token, query tiles
+  int seq, head, r0, ntq;  // first query token, query tiles (0: no further run)
   int lo, hi, sink_end;    // the run sees nothing outside [lo, hi) and [0, sink_end)
   int ns, t_lo, n, t0, t1;
   __device__ bool whole() const { return t0 == 0 && t1 == n; }
   __device__ int key0(int v) const { return kTK * (v < ns ? v : v - ns + t_lo); }
+  __device__ void put(volatile int *d) const {
+    d[0] = seq, d[1] = head, d[2] = r0, d[3] = ntq, d[4] = lo, d[5] = hi, d[6] = sink_end, d[7] = ns, d[8] = t_lo;
+    d[9] = n, d[10] = t0, d[11] = t1;
+  }
+  __device__ void get(const volatile int *d) {
+    seq = d[0], head = d[1], r0 = d[2], ntq = d[3], lo = d[4], hi = d[5], sink_end = d[6], ns = d[7], t_lo = d[8];
+    n = d[9], t0 = d[10], t1 = d[11];
+  }
 };
 
-// The runs of this CTA in order (every role walks the same sequence).
+// The runs of this CTA in order.
 struct Sched {
   long long xa, xb, s;  // the CTA's range; the current run's start
   int seq, head, i;
   bool done;
+  Weights w;  // of the current sequence
   Run x;
 
-  // true: there is a first run
-  __device__ bool begin(const Params &p, const SeqTab &t, int ctas) {
+  __device__ void begin(const Params &p, const SeqTab &t, int ctas) {
     const long long total = t.prefix[p.num_seqs];
     xa = xb = 0;
     if (static_cast<int>(blockIdx.x) < ctas) {
@@ -193,29 +212,27 @@ struct Sched {
       xb = total * (blockIdx.x + 1) / ctas;
     }
     done = xa >= xb;
-    if (done) return false;
+    if (done) return;
     int lo = 0, hi = p.num_seqs;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (t.prefix[mid] <= xa) lo = mid; else hi = mid;
     }
     seq = lo;
-    const Weights w(p, t.lens[seq], t.qc[seq]);
+    w = Weights(p, t.lens[seq], t.qc[seq]);
     const long long per_head = w.sum(w.runs), off = xa - t.prefix[seq];
     head = static_cast<int>(off / per_head);
     i = w.find(off - head * per_head);
     s = t.prefix[seq] + head * per_head + w.sum(i);
-    return settle(p, t);
+    settle(p, t);
   }
-  // the next run of the CTA; false: there is none
-  __device__ bool next(const Params &p, const SeqTab &t) {
+  __device__ void next(const Params &p, const SeqTab &t) {
     step(p, t);
-    return settle(p, t);
+    settle(p, t);
   }
 
  private:
   __device__ void step(const Params &p, const SeqTab &t) {
-    const Weights w(p, t.lens[seq], t.qc[seq]);
     s += w.of(i);
     if (++i < w.runs) return;
     i = 0;
@@ -223,25 +240,24 @@ struct Sched {
     head = 0;
     do ++seq;
     while (seq < p.num_seqs && t.qc[seq] == 0);
+    if (seq < p.num_seqs) w = Weights(p, t.lens[seq], t.qc[seq]);
   }
   // from the current run on: the first that this CTA has a piece of
-  __device__ bool settle(const Params &p, const SeqTab &t) {
+  __device__ void settle(const Params &p, const SeqTab &t) {
     for (; s < xb && seq < p.num_seqs; step(p, t)) {
-      const int L = t.lens[seq], c = t.qc[seq];
-      geometry(p, L, c);
-      const long long w = Weights(p, L, c).of(i);
-      x.t0 = xa <= s ? 0 : border(xa - s, w);
-      x.t1 = xb >= s + w ? x.n : border(xb - s, w);
+      geometry(p, t.lens[seq], t.qc[seq]);
+      const long long weight = w.of(i);
+      x.t0 = xa <= s ? 0 : border(xa - s, weight);
+      x.t1 = xb >= s + weight ? x.n : border(xb - s, weight);
       // a run without keys belongs to the CTA that holds its start; a range
       // inside a tile is an empty piece, which the join expects
       const bool mine = x.n == 0 ? xa <= s : x.t0 < x.t1 || (x.t0 > 0 && x.t0 < x.n);
-      if (mine) return true;
+      if (mine) return;
     }
     done = true;
-    return false;
   }
-  __device__ int border(long long at, long long w) const {
-    const int o = static_cast<int>(at * x.n / w);
+  __device__ int border(long long at, long long weight) const {
+    const int o = static_cast<int>(at * x.n / weight);
     return o < kMinPiece ? 0 : o > x.n - kMinPiece ? x.n : o;
   }
   __device__ void geometry(const Params &p, int L, int c) {
@@ -312,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + BI::kCount);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *odd_tile = reinterpret_cast<int *>(tmem_slot + 2);  // 1 + the last key tile (counted over the CTA) whose values are not all finite
-  long long *prefix = reinterpret_cast<long long *>(bars + BI::kCount + 2);  // [B + 1]
+  volatile int *runs = reinterpret_cast<volatile int *>(bars + BI::kCount + 2);  // [kRunRing][kRunInts]
+  long long *prefix = reinterpret_cast<long long *>(bars + BI::kCount + 2 + kRunRing * kRunInts / 2);  // [B + 1]
   int *lens = reinterpret_cast<int *>(prefix + p.num_seqs + 1);              // [B]
   int *qs = lens + p.num_seqs, *qc = qs + p.num_seqs;                        // [B] each
   const SeqTab tab{prefix, lens, qs, qc};
@@ -368,6 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(BI::kPvDone + i), 1);
     }
     mbar_init(bar(BI::kSFree), kRows);
+    for (int i = 0; i < kRunRing; ++i) {
+      mbar_init(bar(BI::kRunFull + i), 1);
+      mbar_init(bar(BI::kRunFree + i), kRunUsers);
+    }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(BI::kKFull + s), 1);
       mbar_init(bar(BI::kKEmpty + s), 1);
@@ -399,17 +420,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + Lay::kSmemK), sV = smem_u32(smem + Lay::kSmemV);
   const uint32_t tS = tmem + Lay::kTmemS, tP = tmem + Lay::kTmemP;
-  const int ctas = active_ctas(prefix[B]);
-  Sched sc;
-  sc.begin(p, tab, ctas);
   auto timed_out = [&] {
     if (p.status) atomicOr(p.status, PKV_STATUS_TIMEOUT);
     *abort_flag = 1;
   };
+  // the CTA's j-th run, once its descriptor is there; ntq 0: there is none (or a wait gave up)
+  auto run_at = [&](int j, Run &x) {
+    if (mbar_wait(bar(BI::kRunFull + j % kRunRing), (j / kRunRing) & 1)) x.get(runs + (j % kRunRing) * kRunInts);
+    else x.ntq = 0;
+  };
+  auto run_done = [&](int j) { mbar_arrive(bar(BI::kRunFree + j % kRunRing)); };
 
-  if (!sc.done) {
+  if (warp >= kKWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kKWarp || warp == kVWarp) {
-      // ------------------------------------------- producers: K (+ Q), V
+      // ------------------------------------- producers: runs, K (+ Q); V
       const bool is_v = warp == kVWarp;
       const CUtensorMap *tm = is_v ? &tmv : &tmk;
       const uint32_t ring = is_v ? sV : sK;
@@ -418,10 +443,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pol = p.mask && p.max_nodes <= p.span ? l2_policy_evict_first() : l2_policy_evict_normal();
       int g = 0, nq = 0;  // key tiles and query tiles so far
       int tw_seq = -1, tw_base = 0, tw_val = -1;
-      for (; !sc.done && !*abort_flag; sc.next(p, tab)) {
-        const Run &x = sc.x;
-        if (x.t0 >= x.t1) continue;
-        if (!is_v) {
+      Sched sc;
+      int4 desc = make_int4(0, 0, 0, 0);  // this CTA's pieces, for the join
+      if (!is_v) sc.begin(p, tab, active_ctas(prefix[B]));
+      for (int j = 0; !*abort_flag; ++j) {
+        Run x;
+        if (is_v) {
+          run_at(j, x);
+          __syncwarp();
+        } else {
+          if (sc.done) sc.x.ntq = 0;
+          x = sc.x;
+          if (j >= kRunRing && !wait_warp(bar(BI::kRunFree + j % kRunRing), (j / kRunRing - 1) & 1)) {
+            if (lane == 0) timed_out();
+            break;
+          }
+          if (lane == 0) {
+            x.put(runs + (j % kRunRing) * kRunInts);
+            mbar_arrive(bar(BI::kRunFull + j % kRunRing));
+          }
+          if (!sc.done) sc.next(p, tab);
+        }
+        if (x.ntq == 0) break;
+        if (!is_v && !x.whole()) {
+          if (x.t0 > 0 && x.t1 == x.n) desc.z |= kEnds;
+          if (x.t0 == 0) {
+            desc.x = x.seq | (x.head << 16);
+            desc.y = x.r0;
+            desc.z |= kLeaves;
+          }
+        }
+        if (!is_v && x.t0 < x.t1) {
           bool ok = true;
           for (int q = 0; q < x.ntq && ok; ++q, ++nq) {
             const int slot = nq & 1, use = nq >> 1;
@@ -457,24 +509,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), kTile);
           // one lane per (box, half): the box copies go out in parallel
-          const int j = lane / kHalves, hf = lane % kHalves;
-          const int b = __shfl_sync(0xffffffffu, tw_val, (blk + min(j, kBoxes - 1) - tw_base) & 31);
-          if (j < kBoxes) {
-            const int kb = k0 + j * BS;  // the block's first key
+          const int jb = lane / kHalves, hf = lane % kHalves;
+          const int b = __shfl_sync(0xffffffffu, tw_val, (blk + min(jb, kBoxes - 1) - tw_base) & 31);
+          if (jb < kBoxes) {
+            const int kb = k0 + jb * BS;  // the block's first key
             const bool seen = kb < x.hi && (kb + BS > x.lo || kb < x.sink_end);
             int row = p.oob_row;  // no row of the run sees the block, or a bad id: zeros
             if (seen && b >= 0 && b < p.num_blocks) row = (b * hkv + x.head) * BS;
             else if (seen && p.status && !is_v && hf == 0) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
-            tma_load_2d(ring + s * kTile + hf * Lay::kHalf + j * BS * 128, tm, hf * 64, row, bar(full0 + s), pol);
+            tma_load_2d(ring + s * kTile + hf * Lay::kHalf + jb * BS * 128, tm, hf * 64, row, bar(full0 + s), pol);
           }
         }
+        if (is_v && lane == 0) run_done(j);
       }
       // never leave a copy in flight into this CTA's shared memory
       if (lane == 0) {
         for (int y = g > kStages ? g - kStages : 0; y < g; ++y)
           mbar_wait_sleep(bar(full0 + (y % kStages)), (y / kStages) & 1);
-        if (!is_v)
+        if (!is_v) {
           for (int y = nq > 2 ? nq - 2 : 0; y < nq; ++y) mbar_wait_sleep(bar(BI::kQFull + (y & 1)), (y >> 1) & 1);
+          if (p.ws_desc) p.ws_desc[blockIdx.x] = desc;
+        }
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------- S = Q K^T issuer
@@ -485,8 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kIdS = tc::idesc_bf16(kRows, kTK, false, false);
         int g = 0, nq = 0, np = 0;  // key tiles, query tiles, products so far
         bool ok = true;
-        for (; !sc.done && ok; sc.next(p, tab)) {
-          const Run &x = sc.x;
+        for (int j = 0; ok; ++j) {
+          Run x;
+          run_at(j, x);
+          if (x.ntq == 0) break;
+          run_done(j);
           if (x.t0 >= x.t1) continue;
           for (int t = x.t0; t < x.t1 && ok; ++t, ++g) {
             const int s = g % kStages;
@@ -521,8 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kSteps = kTK / 16;  // 16 keys = 8 packed columns of P
         int g = 0, nq = 0, n[2] = {0, 0};  // key tiles, query tiles, each slot's products
         bool ok = true;
-        for (; !sc.done && ok; sc.next(p, tab)) {
-          const Run &x = sc.x;
+        for (int j = 0; ok; ++j) {
+          Run x;
+          run_at(j, x);
+          if (x.ntq == 0) break;
+          run_done(j);
           if (x.t0 >= x.t1) continue;
           for (int t = x.t0; t < x.t1 && ok; ++t, ++g) {
             const int vs = g % kStages;
@@ -556,19 +617,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) timed_out();
       }
-    } else {
-      // ------------------------------------------------------ softmax warps
+    }
+  } else {
+    // ------------------------------------------------------ softmax warps
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    {
       const int slot = warp >> 2;
       const int r = threadIdx.x & (kRows - 1);  // query row = TMEM lane
-      const int tok = r / p.group, gh = r - tok * p.group;
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tO = tmem + slot * D + lane_off, tSr = tS + lane_off, tPr = tP + slot * (kTK / 2) + lane_off;
       const bool neg = p.scale_log2 < 0.f;  // a negative scale turns the largest score into the smallest
       const uint32_t masked = __float_as_uint(neg ? INFINITY : -INFINITY);
       int g = 0, nq = 0, n_tiles = 0;  // key tiles and query tiles of the CTA, key tiles of this slot
       bool ok = true;
-      for (; !sc.done && ok; sc.next(p, tab)) {
-        const Run &x = sc.x;
+      for (int j = 0; ok; ++j) {
+        Run x;
+        run_at(j, x);
+        __syncwarp();
+        if (x.ntq == 0) break;
         const bool any = x.t0 < x.t1;
         // the run's query tile in this slot: without keys (nothing goes through the
         // slots) tile `slot` of the run
@@ -576,10 +642,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any) nq += x.ntq;
         if (q >= x.ntq) {
           g += x.t1 - x.t0;
+          if (lane == 0) run_done(j);
           continue;
         }
-        const int L = lens[x.seq], c = qc[x.seq], ctx = L - c;
-        const int token = x.r0 + q * p.tile_tok + tok;
+        const int c = qc[x.seq], ctx = lens[x.seq] - c;
+        const int tok = r / p.group, token = x.r0 + q * p.tile_tok + tok;
         const bool row_valid = tok < p.tile_tok && token < c;
         RowSight sight;
         sight.tree = p.mask != nullptr;
@@ -750,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float inv = any && l > 0.f ? 1.f / l : 0.f;
         const bool whole = x.whole();
-        const size_t orow = (static_cast<size_t>(qs[x.seq]) + token) * p.num_q_heads + x.head * p.group + gh;
+        const size_t orow = (static_cast<size_t>(qs[x.seq]) + token) * p.num_q_heads + x.head * p.group + (r - tok * p.group);
         const size_t piece = 2 * static_cast<size_t>(blockIdx.x) + (x.t0 == 0 ? 1 : 0);
         const int prow = q * kRows + r;
         const bool odd = any && *reinterpret_cast<volatile int *>(odd_tile) > g0;
@@ -813,25 +880,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(bar(BI::kOFree + slot));
         }
         if (!whole && row_valid) p.ws_ml[piece * p.piece_rows + prow] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) run_done(j);
       }
       if (!ok) timed_out();
     }
-  }
-  // this CTA's pieces, for the join
-  if (p.ws_desc && threadIdx.x == 32 * kVWarp) {
-    int4 d = make_int4(0, 0, 0, 0);
-    Sched w;
-    for (w.begin(p, tab, ctas); !w.done; w.next(p, tab)) {
-      const Run &x = w.x;
-      if (x.whole()) continue;
-      if (x.t0 > 0 && x.t1 == x.n) d.z |= kEnds;
-      if (x.t0 == 0) {
-        d.x = x.seq | (x.head << 16);
-        d.y = x.r0;
-        d.z |= kLeaves;
-      }
-    }
-    p.ws_desc[blockIdx.x] = d;
   }
   tc::fence_before();
   __syncthreads();
