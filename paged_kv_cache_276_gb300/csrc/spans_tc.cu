@@ -4,10 +4,10 @@
 // For one KV head, a query tile of 128 rows holds up to 128 / G tokens x the G
 // query heads of the group (row r = token r / G, head r % G).  Over each tile of
 // 128 keys that some row sees:
-//     S  = Q K^T                     tcgen05.mma, M 128 x N 128 x K d -> TMEM
+//     S  = Q K^T                     tcgen05.mma, M 128 x N 64 x K d, twice -> TMEM
 //     P  = exp2(S * scale*log2e - m)  softmax warps, one query row per thread,
-//                                    bf16 in TMEM
-//     O += P V                       tcgen05.mma, M 128 x N d x K 128 -> TMEM
+//                                    64 keys at a time, bf16 in TMEM
+//     O += P V                       tcgen05.mma, M 128 x N d x K 64, twice -> TMEM
 // with the running max / sum of the online softmax.  What a row sees of a tile is
 // two 64-bit words, from the window's bounds or from the tree's mask: a key whose
 // bit is clear gets the score -inf.
@@ -32,9 +32,10 @@
 // tile the next run starts in the other slot while this one is written out.
 //
 // Values that a row does not see must not reach it, and 0 times NaN or infinity is
-// NaN: in a tile that is not seen whole, values no row of the run sees are
-// zeroed in shared memory and those that are not finite are zeroed and noted; the
-// rows that do see one add it when they are written out (rare).
+// NaN: in a tile that is not seen whole, the P V issuer's warp clears the values no
+// row of the run sees and those that are not finite, in shared memory, while the
+// tile's weights are computed; a tile with any of the latter is noted, and the rows
+// that do see one add it when they are written out (rare).
 //
 // Warp roles: 0-3 and 4-7 softmax of slot 0 and 1 (thread = row), 8 TMA producer of
 // queries and keys, which also finds the CTA's runs and hands them to the others
@@ -73,9 +74,6 @@ constexpr int kMinPiece = 2;     // key tiles that a border leaves on either sid
 constexpr int kJoinThreads = 256;
 constexpr int kRunRing = 4;      // descriptors of runs ahead
 constexpr int kRunUsers = 11;    // arrivals that free one: 8 softmax warps, two issuers, the value producer
-// registers a thread of the softmax warps and of the others: 128 (2 x 200 + 104)
-// is what the block is launched with (384 x 168)
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 
 template <int D>
 struct Layout {
@@ -95,8 +93,9 @@ struct Layout {
 // barrier indices (8 bytes each)
 template <int ST>
 struct Bar {
-  static constexpr int kQFull = 0, kQFree = 2, kOFull = 4, kOFree = 6, kSFull = 8, kPFull = 10, kPLo = 12, kPvDone = 14,
-                       kSFree = 16, kRunFull = 17, kRunFree = kRunFull + kRunRing, kKFull = kRunFree + kRunRing, kKEmpty = kKFull + ST, kVFull = kKEmpty + ST, kVEmpty = kVFull + ST,
+  static constexpr int kQFull = 0, kQFree = 2, kOFull = 4, kOFree = 6,
+                       kPFull = 8, kPvDone = 12, kSFull = 16,  // [slot][half]
+                       kSFree = 20, kRunFull = 22, kRunFree = kRunFull + kRunRing, kKFull = kRunFree + kRunRing, kKEmpty = kKFull + ST, kVFull = kKEmpty + ST, kVEmpty = kVFull + ST,
                        kCount = kVEmpty + ST;
 };
 
@@ -123,7 +122,8 @@ struct Params {
   int num_seqs, max_blocks, num_q_heads, num_kv_heads, num_blocks, total_q, max_len, oob_row;
   int group, tile_tok, span;   // tokens of a query tile (floor(128 / G) or the tree's) and of a run
   int window, sinks, max_nodes, piece_rows;
-  float scale_log2;
+  float scale_log2;            // of the scale's magnitude; negate: it is negative
+  int negate;
 };
 
 // flags of a descriptor
@@ -194,6 +194,24 @@ struct Run {
     seq = d[0], head = d[1], r0 = d[2], ntq = d[3], lo = d[4], hi = d[5], sink_end = d[6], ns = d[7], t_lo = d[8];
     n = d[9], t0 = d[10], t1 = d[11];
   }
+};
+
+// The keys that every row of a run sees: [lo, hi) and [0, sinks).
+struct Common {
+  int lo, hi, sinks;
+  __device__ Common(const Params &p, const Run &x, int L, int c) {
+    const int ctx = L - c;
+    if (p.mask) {
+      lo = sinks = 0;
+      hi = ctx;
+    } else {
+      hi = ctx + x.r0 + 1;
+      lo = max(0, ctx + min(c, x.r0 + p.span) - p.window);
+      sinks = min(p.sinks, hi);
+    }
+  }
+  // all of a key tile
+  __device__ bool has(int k0) const { return (k0 >= lo && k0 + kTK <= hi) || k0 + kTK <= sinks; }
 };
 
 // The runs of this CTA in order.
@@ -294,12 +312,13 @@ __device__ __forceinline__ uint64_t below(int x) { return x <= 0 ? 0ull : x >= 6
 struct RowSight {
   int lo, hi, sinks;   // window: [lo, hi) and [0, sinks)
   int ctx;             // tree: [0, ctx) and bit j of word for key ctx + j
-  uint64_t word;
+  uint64_t word;       // (bits of the tree only: keep)
+  uint64_t keep;
   bool tree;
   __device__ __forceinline__ uint64_t of(int h0) const {
     if (!tree) return (below(hi - h0) & ~below(lo - h0)) | below(sinks - h0);
     const int sh = ctx - h0;
-    const uint64_t own = sh >= 64 || sh <= -64 ? 0ull : sh >= 0 ? word << sh : word >> -sh;
+    const uint64_t w = word & keep, own = sh >= 64 || sh <= -64 ? 0ull : sh >= 0 ? w << sh : w >> -sh;
     return below(sh) | own;
   }
 };
@@ -308,9 +327,64 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
-__device__ __forceinline__ bool not_finite(uint32_t two_bf16) {
-  const uint32_t m = two_bf16 & 0x7F807F80u;
-  return (m & 0x7F80u) == 0x7F80u || (m >> 16) == 0x7F80u;
+// 0 * x + acc for two bf16: NaN where x is not finite.
+__device__ __forceinline__ uint32_t poison2(uint32_t x, uint32_t acc) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(acc));
+  return d;
+}
+__device__ __forceinline__ bool any_nan2(uint32_t x) {
+  const uint32_t m = x & 0x7FFF7FFFu;
+  return (m & 0xFFFFu) > 0x7F80u || (m >> 16) > 0x7F80u;
+}
+
+// One warp: the value rows of a staged tile from key k0 on that no row of the run
+// sees become zeros, and so do values that are not finite; true: there were some.
+template <int D>
+__device__ bool clear_values(uint32_t tile, const Run &x, int k0, int lane) {
+  constexpr int kHalves = D / 64, kHalf = kTK * 128, kPerRow = kHalves * 8;  // 16-byte chunks of a row
+  auto at = [&](int e) {
+    const int row = e / kPerRow, rem = e % kPerRow;
+    return tile + (rem / 8) * kHalf + row * 128 + (rem % 8) * 16;
+  };
+  auto zero = [&](int key0, int key1) {  // rows of keys [key0, key1)
+    const int a = max(0, key0 - k0) * kPerRow, b = min(kTK, key1 - k0) * kPerRow;
+#pragma unroll 1
+    for (int e = a + lane; e < b; e += 32)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at(e)), "r"(0u) : "memory");
+  };
+  zero(x.sink_end, x.lo);
+  zero(x.hi, k0 + kTK);
+  __syncwarp();
+  uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (int e = lane; e < kTK * kPerRow; e += 32 * 8) {
+    uint32_t w[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                   : "r"(at(e + 32 * i))
+                   : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] = poison2(w[i][k], acc[k]);
+  }
+  const bool bad = any_nan2(acc[0]) || any_nan2(acc[1]) || any_nan2(acc[2]) || any_nan2(acc[3]);
+  const bool odd = __any_sync(0xffffffffu, bad);
+  if (odd) {
+#pragma unroll 1
+    for (int e = lane; e < kTK * kPerRow * 8; e += 32) {  // single values
+      const uint32_t a = at(e / 8) + (e % 8) * 2;
+      uint16_t v;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+      if ((v & 0x7F80u) == 0x7F80u) asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(0)) : "memory");
+    }
+  }
+  fence_proxy_async_shared();
+  __syncwarp();
+  return odd;
 }
 
 template <int BS, int D>
@@ -379,12 +453,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(BI::kQFree + i), 1);
       mbar_init(bar(BI::kOFull + i), 1);
       mbar_init(bar(BI::kOFree + i), kRows);
-      mbar_init(bar(BI::kSFull + i), 1);
-      mbar_init(bar(BI::kPFull + i), kRows);
-      mbar_init(bar(BI::kPLo + i), kRows);
-      mbar_init(bar(BI::kPvDone + i), 1);
+      mbar_init(bar(BI::kSFree + i), kRows);  // one per half of the scores
+      for (int h = 2 * i; h < 2 * i + 2; ++h) {  // one per slot and half
+        mbar_init(bar(BI::kPFull + h), kRows);
+        mbar_init(bar(BI::kPvDone + h), 1);
+        mbar_init(bar(BI::kSFull + h), 1);
+      }
     }
-    mbar_init(bar(BI::kSFree), kRows);
     for (int i = 0; i < kRunRing; ++i) {
       mbar_init(bar(BI::kRunFull + i), 1);
       mbar_init(bar(BI::kRunFree + i), kRunUsers);
@@ -432,7 +507,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto run_done = [&](int j) { mbar_arrive(bar(BI::kRunFree + j % kRunRing)); };
 
   if (warp >= kKWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kKWarp || warp == kVWarp) {
       // ------------------------------------- producers: runs, K (+ Q); V
       const bool is_v = warp == kVWarp;
@@ -533,11 +607,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------- S = Q K^T issuer
-      // The slots share one S buffer: a product goes out once the previous one has
-      // been read (the weights have their own columns), so the next product runs
-      // while the softmax of this one is computed.
+      // The slots share one buffer of scores, in two halves of 64 keys: a half's
+      // product goes out once the half before it in its place has been read (the
+      // weights have their own columns), so the products of one half run while the
+      // other is read.
       if (lane == 0) {
-        constexpr uint32_t kIdS = tc::idesc_bf16(kRows, kTK, false, false);
+        // a negative scale is taken as the negated queries' product (bit 13: negate A)
+        const uint32_t kIdS = tc::idesc_bf16(kRows, kTK / 2, false, false) | (p.negate ? 1u << 13 : 0u);
         int g = 0, nq = 0, np = 0;  // key tiles, query tiles, products so far
         bool ok = true;
         for (int j = 0; ok; ++j) {
@@ -553,14 +629,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < x.ntq; ++q) {
               const int slot = (nq + q) & 1;
               if (t == x.t0 && !mbar_wait(bar(BI::kQFull + slot), ((nq + q) >> 1) & 1)) { ok = false; break; }
-              if (np > 0 && !mbar_wait(bar(BI::kSFree), (np - 1) & 1)) { ok = false; break; }
-              tc::fence_after();
               const uint32_t sq = sQ + slot * kTile;
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                if (np > 0 && !mbar_wait(bar(BI::kSFree + h), (np - 1) & 1)) { ok = false; break; }
+                tc::fence_after();
+                const uint32_t kh = kb + h * (kTK / 2) * 128;
 #pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks)
-                tc::mma(tS, tc::desc_sw128(sq + (ks >> 2) * Lay::kHalf + (ks & 3) * 32, 16, 1024),
-                        tc::desc_sw128(kb + (ks >> 2) * Lay::kHalf + (ks & 3) * 32, 16, 1024), kIdS, ks > 0);
-              tc::commit(bar(BI::kSFull + slot));
+                for (int ks = 0; ks < D / 16; ++ks)
+                  tc::mma(tS + h * (kTK / 2), tc::desc_sw128(sq + (ks >> 2) * Lay::kHalf + (ks & 3) * 32, 16, 1024),
+                          tc::desc_sw128(kh + (ks >> 2) * Lay::kHalf + (ks & 3) * 32, 16, 1024), kIdS, ks > 0);
+                tc::commit(bar(BI::kSFull + 2 * slot + h));
+              }
+              if (!ok) break;
               if (t == x.t1 - 1) tc::commit(bar(BI::kQFree + slot));
               ++np;
             }
@@ -572,63 +653,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kPvWarp) {
       // ------------------------------------------------ O += P V issuer
-      // Per key tile the run's first query tile, then its second (whose product so
-      // follows the first one's clearing of the value rows).
-      if (lane == 0) {
-        constexpr uint32_t kIdO = tc::idesc_bf16(kRows, D, false, true);
-        constexpr int kSteps = kTK / 16;  // 16 keys = 8 packed columns of P
-        int g = 0, nq = 0, n[2] = {0, 0};  // key tiles, query tiles, each slot's products
-        bool ok = true;
-        for (int j = 0; ok; ++j) {
-          Run x;
-          run_at(j, x);
-          if (x.ntq == 0) break;
-          run_done(j);
-          if (x.t0 >= x.t1) continue;
-          for (int t = x.t0; t < x.t1 && ok; ++t, ++g) {
-            const int vs = g % kStages;
-            if (!mbar_wait(bar(BI::kVFull + vs), (g / kStages) & 1)) { ok = false; break; }
-            const uint32_t vb = sV + vs * kTile;
-            for (int q = 0; q < x.ntq; ++q) {
+      // The whole warp goes through the tiles, for the values that must be cleared;
+      // one lane issues.
+      constexpr uint32_t kIdO = tc::idesc_bf16(kRows, D, false, true);
+      constexpr int kSteps = kTK / 16;  // 16 keys = 8 packed columns of P
+      int g = 0, nq = 0, n[2] = {0, 0};  // key tiles, query tiles, each slot's products
+      bool ok = true;
+      for (int j = 0;; ++j) {
+        Run x;
+        run_at(j, x);
+        __syncwarp();
+        if (lane == 0) run_done(j);
+        if (x.ntq == 0) break;
+        if (x.t0 >= x.t1) continue;
+        const Common seen(p, x, lens[x.seq], qc[x.seq]);
+        for (int t = x.t0; t < x.t1; ++t, ++g) {
+          const int vs = g % kStages;
+          if (!wait_warp(bar(BI::kVFull + vs), (g / kStages) & 1)) { ok = false; break; }
+          const uint32_t vb = sV + vs * kTile;
+          const int k0 = x.key0(t);
+          if (!seen.has(k0) && clear_values<D>(vb, x, k0, lane) && lane == 0) *odd_tile = g + 1;
+          if (lane == 0) {
+            for (int q = 0; q < x.ntq && ok; ++q) {
               const int slot = (nq + q) & 1, use = (nq + q) >> 1;
               int &done = slot ? n[1] : n[0];
-              if (!mbar_wait(bar(BI::kPFull + slot), done & 1)) { ok = false; break; }
-              // the first product overwrites the accumulator: its last run must have been written out
+              // the first product overwrites the accumulator: its last run must have been read
               if (t == x.t0 && use > 0 && !mbar_wait(bar(BI::kOFree + slot), (use - 1) & 1)) { ok = false; break; }
-              tc::fence_after();
-              const uint32_t pa = tP + slot * (kTK / 2), acc = tmem + slot * D;
-              // keys 64.. first (kPFull), keys 0.. once weighted (kPLo)
+              const uint32_t acc = tmem + slot * D;
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                if (!mbar_wait(bar(BI::kPFull + 2 * slot + h), done & 1)) { ok = false; break; }
+                tc::fence_after();
+                const uint32_t pa = tP + slot * (kTK / 2) + h * (kTK / 4), vh = vb + h * (kTK / 2) * 128;
 #pragma unroll
-              for (int ks = kSteps / 2; ks < kSteps; ++ks)
-                tc::mma_ta(acc, pa + ks * 8, tc::desc_sw128(vb + ks * 2048, Lay::kHalf, 1024), kIdO,
-                           !(t == x.t0 && ks == kSteps / 2));
-              if (!mbar_wait(bar(BI::kPLo + slot), done & 1)) { ok = false; break; }
-              tc::fence_after();
-#pragma unroll
-              for (int ks = 0; ks < kSteps / 2; ++ks)
-                tc::mma_ta(acc, pa + ks * 8, tc::desc_sw128(vb + ks * 2048, Lay::kHalf, 1024), kIdO, true);
-              tc::commit(bar(BI::kPvDone + slot));
+                for (int ks = 0; ks < kSteps / 2; ++ks)
+                  tc::mma_ta(acc, pa + ks * 8, tc::desc_sw128(vh + ks * 2048, Lay::kHalf, 1024), kIdO,
+                             !(t == x.t0 && h == 0 && ks == 0));
+                tc::commit(bar(BI::kPvDone + 2 * slot + h));
+              }
               if (t == x.t1 - 1) tc::commit(bar(BI::kOFull + slot));
               ++done;
             }
             if (ok) tc::commit(bar(BI::kVEmpty + vs));
           }
-          nq += x.ntq;
+          if (!__shfl_sync(0xffffffffu, ok, 0)) { ok = false; break; }  // the other lanes wait for the issues here
         }
-        if (!ok) timed_out();
+        if (!ok) break;
+        nq += x.ntq;
       }
+      if (!ok && lane == 0) timed_out();
     }
   } else {
     // ------------------------------------------------------ softmax warps
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     {
       const int slot = warp >> 2;
       const int r = threadIdx.x & (kRows - 1);  // query row = TMEM lane
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tO = tmem + slot * D + lane_off, tSr = tS + lane_off, tPr = tP + slot * (kTK / 2) + lane_off;
-      const bool neg = p.scale_log2 < 0.f;  // a negative scale turns the largest score into the smallest
-      const uint32_t masked = __float_as_uint(neg ? INFINITY : -INFINITY);
-      int g = 0, nq = 0, n_tiles = 0;  // key tiles and query tiles of the CTA, key tiles of this slot
+      int g = 0, nq = 0, n = 0;  // key tiles and query tiles of the CTA, halves of key tiles of this slot
       bool ok = true;
       for (int j = 0; ok; ++j) {
         Run x;
@@ -651,163 +733,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         RowSight sight;
         sight.tree = p.mask != nullptr;
         sight.ctx = ctx;
-        sight.word = 0;
+        sight.word = sight.keep = 0;
         sight.lo = sight.hi = sight.sinks = 0;
         if (sight.tree) {
-          if (row_valid) sight.word = p.mask[qs[x.seq] + token] & below(c);
-          else sight.ctx = 0;
+          if (row_valid) {
+            sight.word = p.mask[qs[x.seq] + token];
+            sight.keep = below(c);
+          } else {
+            sight.ctx = 0;
+          }
         } else if (row_valid) {
           sight.hi = max(0, ctx + token + 1);
           sight.lo = max(0, sight.hi - p.window);
           sight.sinks = min(p.sinks, sight.hi);
         }
-        // every row of the run sees keys [all_lo, all_hi) and [0, all_sinks)
-        const int last = min(c, x.r0 + p.span) - 1;
-        const int all_hi = sight.tree ? ctx : ctx + x.r0 + 1;
-        const int all_lo = sight.tree ? 0 : max(0, ctx + last - p.window + 1), all_sinks = sight.tree ? 0 : min(p.sinks, all_hi);
+        const Common seen(p, x, lens[x.seq], c);
         float m = -INFINITY, l = 0.f;
         const int g0 = g;
-        for (int t = x.t0; t < x.t1; ++t, ++g) {
-          const int k0 = x.key0(t);
-          const bool full = (k0 >= all_lo && k0 + kTK <= all_hi) || k0 + kTK <= all_sinks;
-          const uint64_t all = row_valid ? ~0ull : 0ull;  // spare rows see nothing
-          const uint64_t see_lo = full ? all : sight.of(k0), see_hi = full ? all : sight.of(k0 + 64);
-          const bool first = t == x.t0;
-          if (!wait_warp(bar(BI::kSFull + slot), n_tiles & 1)) { ok = false; break; }
-          ++n_tiles;
+        g += x.t1 - x.t0;
+#pragma unroll 1
+        for (int u = 2 * x.t0; u < 2 * x.t1; ++u, ++n) {  // halves of key tiles: 64 keys
+          const int h = u & 1, k0 = x.key0(u >> 1);
+          const uint32_t phase = (n >> 1) & 1;
+          // spare rows see nothing
+          const bool full = seen.has(k0);
+          const uint64_t see = full ? (row_valid ? ~0ull : 0ull) : sight.of(k0 + 64 * h);
+          const bool none = __all_sync(0xffffffffu, see == 0);  // no row of the warp sees any of them
+          if (!wait_warp(bar(BI::kSFull + 2 * slot + h), phase)) { ok = false; break; }
+          tc::fence_after();
+          uint32_t pk[32];
           bool scale_o = false;
           float alpha = 1.f;
-          // move the reference max only when a score passes it by more than kSlack
-          // (rare after a run's first tile); exact, since O and l share it
-          auto new_reference = [&](float rm) {
-            const float bm = rm * p.scale_log2;
-            const bool move = bm > m + kSlack;
-            scale_o = move && !first && m != -INFINITY;
-            alpha = scale_o ? fast_exp2(m - bm) : 1.f;
-            if (move) {
-              l = m == -INFINITY ? 0.f : l * exp2f(m - bm);
-              m = bm;
-            }
-            return m == -INFINITY ? 0.f : m;
-          };
-          auto mask = [&](uint32_t(&sv)[64], uint64_t see) {
-            const uint32_t a = static_cast<uint32_t>(see), b = static_cast<uint32_t>(see >> 32);
+          if (none) {
+            mbar_arrive(bar(BI::kSFree + h));
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if (!(a & (1u << k))) sv[k] = masked;
-              if (!(b & (1u << k))) sv[32 + k] = masked;
-            }
-          };
-          auto rescale_o = [&]() {
-            if (__any_sync(0xffffffffu, scale_o)) {  // warp-uniform: tcgen05.ld/st are warp-wide
-#pragma unroll
-              for (int ch = 0; ch < D / 32; ++ch) {
-                uint32_t ov[32];
-                tc::ld32(tO + ch * 32, ov);
-                tc::wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
-                tc::st32(tO + ch * 32, ov);
-              }
-            }
-          };
-          // Values of a tile that is not seen whole, by the run's first query tile
-          // (the other's product follows): clear what no row of the run sees, and
-          // what is not finite, noting the tile.
-          auto clear_values = [&]() {
-            if (full || q > 0) return true;
-            const int s = g % kStages;
-            if (!wait_warp(bar(BI::kVFull + s), (g / kStages) & 1)) return false;
-            const uint32_t vb = sV + s * kTile;
-            bool odd = false;
-#pragma unroll 4
-            for (int e = r; e < kTK * kHalves * 8; e += kRows) {  // 16-byte chunks
-              const int row = e / (kHalves * 8), rem = e % (kHalves * 8), key = k0 + row;
-              const uint32_t at = vb + (rem / 8) * Lay::kHalf + row * 128 + (rem % 8) * 16;
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                           : "r"(at));
-              const bool hidden = key >= x.hi || (key < x.lo && key >= x.sink_end);
-              const bool bad = not_finite(w[0]) || not_finite(w[1]) || not_finite(w[2]) || not_finite(w[3]);
-              if (hidden || bad) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if (hidden || (w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u;
-                  if (hidden || (w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0x0000FFFFu;
-                }
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                             : "memory");
-                odd |= !hidden;
-              }
-            }
-            if (odd) atomicMax(odd_tile, g + 1);  // the other slot may be ahead, or behind
-            return true;
-          };
-          // make this thread's P (tensor memory) and cleared values (shared memory)
-          // visible to the P V issuer, then count in at barrier bi
-          auto publish = [&](int bi) {
-            tc::wait_st();
-            fence_proxy_async_shared();
-            tc::fence_before();
-            mbar_arrive(bar(bi));
-          };
-          // this slot's previous P V product must be complete before its weights'
-          // columns and its accumulator are written
-          auto previous_pv_done = [&]() {
-            if (n_tiles > 1 && !wait_warp(bar(BI::kPvDone + slot), (n_tiles - 2) & 1)) return false;
-            tc::fence_after();
-            return true;
-          };
-          tc::fence_after();
-          if (__all_sync(0xffffffffu, see_lo == 0 && see_hi == 0)) {  // no row of the warp sees any of the tile
-            tc::fence_before();
-            mbar_arrive(bar(BI::kSFree));
-            if (!previous_pv_done()) { ok = false; break; }
-            uint32_t z[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) z[k] = 0u;
-            tc::st32(tPr, z);
-            tc::st32(tPr + 32, z);
-            if (!clear_values()) { ok = false; break; }
-            publish(BI::kPFull + slot);
-            mbar_arrive(bar(BI::kPLo + slot));
+            for (int k = 0; k < 32; ++k) pk[k] = 0u;
           } else {
-            // the row's 128 scores in one load round; once they are in registers the
-            // next score product may overwrite them
-            uint32_t sl[64], sh[64];
-            tc::ld32(tSr, *reinterpret_cast<uint32_t(*)[32]>(&sl[0]));
-            tc::ld32(tSr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sl[32]));
-            tc::ld32(tSr + 64, *reinterpret_cast<uint32_t(*)[32]>(&sh[0]));
-            tc::ld32(tSr + 96, *reinterpret_cast<uint32_t(*)[32]>(&sh[32]));
+            uint32_t sv[64];
+            tc::ld32(tSr + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+            tc::ld32(tSr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
             tc::wait_ld();
             tc::fence_before();
-            mbar_arrive(bar(BI::kSFree));
+            mbar_arrive(bar(BI::kSFree + h));  // the next product may take their place
             if (!full) {
-              mask(sl, see_lo);
-              mask(sh, see_hi);
+              const uint32_t a = static_cast<uint32_t>(see), b = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                if (!(a & (1u << k))) sv[k] = __float_as_uint(-INFINITY);
+                if (!(b & (1u << k))) sv[32 + k] = __float_as_uint(-INFINITY);
+              }
             }
-            const float el = extreme64(sl, neg), eh = extreme64(sh, neg);
-            const float msub = new_reference(neg ? fminf(el, eh) : fmaxf(el, eh));
+            // move the reference max only when a score passes it by more than kSlack
+            // (rare after a run's first tile); exact, since O and l share it
+            const float bm = extreme64(sv, false) * p.scale_log2;
+            if (bm > m + kSlack) {
+              scale_o = m != -INFINITY;
+              alpha = scale_o ? fast_exp2(m - bm) : 1.f;
+              l *= alpha;
+              m = bm;
+            }
+            const float msub = m == -INFINITY ? 0.f : m;
             const uint64_t ks2 = f32x2_bits(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
             const uint64_t nm2 = f32x2_bits(__float_as_uint(-msub), __float_as_uint(-msub));
-            // keys 64..127 first: their P V product starts while keys 0..63 are weighted
-            uint32_t pk[32];
-            float lsum = weights64(sh, ks2, nm2, pk);
-            if (!previous_pv_done()) { ok = false; break; }
-            tc::st32(tPr + 32, pk);
-            // none of this tile's P V products is issued before kPFull: the accumulator
-            // holds its final value and may be rescaled here
-            rescale_o();
-            if (!clear_values()) { ok = false; break; }
-            publish(BI::kPFull + slot);
-            lsum += weights64(sl, ks2, nm2, pk);
-            tc::st32(tPr, pk);
-            tc::wait_st();
-            tc::fence_before();
-            mbar_arrive(bar(BI::kPLo + slot));
-            l += lsum;
+            l += weights64(sv, ks2, nm2, pk);
           }
+          // this half's last product must be complete before its weights' columns are
+          // written, and every product before the accumulator is
+          if (n > 1 && !wait_warp(bar(BI::kPvDone + 2 * slot + h), phase ^ 1)) { ok = false; break; }
+          if (__any_sync(0xffffffffu, scale_o)) {  // warp-uniform: tcgen05.ld/st are warp-wide
+            if (!wait_warp(bar(BI::kPvDone + 2 * slot + (h ^ 1)), ((n - 1) >> 1) & 1)) { ok = false; break; }
+            tc::fence_after();
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+              uint32_t ov[32];
+              tc::ld32(tO + ch * 32, ov);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+              tc::st32(tO + ch * 32, ov);
+            }
+          }
+          tc::fence_after();
+          tc::st32(tPr + h * 32, pk);
+          tc::wait_st();
+          tc::fence_before();
+          mbar_arrive(bar(BI::kPFull + 2 * slot + h));
         }
         if (!ok) break;
         // ---- end of the piece: normalise and store the rows, or store the partial
@@ -821,21 +831,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t piece = 2 * static_cast<size_t>(blockIdx.x) + (x.t0 == 0 ? 1 : 0);
         const int prow = q * kRows + r;
         const bool odd = any && *reinterpret_cast<volatile int *>(odd_tile) > g0;
-#pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          __syncwarp();
-          uint32_t ov[32];
+        auto store = [&](int ch, const uint32_t (&ov)[32]) {
+          if (!whole) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) ov[k] = 0u;
-          if (any) {
+            for (int c4 = 0; c4 < 8; ++c4)
+              p.ws_o[(piece * (D / 4) + ch * 8 + c4) * p.piece_rows + prow] =
+                  make_float4(__uint_as_float(ov[c4 * 4]), __uint_as_float(ov[c4 * 4 + 1]), __uint_as_float(ov[c4 * 4 + 2]),
+                              __uint_as_float(ov[c4 * 4 + 3]));
+            return;
+          }
+          // a thread writes its own row: 32-byte stores (when the output allows) halve the requests
+          __nv_bfloat16 *dst = p.out + orow * D + ch * 32;
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(__uint_as_float(ov[2 * k]) * inv, __uint_as_float(ov[2 * k + 1]) * inv);
+          if ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
+#pragma unroll
+            for (int h8 = 0; h8 < 2; ++h8) st_global_v8(dst + h8 * 16, &w[8 * h8]);
+          } else {
+#pragma unroll
+            for (int c8 = 0; c8 < 4; ++c8)
+              reinterpret_cast<uint4 *>(dst)[c8] = make_uint4(w[4 * c8], w[4 * c8 + 1], w[4 * c8 + 2], w[4 * c8 + 3]);
+          }
+        };
+        if (!any) {
+          if (row_valid) {
+            uint32_t ov[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) ov[k] = 0u;
+#pragma unroll 1
+            for (int ch = 0; whole && ch < D / 32; ++ch) store(ch, ov);  // an empty piece's O is not read
+          }
+        } else {
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            __syncwarp();
+            uint32_t ov[32];
             tc::ld32(tO + ch * 32, ov);
             tc::wait_ld();
-          }
-          if (odd && row_valid) {
+            if (!row_valid) continue;
             // add the values that were cleared because they are not finite, where this row sees them
-            for (int t = x.t0; t < x.t1; ++t) {
+            for (int t = x.t0; odd && t < x.t1; ++t) {
               const int k0 = x.key0(t);
-              if ((k0 >= all_lo && k0 + kTK <= all_hi) || k0 + kTK <= all_sinks) continue;
+              if (seen.has(k0)) continue;
               for (int k = 0; k < kTK; ++k) {
                 if (!((sight.of(k0 + (k & 64)) >> (k & 63)) & 1)) continue;
                 const int b = p.block_tables[static_cast<size_t>(x.seq) * p.max_blocks + (k0 + k) / BS];
@@ -851,31 +889,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
+            store(ch, ov);
           }
-          if (!row_valid) continue;
-          if (!whole) {
-#pragma unroll
-            for (int c4 = 0; c4 < 8; ++c4)
-              p.ws_o[(piece * (D / 4) + ch * 8 + c4) * p.piece_rows + prow] =
-                  make_float4(__uint_as_float(ov[c4 * 4]), __uint_as_float(ov[c4 * 4 + 1]), __uint_as_float(ov[c4 * 4 + 2]),
-                              __uint_as_float(ov[c4 * 4 + 3]));
-            continue;
-          }
-          // a thread writes its own row: 32-byte stores (when the output allows) halve the requests
-          __nv_bfloat16 *dst = p.out + orow * D + ch * 32;
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(__uint_as_float(ov[2 * k]) * inv, __uint_as_float(ov[2 * k + 1]) * inv);
-          if ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
-#pragma unroll
-            for (int h8 = 0; h8 < 2; ++h8) st_global_v8(dst + h8 * 16, &w[8 * h8]);
-          } else {
-#pragma unroll
-            for (int c8 = 0; c8 < 4; ++c8)
-              reinterpret_cast<uint4 *>(dst)[c8] = make_uint4(w[4 * c8], w[4 * c8 + 1], w[4 * c8 + 2], w[4 * c8 + 3]);
-          }
-        }
-        if (any) {
+          __syncwarp();
           tc::fence_before();
           mbar_arrive(bar(BI::kOFree + slot));
         }
@@ -1055,7 +1071,8 @@ int tc_launch(const Call &a) {
   p.sinks = a.sinks;
   p.max_nodes = a.max_nodes;
   p.piece_rows = plan.piece_rows;
-  p.scale_log2 = kernel_scale_log2(a.scale);
+  p.scale_log2 = kernel_scale_log2(std::fabs(a.scale));
+  p.negate = a.scale < 0.f;
   return a.head_dim == 64 ? launch<64>(tmq, tmk, tmv, p, a.block_size, plan.split, as_stream(a.stream))
                           : launch<128>(tmq, tmk, tmv, p, a.block_size, plan.split, as_stream(a.stream));
 }
