@@ -327,6 +327,14 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
+// Shared-memory matrix descriptors (tc::desc_sw128, groups of 8 rows 1024 bytes
+// apart) in two words: the first holds the address (in 16 bytes), so that a product's
+// steps differ by an addition to it; few instructions between the issues matter, as
+// one thread issues them.
+constexpr uint32_t kSpanHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_word(uint32_t saddr) { return (saddr >> 4) & 0x3FFFu; }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return f32x2_bits(lo, hi); }
+
 // 0 * x + acc for two bf16: NaN where x is not finite.
 __device__ __forceinline__ uint32_t poison2(uint32_t x, uint32_t acc) {
   uint32_t d;
@@ -611,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // product goes out once the half before it in its place has been read (the
       // weights have their own columns), so the products of one half run while the
       // other is read.
-      if (lane == 0) {
+      if (tc::elect_one()) {
         // a negative scale is taken as the negated queries' product (bit 13: negate A)
         const uint32_t kIdS = tc::idesc_bf16(kRows, kTK / 2, false, false) | (p.negate ? 1u << 13 : 0u);
         int g = 0, nq = 0, np = 0;  // key tiles, query tiles, products so far
@@ -629,16 +637,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < x.ntq; ++q) {
               const int slot = (nq + q) & 1;
               if (t == x.t0 && !mbar_wait(bar(BI::kQFull + slot), ((nq + q) >> 1) & 1)) { ok = false; break; }
-              const uint32_t sq = sQ + slot * kTile;
+              const uint32_t qd = desc_word(sQ + slot * kTile);
 #pragma unroll 1
               for (int h = 0; h < 2; ++h) {
                 if (np > 0 && !mbar_wait(bar(BI::kSFree + h), (np - 1) & 1)) { ok = false; break; }
                 tc::fence_after();
-                const uint32_t kh = kb + h * (kTK / 2) * 128;
+                const uint32_t kd = desc_word(kb) + h * ((kTK / 2) * 128 >> 4);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                  tc::mma(tS + h * (kTK / 2), tc::desc_sw128(sq + (ks >> 2) * Lay::kHalf + (ks & 3) * 32, 16, 1024),
-                          tc::desc_sw128(kh + (ks >> 2) * Lay::kHalf + (ks & 3) * 32, 16, 1024), kIdS, ks > 0);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                  const uint32_t off = ((ks >> 2) * Lay::kHalf + (ks & 3) * 32) >> 4;
+                  tc::mma(tS + h * (kTK / 2), desc_of(qd + off, kSpanHi), desc_of(kd + off, kSpanHi), kIdS, ks > 0);
+                }
                 tc::commit(bar(BI::kSFull + 2 * slot + h));
               }
               if (!ok) break;
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t vb = sV + vs * kTile;
           const int k0 = x.key0(t);
           if (!seen.has(k0) && clear_values<D>(vb, x, k0, lane) && lane == 0) *odd_tile = g + 1;
-          if (lane == 0) {
+          if (tc::elect_one()) {
             for (int q = 0; q < x.ntq && ok; ++q) {
               const int slot = (nq + q) & 1, use = (nq + q) >> 1;
               int &done = slot ? n[1] : n[0];
@@ -684,10 +693,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int h = 0; h < 2; ++h) {
                 if (!mbar_wait(bar(BI::kPFull + 2 * slot + h), done & 1)) { ok = false; break; }
                 tc::fence_after();
-                const uint32_t pa = tP + slot * (kTK / 2) + h * (kTK / 4), vh = vb + h * (kTK / 2) * 128;
+                const uint32_t pa = tP + slot * (kTK / 2) + h * (kTK / 4);
+                const uint32_t vd = (desc_word(vb) | (Lay::kHalf >> 4) << 16) + h * ((kTK / 2) * 128 >> 4);
 #pragma unroll
                 for (int ks = 0; ks < kSteps / 2; ++ks)
-                  tc::mma_ta(acc, pa + ks * 8, tc::desc_sw128(vh + ks * 2048, Lay::kHalf, 1024), kIdO,
+                  tc::mma_ta(acc, pa + ks * 8, desc_of(vd + (ks * 2048 >> 4), kSpanHi), kIdO,
                              !(t == x.t0 && h == 0 && ks == 0));
                 tc::commit(bar(BI::kPvDone + 2 * slot + h));
               }
@@ -696,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (ok) tc::commit(bar(BI::kVEmpty + vs));
           }
-          if (!__shfl_sync(0xffffffffu, ok, 0)) { ok = false; break; }  // the other lanes wait for the issues here
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }  // the other lanes wait for the issues here
         }
         if (!ok) break;
         nq += x.ntq;
