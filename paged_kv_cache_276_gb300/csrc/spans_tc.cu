@@ -3,13 +3,13 @@
 //
 // For one KV head, a query tile of 128 rows holds up to 128 / G tokens x the G
 // query heads of the group (row r = token r / G, head r % G).  Over each tile of
-// 128 keys that some row sees:
-//     S  = Q K^T                     tcgen05.mma, M 128 x N 64 x K d, twice -> TMEM
+// 64 keys that some row sees:
+//     S  = Q K^T                     tcgen05.mma, M 128 x N 64 x K d -> TMEM
 //     P  = exp2(S * scale*log2e - m)  softmax warps, one query row per thread,
-//                                    64 keys at a time, bf16 in TMEM
-//     O += P V                       tcgen05.mma, M 128 x N d x K 64, twice -> TMEM
+//                                    bf16 in TMEM
+//     O += P V                       tcgen05.mma, M 128 x N d x K 64 -> TMEM
 // with the running max / sum of the online softmax.  What a row sees of a tile is
-// two 64-bit words, from the window's bounds or from the tree's mask: a key whose
+// a 64-bit word, from the window's bounds or from the tree's mask: a key whose
 // bit is clear gets the score -inf.
 //
 // Runs and ranges.  A run is one (sequence, KV head, query tile or pair of query
@@ -63,14 +63,15 @@ namespace spans {
 namespace {
 
 constexpr int kRows = 128;       // query rows per tile
-constexpr int kTK = 128;         // keys per tile
+constexpr int kTK = 64;          // keys per tile
 constexpr int kTmemCols = 512;
 constexpr int kKWarp = 8, kMmaWarp = 9, kPvWarp = 10, kVWarp = 11;
 constexpr int kThreads = 12 * 32;
 constexpr float kSlack = 8.f;    // lazy rescale threshold (log2 units)
 constexpr int kRunCost = 256;    // a run's start and end, in keys
 constexpr int kMinRange = 512;   // least weight of a CTA's range, in keys
-constexpr int kMinPiece = 2;     // key tiles that a border leaves on either side
+constexpr int kRoundsFrom = 4;   // runs per CTA from which most go round the CTAs whole
+constexpr int kMinPiece = 4;     // key tiles that a border leaves on either side
 constexpr int kJoinThreads = 256;
 constexpr int kRunRing = 4;      // descriptors of runs ahead
 constexpr int kRunUsers = 11;    // arrivals that free one: 8 softmax warps, two issuers, the value producer
@@ -79,23 +80,25 @@ template <int D>
 struct Layout {
   static_assert(D == 64 || D == 128, "head dim");
   static constexpr int kHalves = D / 64;            // 64-column (128-byte) halves of a row
-  static constexpr int kHalf = kRows * 128;         // one half of a tile of 128 rows
-  static constexpr int kTile = kHalves * kHalf;     // [half][128 rows][128 B]
-  static constexpr int kStages = D == 128 ? 2 : 4;  // of keys, and of values
-  static constexpr int kSmemK = 2 * kTile;          // after two query tiles
+  static constexpr int kQHalf = kRows * 128;        // one half of a query tile
+  static constexpr int kQTile = kHalves * kQHalf;   // [half][128 rows][128 B]
+  static constexpr int kHalf = kTK * 128;           // one half of a key or value tile
+  static constexpr int kTile = kHalves * kHalf;     // [half][64 rows][128 B]
+  static constexpr int kStages = D == 128 ? 4 : 8;  // of keys, and of values: 64 KB each
+  static constexpr int kSmemK = 2 * kQTile;         // after two query tiles
   static constexpr int kSmemV = kSmemK + kStages * kTile;
   static constexpr int kSmemBars = kSmemV + kStages * kTile;
-  // tensor memory: accumulators at 0 and D, scores, then each slot's P
-  static constexpr int kTmemS = 2 * D, kTmemP = kTmemS + kTK;
-  static_assert(kTmemP + 2 * (kTK / 2) <= kTmemCols, "tensor memory");
+  // tensor memory: each slot's accumulator, then its scores, then its two P
+  static constexpr int kTmemS = 2 * D, kTmemP = kTmemS + 2 * kTK;
+  static_assert(kTmemP + 4 * (kTK / 2) <= kTmemCols, "tensor memory");
 };
 
 // barrier indices (8 bytes each)
 template <int ST>
 struct Bar {
-  static constexpr int kQFull = 0, kQFree = 2, kOFull = 4, kOFree = 6,
-                       kPFull = 8, kPvDone = 12, kSFull = 16,  // [slot][half]
-                       kSFree = 20, kRunFull = 22, kRunFree = kRunFull + kRunRing, kKFull = kRunFree + kRunRing, kKEmpty = kKFull + ST, kVFull = kKEmpty + ST, kVEmpty = kVFull + ST,
+  static constexpr int kQFull = 0, kQFree = 2, kOFull = 4, kOFree = 6, kSFull = 8, kSFree = 10,  // [slot]
+                       kPFull = 12, kPvDone = 16,  // [slot][buffer of P]
+                       kRunFull = 20, kRunFree = kRunFull + kRunRing, kKFull = kRunFree + kRunRing, kKEmpty = kKFull + ST, kVFull = kKEmpty + ST, kVEmpty = kVFull + ST,
                        kCount = kVEmpty + ST;
 };
 
@@ -106,7 +109,7 @@ template <int D>
 constexpr size_t smem_bytes(int num_seqs) {
   using Lay = Layout<D>;
   return 1024 + Lay::kSmemBars + Bar<Lay::kStages>::kCount * 8 + 16 + kRunRing * kRunInts * 4 +
-         static_cast<size_t>(num_seqs + 1) * 8 + static_cast<size_t>(num_seqs) * 12;
+         static_cast<size_t>(num_seqs + 1) * 12 + static_cast<size_t>(num_seqs) * 12;
 }
 static_assert(smem_bytes<128>(kMaxSeqs) <= 227 * 1024, "shared memory");
 
@@ -135,6 +138,7 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 // Per-sequence values kept in shared memory.
 struct SeqTab {
   const long long *prefix;  // [B + 1] weight before each sequence
+  const int *first;           // [B + 1] runs before each sequence
   const int *lens, *qs, *qc;  // [B] clamped length, first query row, query tokens (0: none or a bad q_start)
 };
 
@@ -179,7 +183,7 @@ struct Weights {
 };
 
 // A CTA's piece of a run: key tiles [t0, t1) of its n.  Tile v starts at key
-// 128 v (the sinks', v < ns) or 128 (v - ns + t_lo).
+// 64 v (the sinks', v < ns) or 64 (v - ns + t_lo).
 struct Run {
   int seq, head, r0, ntq;  // first query token, query tiles (0: no further run)
   int lo, hi, sink_end;    // the run sees nothing outside [lo, hi) and [0, sink_end)
@@ -214,20 +218,69 @@ struct Common {
   __device__ bool has(int k0) const { return (k0 >= lo && k0 + kTK <= hi) || k0 + kTK <= sinks; }
 };
 
-// The runs of this CTA in order.
+// The runs of this CTA in order: first whole rounds (run c, c + grid, ... for CTA
+// c), then its range of the weight of the rest.
 struct Sched {
   long long xa, xb, s;  // the CTA's range; the current run's start
-  int seq, head, i;
+  int seq, head, i, round, rounds, grid;
   bool done;
   Weights w;  // of the current sequence
   Run x;
 
-  __device__ void begin(const Params &p, const SeqTab &t, int ctas) {
-    const long long total = t.prefix[p.num_seqs];
+  __device__ void begin(const Params &p, const SeqTab &t) {
+    grid = gridDim.x;
+    const int runs = t.first[p.num_seqs];
+    rounds = !p.mask && runs >= kRoundsFrom * grid ? runs / grid - 1 : 0;
+    round = 0;
+    done = false;
+    if (rounds > 0) whole_run(p, t);
+    else begin_range(p, t);
+  }
+  __device__ void next(const Params &p, const SeqTab &t) {
+    if (round < rounds) {
+      if (++round < rounds) whole_run(p, t);
+      else begin_range(p, t);
+    } else {
+      step(p, t);
+      settle(p, t);
+    }
+  }
+
+ private:
+  __device__ void enter(const Params &p, const SeqTab &t, int sequence) {
+    seq = sequence;
+    w = Weights(p, t.lens[seq], t.qc[seq]);
+  }
+  // run number `run` of the batch
+  __device__ void locate(const Params &p, const SeqTab &t, int run) {
+    int lo = 0, hi = p.num_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (t.first[mid] <= run) lo = mid; else hi = mid;
+    }
+    enter(p, t, lo);
+    const int off = run - t.first[seq];
+    head = off / w.runs;
+    i = off - head * w.runs;
+  }
+  __device__ void whole_run(const Params &p, const SeqTab &t) {
+    locate(p, t, round * grid + blockIdx.x);
+    geometry(p, t.lens[seq], t.qc[seq]);
+    x.t0 = 0;
+    x.t1 = x.n;
+  }
+  __device__ void begin_range(const Params &p, const SeqTab &t) {
+    long long start = 0;  // weight of the whole rounds
+    if (rounds > 0) {
+      locate(p, t, rounds * grid);
+      start = t.prefix[seq] + head * w.sum(w.runs) + w.sum(i);
+    }
+    const long long rest = t.prefix[p.num_seqs] - start;
+    const long long most = rest / kMinRange, ctas = most < 1 ? 1 : most < grid ? most : grid;
     xa = xb = 0;
     if (static_cast<int>(blockIdx.x) < ctas) {
-      xa = total * blockIdx.x / ctas;
-      xb = total * (blockIdx.x + 1) / ctas;
+      xa = start + rest * blockIdx.x / ctas;
+      xb = start + rest * (blockIdx.x + 1) / ctas;
     }
     done = xa >= xb;
     if (done) return;
@@ -236,20 +289,13 @@ struct Sched {
       const int mid = (lo + hi) >> 1;
       if (t.prefix[mid] <= xa) lo = mid; else hi = mid;
     }
-    seq = lo;
-    w = Weights(p, t.lens[seq], t.qc[seq]);
+    enter(p, t, lo);
     const long long per_head = w.sum(w.runs), off = xa - t.prefix[seq];
     head = static_cast<int>(off / per_head);
     i = w.find(off - head * per_head);
     s = t.prefix[seq] + head * per_head + w.sum(i);
     settle(p, t);
   }
-  __device__ void next(const Params &p, const SeqTab &t) {
-    step(p, t);
-    settle(p, t);
-  }
-
- private:
   __device__ void step(const Params &p, const SeqTab &t) {
     s += w.of(i);
     if (++i < w.runs) return;
@@ -258,7 +304,7 @@ struct Sched {
     head = 0;
     do ++seq;
     while (seq < p.num_seqs && t.qc[seq] == 0);
-    if (seq < p.num_seqs) w = Weights(p, t.lens[seq], t.qc[seq]);
+    if (seq < p.num_seqs) enter(p, t, seq);
   }
   // from the current run on: the first that this CTA has a piece of
   __device__ void settle(const Params &p, const SeqTab &t) {
@@ -298,12 +344,6 @@ struct Sched {
     x.n = x.hi > 0 ? x.ns + ceil_div(x.hi, kTK) - x.t_lo : 0;
   }
 };
-
-// CTAs that get a range.
-__device__ __forceinline__ int active_ctas(long long total) {
-  const long long most = total / kMinRange;
-  return most < 1 ? 1 : most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
-}
 
 // Bits below x of a 64-bit word.
 __device__ __forceinline__ uint64_t below(int x) { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1; }
@@ -400,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     spans_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv, const Params p) {
   using Lay = Layout<D>;
-  constexpr int kStages = Lay::kStages, kHalves = Lay::kHalves, kTile = Lay::kTile;
+  constexpr int kStages = Lay::kStages, kHalves = Lay::kHalves, kTile = Lay::kTile, kQTile = Lay::kQTile;
   using BI = Bar<kStages>;
-  // one TMA box per block of the tile
-  constexpr int kBoxes = kTK / BS;
+  // one TMA box per block of the tile (a block longer than the tile: the tile's piece of it)
+  constexpr int kBoxRows = BS < kTK ? BS : kTK, kBoxes = kTK / kBoxRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kSmemBars);
@@ -412,9 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   int *odd_tile = reinterpret_cast<int *>(tmem_slot + 2);  // 1 + the last key tile (counted over the CTA) whose values are not all finite
   volatile int *runs = reinterpret_cast<volatile int *>(bars + BI::kCount + 2);  // [kRunRing][kRunInts]
   long long *prefix = reinterpret_cast<long long *>(bars + BI::kCount + 2 + kRunRing * kRunInts / 2);  // [B + 1]
-  int *lens = reinterpret_cast<int *>(prefix + p.num_seqs + 1);              // [B]
+  int *first = reinterpret_cast<int *>(prefix + p.num_seqs + 1);             // [B + 1]
+  int *lens = first + p.num_seqs + 1;                                        // [B]
   int *qs = lens + p.num_seqs, *qc = qs + p.num_seqs;                        // [B] each
-  const SeqTab tab{prefix, lens, qs, qc};
+  const SeqTab tab{prefix, first, lens, qs, qc};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int B = p.num_seqs, hkv = p.num_kv_heads;
   auto bar = [&](int i) { return smem_u32(bars + i); };
@@ -422,11 +463,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_launch_dependents();
   grid_dependency_wait();
 
-  if (warp == 0) {  // weight per sequence -> exclusive prefix
+  if (warp == 0) {  // weight and runs per sequence -> exclusive prefixes
     const int per = (B + 31) / 32;
     const int lo = min(B, lane * per), hi = min(B, lo + per);
     const int cap = min(p.max_blocks * BS, p.max_len);
     long long sum = 0;
+    int count = 0;
     for (int i = lo; i < hi; ++i) {
       int L = p.seq_lens[i];
       if (L < 0 || L > cap) {
@@ -444,16 +486,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       qc[i] = c;
       const Weights w(p, L, c);
       sum += w.sum(w.runs) * hkv;
+      count += w.runs * hkv;
       prefix[i + 1] = sum;  // within the lane's stretch
+      first[i + 1] = count;
     }
     long long incl = sum;
+    int before = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int n = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) incl += v, before += n;
     }
-    for (int i = lo; i < hi; ++i) prefix[i + 1] += incl - sum;
-    if (lane == 0) prefix[0] = 0;
+    for (int i = lo; i < hi; ++i) prefix[i + 1] += incl - sum, first[i + 1] += before - count;
+    if (lane == 0) prefix[0] = 0, first[0] = 0;
   }
   if (threadIdx.x == 32 * kKWarp) {
     for (int i = 0; i < 2; ++i) {  // one per slot
@@ -461,11 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(BI::kQFree + i), 1);
       mbar_init(bar(BI::kOFull + i), 1);
       mbar_init(bar(BI::kOFree + i), kRows);
-      mbar_init(bar(BI::kSFree + i), kRows);  // one per half of the scores
-      for (int h = 2 * i; h < 2 * i + 2; ++h) {  // one per slot and half
+      mbar_init(bar(BI::kSFull + i), 1);
+      mbar_init(bar(BI::kSFree + i), kRows);
+      for (int h = 2 * i; h < 2 * i + 2; ++h) {  // one per slot and buffer of P
         mbar_init(bar(BI::kPFull + h), kRows);
         mbar_init(bar(BI::kPvDone + h), 1);
-        mbar_init(bar(BI::kSFull + h), 1);
       }
     }
     for (int i = 0; i < kRunRing; ++i) {
@@ -488,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (p.tile_tok * p.group < kRows) {
     // the loads fill the tile's first tile_tok * G rows only: the rest stay zero
-    for (int i = threadIdx.x; i < 2 * kTile / 16; i += kThreads)
+    for (int i = threadIdx.x; i < 2 * kQTile / 16; i += kThreads)
       asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_u32(smem) + i * 16), "r"(0u) : "memory");
     fence_proxy_async_shared();
   }
@@ -527,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tw_seq = -1, tw_base = 0, tw_val = -1;
       Sched sc;
       int4 desc = make_int4(0, 0, 0, 0);  // this CTA's pieces, for the join
-      if (!is_v) sc.begin(p, tab, active_ctas(prefix[B]));
+      if (!is_v) sc.begin(p, tab);
       for (int j = 0; !*abort_flag; ++j) {
         Run x;
         if (is_v) {
@@ -565,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int hf = 0; hf < kHalves; ++hf)
                 asm volatile(
                     "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                    " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(sQ + slot * kTile + hf * Lay::kHalf),
+                    " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(sQ + slot * kQTile + hf * Lay::kQHalf),
                     "l"(reinterpret_cast<uint64_t>(&tmq)), "r"(hf * 64), "r"(x.head * p.group),
                     "r"(qs[x.seq] + x.r0 + q * p.tile_tok), "r"(bar(BI::kQFull + slot))
                     : "memory");
@@ -594,12 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int jb = lane / kHalves, hf = lane % kHalves;
           const int b = __shfl_sync(0xffffffffu, tw_val, (blk + min(jb, kBoxes - 1) - tw_base) & 31);
           if (jb < kBoxes) {
-            const int kb = k0 + jb * BS;  // the block's first key
-            const bool seen = kb < x.hi && (kb + BS > x.lo || kb < x.sink_end);
-            int row = p.oob_row;  // no row of the run sees the block, or a bad id: zeros
-            if (seen && b >= 0 && b < p.num_blocks) row = (b * hkv + x.head) * BS;
+            const int kb = k0 + jb * kBoxRows;  // the box's first key
+            const bool seen = kb < x.hi && (kb + kBoxRows > x.lo || kb < x.sink_end);
+            int row = p.oob_row;  // no row of the run sees any of it, or a bad id: zeros
+            if (seen && b >= 0 && b < p.num_blocks) row = (b * hkv + x.head) * BS + kb % BS;
             else if (seen && p.status && !is_v && hf == 0) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
-            tma_load_2d(ring + s * kTile + hf * Lay::kHalf + jb * BS * 128, tm, hf * 64, row, bar(full0 + s), pol);
+            tma_load_2d(ring + s * kTile + hf * Lay::kHalf + jb * kBoxRows * 128, tm, hf * 64, row, bar(full0 + s), pol);
           }
         }
         if (is_v && lane == 0) run_done(j);
@@ -615,14 +661,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------- S = Q K^T issuer
-      // The slots share one buffer of scores, in two halves of 64 keys: a half's
-      // product goes out once the half before it in its place has been read (the
-      // weights have their own columns), so the products of one half run while the
-      // other is read.
+      // A product goes out once the slot's softmax has read the one before it (its
+      // weights have their own columns), so the next product of a slot runs while
+      // the weights of this one are computed.
       if (tc::elect_one()) {
         // a negative scale is taken as the negated queries' product (bit 13: negate A)
-        const uint32_t kIdS = tc::idesc_bf16(kRows, kTK / 2, false, false) | (p.negate ? 1u << 13 : 0u);
-        int g = 0, nq = 0, np = 0;  // key tiles, query tiles, products so far
+        const uint32_t kIdS = tc::idesc_bf16(kRows, kTK, false, false) | (p.negate ? 1u << 13 : 0u);
+        int g = 0, nq = 0, n[2] = {0, 0};  // key tiles, query tiles, each slot's products so far
         bool ok = true;
         for (int j = 0; ok; ++j) {
           Run x;
@@ -636,23 +681,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t kb = sK + s * kTile;
             for (int q = 0; q < x.ntq; ++q) {
               const int slot = (nq + q) & 1;
+              int &done = slot ? n[1] : n[0];
               if (t == x.t0 && !mbar_wait(bar(BI::kQFull + slot), ((nq + q) >> 1) & 1)) { ok = false; break; }
-              const uint32_t qd = desc_word(sQ + slot * kTile);
-#pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
-                if (np > 0 && !mbar_wait(bar(BI::kSFree + h), (np - 1) & 1)) { ok = false; break; }
-                tc::fence_after();
-                const uint32_t kd = desc_word(kb) + h * ((kTK / 2) * 128 >> 4);
+              if (done > 0 && !mbar_wait(bar(BI::kSFree + slot), (done - 1) & 1)) { ok = false; break; }
+              tc::fence_after();
+              const uint32_t qd = desc_word(sQ + slot * kQTile), kd = desc_word(kb);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                  const uint32_t off = ((ks >> 2) * Lay::kHalf + (ks & 3) * 32) >> 4;
-                  tc::mma(tS + h * (kTK / 2), desc_of(qd + off, kSpanHi), desc_of(kd + off, kSpanHi), kIdS, ks > 0);
-                }
-                tc::commit(bar(BI::kSFull + 2 * slot + h));
-              }
-              if (!ok) break;
+              for (int ks = 0; ks < D / 16; ++ks)
+                tc::mma(tS + slot * kTK, desc_of(qd + (((ks >> 2) * Lay::kQHalf + (ks & 3) * 32) >> 4), kSpanHi),
+                        desc_of(kd + (((ks >> 2) * Lay::kHalf + (ks & 3) * 32) >> 4), kSpanHi), kIdS, ks > 0);
+              tc::commit(bar(BI::kSFull + slot));
               if (t == x.t1 - 1) tc::commit(bar(BI::kQFree + slot));
-              ++np;
+              ++done;
             }
             if (ok) tc::commit(bar(BI::kKEmpty + s));  // the keys are read by these products only
           }
@@ -688,19 +728,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               int &done = slot ? n[1] : n[0];
               // the first product overwrites the accumulator: its last run must have been read
               if (t == x.t0 && use > 0 && !mbar_wait(bar(BI::kOFree + slot), (use - 1) & 1)) { ok = false; break; }
-              const uint32_t acc = tmem + slot * D;
-#pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
-                if (!mbar_wait(bar(BI::kPFull + 2 * slot + h), done & 1)) { ok = false; break; }
-                tc::fence_after();
-                const uint32_t pa = tP + slot * (kTK / 2) + h * (kTK / 4);
-                const uint32_t vd = (desc_word(vb) | (Lay::kHalf >> 4) << 16) + h * ((kTK / 2) * 128 >> 4);
+              const int buf = 2 * slot + (done & 1);
+              if (!mbar_wait(bar(BI::kPFull + buf), (done >> 1) & 1)) { ok = false; break; }
+              tc::fence_after();
+              const uint32_t pa = tP + buf * (kTK / 2), vd = desc_word(vb) | (Lay::kHalf >> 4) << 16;
 #pragma unroll
-                for (int ks = 0; ks < kSteps / 2; ++ks)
-                  tc::mma_ta(acc, pa + ks * 8, desc_of(vd + (ks * 2048 >> 4), kSpanHi), kIdO,
-                             !(t == x.t0 && h == 0 && ks == 0));
-                tc::commit(bar(BI::kPvDone + 2 * slot + h));
-              }
+              for (int ks = 0; ks < kSteps; ++ks)
+                tc::mma_ta(tmem + slot * D, pa + ks * 8, desc_of(vd + (ks * 2048 >> 4), kSpanHi), kIdO,
+                           !(t == x.t0 && ks == 0));
+              tc::commit(bar(BI::kPvDone + buf));
               if (t == x.t1 - 1) tc::commit(bar(BI::kOFull + slot));
               ++done;
             }
@@ -719,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = warp >> 2;
       const int r = threadIdx.x & (kRows - 1);  // query row = TMEM lane
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t tO = tmem + slot * D + lane_off, tSr = tS + lane_off, tPr = tP + slot * (kTK / 2) + lane_off;
-      int g = 0, nq = 0, n = 0;  // key tiles and query tiles of the CTA, halves of key tiles of this slot
+      const uint32_t tO = tmem + slot * D + lane_off, tSr = tS + slot * kTK + lane_off, tPr = tP + slot * kTK + lane_off;
+      int g = 0, nq = 0, n = 0;  // key tiles and query tiles of the CTA, key tiles of this slot
       bool ok = true;
       for (int j = 0; ok; ++j) {
         Run x;
@@ -762,29 +798,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g0 = g;
         g += x.t1 - x.t0;
 #pragma unroll 1
-        for (int u = 2 * x.t0; u < 2 * x.t1; ++u, ++n) {  // halves of key tiles: 64 keys
-          const int h = u & 1, k0 = x.key0(u >> 1);
-          const uint32_t phase = (n >> 1) & 1;
+        for (int t = x.t0; t < x.t1; ++t, ++n) {
+          const int k0 = x.key0(t), buf = n & 1;
           // spare rows see nothing
           const bool full = seen.has(k0);
-          const uint64_t see = full ? (row_valid ? ~0ull : 0ull) : sight.of(k0 + 64 * h);
+          const uint64_t see = full ? (row_valid ? ~0ull : 0ull) : sight.of(k0);
           const bool none = __all_sync(0xffffffffu, see == 0);  // no row of the warp sees any of them
-          if (!wait_warp(bar(BI::kSFull + 2 * slot + h), phase)) { ok = false; break; }
+          if (!wait_warp(bar(BI::kSFull + slot), n & 1)) { ok = false; break; }
           tc::fence_after();
           uint32_t pk[32];
           bool scale_o = false;
           float alpha = 1.f;
           if (none) {
-            mbar_arrive(bar(BI::kSFree + h));
+            mbar_arrive(bar(BI::kSFree + slot));
 #pragma unroll
             for (int k = 0; k < 32; ++k) pk[k] = 0u;
           } else {
             uint32_t sv[64];
-            tc::ld32(tSr + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-            tc::ld32(tSr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+            tc::ld32(tSr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+            tc::ld32(tSr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
             tc::wait_ld();
             tc::fence_before();
-            mbar_arrive(bar(BI::kSFree + h));  // the next product may take their place
+            mbar_arrive(bar(BI::kSFree + slot));  // the next product may take their place
             if (!full) {
               const uint32_t a = static_cast<uint32_t>(see), b = static_cast<uint32_t>(see >> 32);
 #pragma unroll
@@ -807,11 +842,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t nm2 = f32x2_bits(__float_as_uint(-msub), __float_as_uint(-msub));
             l += weights64(sv, ks2, nm2, pk);
           }
-          // this half's last product must be complete before its weights' columns are
-          // written, and every product before the accumulator is
-          if (n > 1 && !wait_warp(bar(BI::kPvDone + 2 * slot + h), phase ^ 1)) { ok = false; break; }
+          // the last product from this buffer must be complete before it is written, and
+          // every product before the accumulator is
+          if (n > 1 && !wait_warp(bar(BI::kPvDone + 2 * slot + buf), ((n >> 1) - 1) & 1)) { ok = false; break; }
           if (__any_sync(0xffffffffu, scale_o)) {  // warp-uniform: tcgen05.ld/st are warp-wide
-            if (!wait_warp(bar(BI::kPvDone + 2 * slot + (h ^ 1)), ((n - 1) >> 1) & 1)) { ok = false; break; }
+            if (!wait_warp(bar(BI::kPvDone + 2 * slot + (buf ^ 1)), ((n - 1) >> 1) & 1)) { ok = false; break; }
             tc::fence_after();
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
@@ -824,10 +859,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tc::fence_after();
-          tc::st32(tPr + h * 32, pk);
+          tc::st32(tPr + buf * (kTK / 2), pk);
           tc::wait_st();
           tc::fence_before();
-          mbar_arrive(bar(BI::kPFull + 2 * slot + h));
+          mbar_arrive(bar(BI::kPFull + 2 * slot + buf));
         }
         if (!ok) break;
         // ---- end of the piece: normalise and store the rows, or store the partial
@@ -885,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int k0 = x.key0(t);
               if (seen.has(k0)) continue;
               for (int k = 0; k < kTK; ++k) {
-                if (!((sight.of(k0 + (k & 64)) >> (k & 63)) & 1)) continue;
+                if (!((sight.of(k0) >> k) & 1)) continue;
                 const int b = p.block_tables[static_cast<size_t>(x.seq) * p.max_blocks + (k0 + k) / BS];
                 if (b < 0 || b >= p.num_blocks) continue;
                 const uint32_t *row = reinterpret_cast<const uint32_t *>(
@@ -1048,9 +1083,10 @@ int tc_launch(const Call &a) {
   const long long rows = static_cast<long long>(a.num_blocks) * a.num_kv_heads * a.block_size;
   CUtensorMap tmq, tmk, tmv;
   // q viewed as [total_q][Hq][d]: a box is 64 columns x G heads x the tile's tokens
+  const int box = std::min(a.block_size, kTK);
   if (!make_tensor_map_3d(&tmq, a.q, a.head_dim, a.num_q_heads, a.total_q, 64, plan.group, plan.tile_tok) ||
-      !make_tensor_map_2d(&tmk, a.k_cache, a.head_dim, rows, 64, a.block_size) ||
-      !make_tensor_map_2d(&tmv, a.v_cache, a.head_dim, rows, 64, a.block_size))
+      !make_tensor_map_2d(&tmk, a.k_cache, a.head_dim, rows, 64, box) ||
+      !make_tensor_map_2d(&tmv, a.v_cache, a.head_dim, rows, 64, box))
     return PKV_ERR_CUDA;
   Params p{};
   p.block_tables = a.block_tables;
