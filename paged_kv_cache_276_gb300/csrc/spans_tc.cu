@@ -26,10 +26,13 @@
 // unnormalised O), and a second kernel joins them in the order of the CTAs:
 // results repeat bit for bit.
 //
-// Both query tiles of a pair are multiplied against each key and value tile: half
-// the traffic per product.  A query tile goes to one of two slots in turn (its
-// queries' buffer, its softmax warps, its accumulator), so that with runs of one
-// tile the next run starts in the other slot while this one is written out.
+// A slot is what works on one query tile: its queries' buffer, softmax warps,
+// scores, weights and accumulator.  Batches of long chunks and of large trees run
+// with two slots in a CTA, one CTA per SM: both query tiles of a pair are multiplied
+// against each key and value tile, half the traffic per product (a query tile
+// without a partner goes to the slots in turn).  Batches of one query tile per
+// sequence run with one slot in a CTA, two CTAs per SM, each over runs of its own:
+// while one starts or ends a run the other streams.
 //
 // Values that a row does not see must not reach it, and 0 times NaN or infinity is
 // NaN: in a tile that is not seen whole, the P V issuer's warp clears the values no
@@ -37,11 +40,11 @@
 // tile's weights are computed; a tile with any of the latter is noted, and the rows
 // that do see one add it when they are written out (rare).
 //
-// Warp roles: 0-3 and 4-7 softmax of slot 0 and 1 (thread = row), 8 TMA producer of
+// Warp roles: four softmax warps per slot (thread = row), then a TMA producer of
 // queries and keys, which also finds the CTA's runs and hands them to the others
-// through a ring of descriptors in shared memory, 9 score-product issuer (one
-// lane) and tensor-memory owner, 10 P V product issuer (one lane), 11 TMA producer
-// of values.
+// through a ring of descriptors in shared memory, the score-product issuer (one
+// lane) and tensor-memory owner, the P V product issuer (one lane), and the TMA
+// producer of values.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -64,54 +67,55 @@ namespace {
 
 constexpr int kRows = 128;       // query rows per tile
 constexpr int kTK = 64;          // keys per tile
-constexpr int kTmemCols = 512;
-constexpr int kKWarp = 8, kMmaWarp = 9, kPvWarp = 10, kVWarp = 11;
-constexpr int kThreads = 12 * 32;
 constexpr float kSlack = 8.f;    // lazy rescale threshold (log2 units)
 constexpr int kRunCost = 256;    // a run's start and end, in keys
 constexpr int kMinRange = 512;   // least weight of a CTA's range, in keys
 constexpr int kRoundsFrom = 4;   // runs per CTA from which most go round the CTAs whole
 constexpr int kMinPiece = 4;     // key tiles that a border leaves on either side
 constexpr int kJoinThreads = 256;
+constexpr int kPairedSeqs = 512;  // sequences up to which two CTAs of one slot fit an SM
 constexpr int kRunRing = 4;      // descriptors of runs ahead
-constexpr int kRunUsers = 11;    // arrivals that free one: 8 softmax warps, two issuers, the value producer
 
-template <int D>
+template <int D, int S>
 struct Layout {
   static_assert(D == 64 || D == 128, "head dim");
+  static_assert(S == 1 || S == 2, "slots");
+  static constexpr int kKWarp = 4 * S, kMmaWarp = kKWarp + 1, kPvWarp = kKWarp + 2, kVWarp = kKWarp + 3;
+  static constexpr int kThreads = (kKWarp + 4) * 32, kCtasPerSm = 3 - S;
   static constexpr int kHalves = D / 64;            // 64-column (128-byte) halves of a row
   static constexpr int kQHalf = kRows * 128;        // one half of a query tile
   static constexpr int kQTile = kHalves * kQHalf;   // [half][128 rows][128 B]
   static constexpr int kHalf = kTK * 128;           // one half of a key or value tile
   static constexpr int kTile = kHalves * kHalf;     // [half][64 rows][128 B]
-  static constexpr int kStages = D == 128 ? 4 : 8;  // of keys, and of values: 64 KB each
-  static constexpr int kSmemK = 2 * kQTile;         // after two query tiles
+  static constexpr int kStages = S * 256 / D;       // of keys, and of values: 32 KB per slot each
+  static constexpr int kSmemK = S * kQTile;         // after the query tiles
   static constexpr int kSmemV = kSmemK + kStages * kTile;
   static constexpr int kSmemBars = kSmemV + kStages * kTile;
-  // tensor memory: each slot's accumulator, then its scores, then its two P
-  static constexpr int kTmemS = 2 * D, kTmemP = kTmemS + 2 * kTK;
-  static_assert(kTmemP + 4 * (kTK / 2) <= kTmemCols, "tensor memory");
-};
-
-// barrier indices (8 bytes each)
-template <int ST>
-struct Bar {
-  static constexpr int kQFull = 0, kQFree = 2, kOFull = 4, kOFree = 6, kSFull = 8, kSFree = 10,  // [slot]
-                       kPFull = 12, kPvDone = 16,  // [slot][buffer of P]
-                       kRunFull = 20, kRunFree = kRunFull + kRunRing, kKFull = kRunFree + kRunRing, kKEmpty = kKFull + ST, kVFull = kKEmpty + ST, kVEmpty = kVFull + ST,
-                       kCount = kVEmpty + ST;
+  // tensor memory: the slots' accumulators, then their scores, then two P of each
+  static constexpr int kTmemCols = S * 256;
+  static constexpr int kTmemS = S * D, kTmemP = kTmemS + S * kTK;
+  static_assert(kTmemP + 2 * S * (kTK / 2) <= kTmemCols, "tensor memory");
+  // barrier indices (8 bytes each)
+  static constexpr int kQFull = 0, kQFree = kQFull + S, kOFull = kQFree + S, kOFree = kOFull + S, kSFull = kOFree + S,
+                       kSFree = kSFull + S,                                // [slot]
+                       kPFull = kSFree + S, kPvDone = kPFull + 2 * S,      // [slot][buffer of P]
+                       kRunFull = kPvDone + 2 * S, kRunFree = kRunFull + kRunRing,
+                       kKFull = kRunFree + kRunRing, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages,
+                       kVEmpty = kVFull + kStages, kBars = (kVEmpty + kStages + 1) / 2 * 2;
 };
 
 // A run's descriptor: the fields of Run in this order.
 constexpr int kRunInts = 12;
 
-template <int D>
+template <int D, int S>
 constexpr size_t smem_bytes(int num_seqs) {
-  using Lay = Layout<D>;
-  return 1024 + Lay::kSmemBars + Bar<Lay::kStages>::kCount * 8 + 16 + kRunRing * kRunInts * 4 +
-         static_cast<size_t>(num_seqs + 1) * 12 + static_cast<size_t>(num_seqs) * 12;
+  using Lay = Layout<D, S>;
+  return 1024 + Lay::kSmemBars + Lay::kBars * 8 + 16 + kRunRing * kRunInts * 4 + static_cast<size_t>(num_seqs + 1) * 12 +
+         static_cast<size_t>(num_seqs) * 12;
 }
-static_assert(smem_bytes<128>(kMaxSeqs) <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<128, 2>(kMaxSeqs) <= 227 * 1024, "shared memory");
+// two CTAs (and 1 KB that the system takes of each) in an SM's 228 KB
+static_assert(smem_bytes<128, 1>(kPairedSeqs) <= 113 * 1024, "shared memory");
 
 struct Params {
   const int32_t *block_tables, *seq_lens, *q_start;
@@ -435,23 +439,28 @@ __device__ bool clear_values(uint32_t tile, const Run &x, int k0, int lane) {
   return odd;
 }
 
-template <int BS, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int BS, int D, int S>
+__global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPerSm)
     spans_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv, const Params p) {
-  using Lay = Layout<D>;
+  using Lay = Layout<D, S>;
+  using BI = Lay;
   constexpr int kStages = Lay::kStages, kHalves = Lay::kHalves, kTile = Lay::kTile, kQTile = Lay::kQTile;
-  using BI = Bar<kStages>;
+  constexpr int kKWarp = Lay::kKWarp, kMmaWarp = Lay::kMmaWarp, kPvWarp = Lay::kPvWarp, kVWarp = Lay::kVWarp;
+  constexpr int kTmemCols = Lay::kTmemCols, kThreads = Lay::kThreads;
+  // the slot of the n-th query tile, and how many tiles the slot had before it
+  auto slot_of = [](int n) { return S == 2 ? n & 1 : 0; };
+  auto use_of = [](int n) { return S == 2 ? n >> 1 : n; };
   // one TMA box per block of the tile (a block longer than the tile: the tile's piece of it)
   constexpr int kBoxRows = BS < kTK ? BS : kTK, kBoxes = kTK / kBoxRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kSmemBars);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + BI::kCount);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + BI::kBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *odd_tile = reinterpret_cast<int *>(tmem_slot + 2);  // 1 + the last key tile (counted over the CTA) whose values are not all finite
-  volatile int *runs = reinterpret_cast<volatile int *>(bars + BI::kCount + 2);  // [kRunRing][kRunInts]
-  long long *prefix = reinterpret_cast<long long *>(bars + BI::kCount + 2 + kRunRing * kRunInts / 2);  // [B + 1]
+  volatile int *runs = reinterpret_cast<volatile int *>(bars + BI::kBars + 2);  // [kRunRing][kRunInts]
+  long long *prefix = reinterpret_cast<long long *>(bars + BI::kBars + 2 + kRunRing * kRunInts / 2);  // [B + 1]
   int *first = reinterpret_cast<int *>(prefix + p.num_seqs + 1);             // [B + 1]
   int *lens = first + p.num_seqs + 1;                                        // [B]
   int *qs = lens + p.num_seqs, *qc = qs + p.num_seqs;                        // [B] each
@@ -502,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) prefix[0] = 0, first[0] = 0;
   }
   if (threadIdx.x == 32 * kKWarp) {
-    for (int i = 0; i < 2; ++i) {  // one per slot
+    for (int i = 0; i < S; ++i) {  // one per slot
       mbar_init(bar(BI::kQFull + i), 1);
       mbar_init(bar(BI::kQFree + i), 1);
       mbar_init(bar(BI::kOFull + i), 1);
@@ -516,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kRunRing; ++i) {
       mbar_init(bar(BI::kRunFull + i), 1);
-      mbar_init(bar(BI::kRunFree + i), kRunUsers);
+      mbar_init(bar(BI::kRunFree + i), 4 * S + 3);  // the softmax warps, two issuers, the value producer
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(BI::kKFull + s), 1);
@@ -534,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (p.tile_tok * p.group < kRows) {
     // the loads fill the tile's first tile_tok * G rows only: the rest stay zero
-    for (int i = threadIdx.x; i < 2 * kQTile / 16; i += kThreads)
+    for (int i = threadIdx.x; i < S * kQTile / 16; i += kThreads)
       asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_u32(smem) + i * 16), "r"(0u) : "memory");
     fence_proxy_async_shared();
   }
@@ -560,7 +569,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto run_done = [&](int j) { mbar_arrive(bar(BI::kRunFree + j % kRunRing)); };
 
+  // one slot: 128 registers a thread at launch (256 threads, two CTAs) do not hold a
+  // softmax; 128 (160 + 96) are as many
   if (warp >= kKWarp) {
+    if constexpr (S == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == kKWarp || warp == kVWarp) {
       // ------------------------------------- producers: runs, K (+ Q); V
       const bool is_v = warp == kVWarp;
@@ -604,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!is_v && x.t0 < x.t1) {
           bool ok = true;
           for (int q = 0; q < x.ntq && ok; ++q, ++nq) {
-            const int slot = nq & 1, use = nq >> 1;
+            const int slot = slot_of(nq), use = use_of(nq);
             if (use > 0 && !wait_warp(bar(BI::kQFree + slot), (use - 1) & 1)) ok = false;
             if (ok && lane == 0) {
               mbar_arrive_expect_tx(bar(BI::kQFull + slot), p.tile_tok * p.group * D * 2);  // the boxes' bytes
@@ -655,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int y = g > kStages ? g - kStages : 0; y < g; ++y)
           mbar_wait_sleep(bar(full0 + (y % kStages)), (y / kStages) & 1);
         if (!is_v) {
-          for (int y = nq > 2 ? nq - 2 : 0; y < nq; ++y) mbar_wait_sleep(bar(BI::kQFull + (y & 1)), (y >> 1) & 1);
+          for (int y = nq > S ? nq - S : 0; y < nq; ++y) mbar_wait_sleep(bar(BI::kQFull + slot_of(y)), use_of(y) & 1);
           if (p.ws_desc) p.ws_desc[blockIdx.x] = desc;
         }
       }
@@ -680,9 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!mbar_wait(bar(BI::kKFull + s), (g / kStages) & 1)) { ok = false; break; }
             const uint32_t kb = sK + s * kTile;
             for (int q = 0; q < x.ntq; ++q) {
-              const int slot = (nq + q) & 1;
+              const int slot = slot_of(nq + q);
               int &done = slot ? n[1] : n[0];
-              if (t == x.t0 && !mbar_wait(bar(BI::kQFull + slot), ((nq + q) >> 1) & 1)) { ok = false; break; }
+              if (t == x.t0 && !mbar_wait(bar(BI::kQFull + slot), use_of(nq + q) & 1)) { ok = false; break; }
               if (done > 0 && !mbar_wait(bar(BI::kSFree + slot), (done - 1) & 1)) { ok = false; break; }
               tc::fence_after();
               const uint32_t qd = desc_word(sQ + slot * kQTile), kd = desc_word(kb);
@@ -724,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!seen.has(k0) && clear_values<D>(vb, x, k0, lane) && lane == 0) *odd_tile = g + 1;
           if (tc::elect_one()) {
             for (int q = 0; q < x.ntq && ok; ++q) {
-              const int slot = (nq + q) & 1, use = (nq + q) >> 1;
+              const int slot = slot_of(nq + q), use = use_of(nq + q);
               int &done = slot ? n[1] : n[0];
               // the first product overwrites the accumulator: its last run must have been read
               if (t == x.t0 && use > 0 && !mbar_wait(bar(BI::kOFree + slot), (use - 1) & 1)) { ok = false; break; }
@@ -751,6 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------ softmax warps
+    if constexpr (S == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     {
       const int slot = warp >> 2;
       const int r = threadIdx.x & (kRows - 1);  // query row = TMEM lane
@@ -766,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool any = x.t0 < x.t1;
         // the run's query tile in this slot: without keys (nothing goes through the
         // slots) tile `slot` of the run
-        const int q = any ? (slot - nq) & 1 : slot, use = (nq + q) >> 1;
+        const int q = S == 1 ? 0 : any ? (slot - nq) & 1 : slot, use = use_of(nq + q);
         if (any) nq += x.ntq;
         if (q >= x.ntq) {
           g += x.t1 - x.t0;
@@ -1019,7 +1032,7 @@ __global__ void __launch_bounds__(kJoinThreads) spans_join_kernel(const Params p
 
 // ------------------------------------------------------------------ host
 struct Plan {
-  int group, tile_tok, span, piece_rows;
+  int group, tile_tok, span, piece_rows, slots, grid;
   bool split;  // some run may be cut
   size_t o_bytes, ml_bytes, desc_bytes;
   size_t bytes() const { return split ? o_bytes + ml_bytes + desc_bytes : 0; }
@@ -1031,8 +1044,13 @@ Plan make_plan(const Call &a) {
   plan.tile_tok = kRows / plan.group;
   const int longest = a.mask ? a.max_nodes : a.total_q;  // tokens of a chunk or tree, at most
   plan.tile_tok = std::min(plan.tile_tok, std::max(1, longest));
-  plan.span = longest > plan.tile_tok ? 2 * plan.tile_tok : plan.tile_tok;
-  plan.piece_rows = plan.span > plan.tile_tok ? 2 * kRows : kRows;
+  // pairs of query tiles where the trees may have two, or the chunks have on average
+  const bool pairs = a.mask ? a.max_nodes > plan.tile_tok
+                            : a.total_q > static_cast<long long>(plan.tile_tok) * a.num_seqs;
+  plan.slots = pairs || a.num_seqs > kPairedSeqs ? 2 : 1;
+  plan.span = pairs ? 2 * plan.tile_tok : plan.tile_tok;
+  plan.grid = num_sms() * (3 - plan.slots);
+  plan.piece_rows = pairs ? 2 * kRows : kRows;
   // a run of fewer tiles than two least pieces is never cut
   long long keys = a.max_seq_len;
   if (!a.mask) {
@@ -1040,35 +1058,36 @@ Plan make_plan(const Call &a) {
     keys = std::min(keys, static_cast<long long>(a.window) + plan.span + 2 * kTK + sunk);
   }
   plan.split = (keys + kTK - 1) / kTK >= 2 * kMinPiece;
-  const size_t pieces = 2 * static_cast<size_t>(num_sms());
+  const size_t pieces = 2 * static_cast<size_t>(plan.grid);
   plan.o_bytes = pieces * plan.piece_rows * a.head_dim * sizeof(float);
   plan.ml_bytes = pieces * plan.piece_rows * sizeof(float2);
-  plan.desc_bytes = static_cast<size_t>(num_sms()) * sizeof(int4);
+  plan.desc_bytes = static_cast<size_t>(plan.grid) * sizeof(int4);
   return plan;
 }
 
 using KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Params);
 
-template <int D>
+template <int D, int S>
 KernelFn pick_kernel(int block_size) {
   switch (block_size) {
-    case 16: return spans_tc_kernel<16, D>;
-    case 32: return spans_tc_kernel<32, D>;
-    case 64: return spans_tc_kernel<64, D>;
-    default: return spans_tc_kernel<128, D>;
+    case 16: return spans_tc_kernel<16, D, S>;
+    case 32: return spans_tc_kernel<32, D, S>;
+    case 64: return spans_tc_kernel<64, D, S>;
+    default: return spans_tc_kernel<128, D, S>;
   }
 }
 
-template <int D>
+template <int D, int S>
 int launch(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const Params &p, int block_size,
-           bool split, cudaStream_t stream) {
-  const KernelFn kernel = pick_kernel<D>(block_size);
+           const Plan &plan, cudaStream_t stream) {
+  const KernelFn kernel = pick_kernel<D, S>(block_size);
+  const size_t smem = smem_bytes<D, S>(p.num_seqs);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem_bytes<D>(kMaxSeqs)));
-  const unsigned grid = static_cast<unsigned>(num_sms());
-  if (e == cudaSuccess) e = launch_overlapped(kernel, grid, kThreads, smem_bytes<D>(p.num_seqs), stream, tmq, tmk, tmv, p);
-  if (e == cudaSuccess && split)
-    e = launch_overlapped(spans_join_kernel<D>, dim3(grid, 8), kJoinThreads, 0, stream, p, static_cast<int>(grid));
+                                       static_cast<int>(smem_bytes<D, S>(S == 2 ? kMaxSeqs : kPairedSeqs)));
+  const unsigned grid = static_cast<unsigned>(plan.grid);
+  if (e == cudaSuccess) e = launch_overlapped(kernel, grid, Layout<D, S>::kThreads, smem, stream, tmq, tmk, tmv, p);
+  if (e == cudaSuccess && plan.split)
+    e = launch_overlapped(spans_join_kernel<D>, dim3(grid, 8), kJoinThreads, 0, stream, p, plan.grid);
   return e == cudaSuccess ? PKV_OK : (set_cuda_error(e), PKV_ERR_CUDA);
 }
 
@@ -1081,6 +1100,8 @@ int tc_launch(const Call &a) {
   if (plan.bytes() > 0 && (!a.workspace || a.workspace_bytes < plan.bytes() || !aligned16(a.workspace)))
     return PKV_ERR_WORKSPACE;
   const long long rows = static_cast<long long>(a.num_blocks) * a.num_kv_heads * a.block_size;
+  // runs are counted in 32 bits
+  if ((a.total_q / plan.span + static_cast<long long>(a.num_seqs)) * a.num_kv_heads >= (1ll << 31)) return PKV_ERR_UNSUPPORTED;
   CUtensorMap tmq, tmk, tmv;
   // q viewed as [total_q][Hq][d]: a box is 64 columns x G heads x the tile's tokens
   const int box = std::min(a.block_size, kTK);
@@ -1119,8 +1140,12 @@ int tc_launch(const Call &a) {
   p.piece_rows = plan.piece_rows;
   p.scale_log2 = kernel_scale_log2(std::fabs(a.scale));
   p.negate = a.scale < 0.f;
-  return a.head_dim == 64 ? launch<64>(tmq, tmk, tmv, p, a.block_size, plan.split, as_stream(a.stream))
-                          : launch<128>(tmq, tmk, tmv, p, a.block_size, plan.split, as_stream(a.stream));
+  const cudaStream_t st = as_stream(a.stream);
+  if (plan.slots == 1)
+    return a.head_dim == 64 ? launch<64, 1>(tmq, tmk, tmv, p, a.block_size, plan, st)
+                            : launch<128, 1>(tmq, tmk, tmv, p, a.block_size, plan, st);
+  return a.head_dim == 64 ? launch<64, 2>(tmq, tmk, tmv, p, a.block_size, plan, st)
+                          : launch<128, 2>(tmq, tmk, tmv, p, a.block_size, plan, st);
 }
 
 }  // namespace spans
