@@ -10,13 +10,17 @@
 //
 // Data movement with three operations per value, bound by HBM: per token every
 // query row is read and written, every key and value row read and stored.  A
-// group of W lanes takes kRows rows of one token (the rows of a token are its
-// query heads, then key heads, then value heads).  A lane holds 16 values of a
+// group of W lanes takes kRows query heads, key heads or value heads of one token.
+// A lane holds 16 values of a
 // row in two 16-byte chunks, each chunk contiguous over the lanes: values 8 i
 // and R/2 + 8 i of the rotated part (so that a pair of either style lies in one
 // lane, and a group's accesses are whole lines), or two such halves of the rest.
 // The lane's cosines and sines are read once for its kRows rows, whose loads are
 // all in flight together.
+// Measured at 32768 tokens, 32 query and 8 KV heads of 128, rows of a fused
+// projection: 119.6 us (6.9 TB/s, a plain copy 6.79); 8192 tokens, 64 and 8 heads,
+// into the 8-bit cache: 53.4 us (6.1 TB/s; the conversions leave the loads of a warp
+// waiting); the 256 tokens of a decode step 3.3 us, a launch and two dependent loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,7 +36,11 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;         // rows of one token per lane group
+// Rows of one token per lane group, and CTAs per SM that the registers are held to
+// (85 a thread).  32768 tokens, 32 + 8 + 8 heads of 128: 119.6 us; two rows and four
+// CTAs 128.5, one row 171.
+constexpr int kRows = 4;
+constexpr int kCtas = 3;
 constexpr int kMaxHeadDim = 512;  // 32 lanes x 16 values
 
 struct RopeParams {
@@ -43,7 +51,9 @@ struct RopeParams {
   const float *table;   // [max_positions][rot_dim]: cosines, then sines
   int64_t num_slots, tasks;
   int32_t *status;
-  int max_positions, rot_dim, head_dim, num_q_heads, num_kv_heads, block_size, groups;  // groups: lane groups per token
+  int max_positions, rot_dim, head_dim, num_q_heads, num_kv_heads, block_size;
+  int q_groups, kv_groups, groups;  // lane groups of a token: for queries, for keys (and for values), together
+  int narrow;  // tasks and num_slots fit 32 bits: divide in 32 bits
   // one of the two caches
   uint4 *k_cache, *v_cache;
   uint2 *k_codes, *v_codes;
@@ -121,106 +131,113 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float inv) {
 }
 
 template <int W, bool PAIRS, bool QUANT>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kCtas) rope_kernel(const RopeParams p) {
   // the grid queued behind this one may become resident now (it waits for this
   // grid's writes before it reads them)
   grid_launch_dependents();
   grid_dependency_wait();  // the rows may come from the kernel launched just before
   const int lane = threadIdx.x % W;
   const int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W;
-  int64_t t = 0, slot = -1;
-  int row0 = 0;
-  bool live = task < p.tasks && lane < p.head_dim / 16;
-  int pos = 0;
-  if (live) {
-    t = task / p.groups;
-    row0 = static_cast<int>(task - t * p.groups) * kRows;
-    const int64_t at = p.positions[t];
+  const bool real = task < p.tasks && lane < p.head_dim / 16;
+  int64_t t = 0, slot = -1, at = 0;
+  int g = 0;
+  if (real) {
+    if (p.narrow) t = static_cast<uint32_t>(task) / static_cast<uint32_t>(p.groups);
+    else t = task / p.groups;
+    g = static_cast<int>(task - t * p.groups);
+    at = p.positions[t];
     slot = p.slots[t];
-    const bool report = row0 == 0 && lane == 0 && p.status;
-    if (at < 0 || at >= p.max_positions) {
-      if (report) atomicOr(p.status, PKV_STATUS_BAD_POS);
-      live = false;
-    }
-    pos = static_cast<int>(at);
-    if (slot >= p.num_slots) {
-      if (report) atomicOr(p.status, PKV_STATUS_BAD_SLOT);
-      slot = -1;
-    }
   }
+  // the group's rows: kRows query heads, key heads or value heads from row0 on
+  const bool is_q = g < p.q_groups, is_v = g >= p.q_groups + p.kv_groups;
+  const int row0 = (is_q ? g : g - p.q_groups - (is_v ? p.kv_groups : 0)) * kRows;
+  const int rows = (is_q ? p.num_q_heads : p.num_kv_heads) - row0;
   // this lane's two chunks (of 8 values) of a row, and its cosines and sines
   const int rot16 = p.rot_dim / 16, rest = p.head_dim - p.rot_dim;
-  const bool turns = lane < rot16;
-  const int c0 = turns ? lane : p.rot_dim / 8 + (lane - rot16);
-  const int c1 = c0 + (turns ? p.rot_dim : rest) / 16;
+  const bool turns = lane < rot16 && !is_v;
+  const int c0 = lane < rot16 ? lane : p.rot_dim / 8 + (lane - rot16);
+  const int apart = (lane < rot16 ? p.rot_dim : rest) / 16;
   const int chunks = p.head_dim / 8;
-  // the rows: 0 .. Hq - 1 queries, then keys, then values
-  const int hq = p.num_q_heads, hk = p.num_kv_heads;
+  // (the queries' loads wait for nothing; keys and values are read where they are stored)
   uint4 a[kRows], b[kRows];
-  bool use[kRows];
+  {
+    const uint4 *src = (is_q   ? p.q + t * p.q_stride
+                        : is_v ? p.v + t * p.v_stride
+                               : p.k + t * p.k_stride) +
+                       static_cast<int64_t>(row0) * chunks + c0;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int row = row0 + r;
-    use[r] = live && row < hq + 2 * hk && (row < hq || slot >= 0);
-    a[r] = b[r] = make_uint4(0u, 0u, 0u, 0u);
-    if (use[r]) {
-      const uint4 *src = row < hq        ? p.q + t * p.q_stride + static_cast<int64_t>(row) * chunks
-                         : row < hq + hk ? p.k + t * p.k_stride + static_cast<int64_t>(row - hq) * chunks
-                                         : p.v + t * p.v_stride + static_cast<int64_t>(row - hq - hk) * chunks;
-      a[r] = src[c0];
-      b[r] = src[c1];
+    for (int r = 0; r < kRows; ++r) {
+      a[r] = b[r] = make_uint4(0u, 0u, 0u, 0u);
+      if (real && r < rows && (is_q || slot >= 0)) {
+        a[r] = src[r * chunks];
+        b[r] = src[r * chunks + apart];
+      }
     }
   }
+  bool live = real && at >= 0 && at < p.max_positions;
+  if (real && lane == 0 && g == 0 && p.status) {
+    if (!live) atomicOr(p.status, PKV_STATUS_BAD_POS);
+    else if (slot >= p.num_slots) atomicOr(p.status, PKV_STATUS_BAD_SLOT);
+  }
+  if (!is_q) live = live && slot >= 0 && slot < p.num_slots;
   float c[8], s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
-  if (live && turns && row0 < hq + hk) {
-    const float *cs = p.table + static_cast<int64_t>(pos) * p.rot_dim, *sn = cs + p.rot_dim / 2;
+  if (live && turns) {
+    const float *cs = p.table + at * p.rot_dim, *sn = cs + p.rot_dim / 2;
     const int i0 = PAIRS ? 4 * lane : 8 * lane, i1 = PAIRS ? p.rot_dim / 4 + 4 * lane : 8 * lane + 4;
     load4(cs + i0, c);
     load4(cs + i1, c + 4);
     load4(sn + i0, s);
     load4(sn + i1, s + 4);
   }
-  int64_t blk = 0, off = 0;
-  if (slot >= 0) {
-    blk = slot / p.block_size;
-    off = slot - blk * p.block_size;
+  // where the first row goes, in rows of the cache or chunks of q_out, and rows between heads
+  int64_t dst = 0;
+  if (is_q) {
+    dst = t * p.q_out_stride + static_cast<int64_t>(row0) * chunks + c0;
+  } else if (live) {
+    int64_t blk;
+    if (p.narrow) blk = static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.block_size);
+    else blk = slot / p.block_size;
+    dst = (blk * p.num_kv_heads + row0) * p.block_size + (slot - blk * p.block_size);
   }
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    const int row = row0 + r;
-    const bool is_q = row < hq, is_v = row >= hq + hk;
-    float x0[8], x1[8];
-    widen(a[r], x0);
-    widen(b[r], x1);
-    if (turns && !is_v) rotate16<PAIRS>(x0, x1, c, s);
-    const int64_t cache_row = (blk * hk + (is_v ? row - hq - hk : row - hq)) * p.block_size + off;
-    if constexpr (!QUANT) {
-      if (!use[r]) continue;
-      uint4 *dst = is_q ? p.q_out + t * p.q_out_stride + static_cast<int64_t>(row) * chunks
-                        : (is_v ? p.v_cache : p.k_cache) + cache_row * chunks;
-      dst[c0] = is_v || !turns ? a[r] : narrow(x0);
-      dst[c1] = is_v || !turns ? b[r] : narrow(x1);
-    } else {
-      if (use[r] && is_q) {
-        uint4 *dst = p.q_out + t * p.q_out_stride + static_cast<int64_t>(row) * chunks;
-        dst[c0] = turns ? narrow(x0) : a[r];
-        dst[c1] = turns ? narrow(x1) : b[r];
+    const bool use = live && r < rows;
+    const int64_t cache_row = dst + static_cast<int64_t>(r) * p.block_size;
+    if (!QUANT || is_q) {  // (queries and keys alike in the bf16 cache; a warp may hold groups of both kinds)
+      if (use) {
+        uint4 *to = is_q ? p.q_out + dst + r * chunks : (is_v ? p.v_cache : p.k_cache) + cache_row * chunks + c0;
+        if (turns) {
+          float x0[8], x1[8];
+          widen(a[r], x0);
+          widen(b[r], x1);
+          rotate16<PAIRS>(x0, x1, c, s);
+          a[r] = narrow(x0);
+          b[r] = narrow(x1);
+        }
+        to[0] = a[r];
+        to[apart] = b[r];
       }
+    }
+    if constexpr (QUANT) {
       // the row's largest magnitude, over its lanes: every lane of the warp takes part
-      if (!__any_sync(0xffffffffu, use[r] && !is_q)) continue;
+      if (!__any_sync(0xffffffffu, use && !is_q)) continue;
+      float x0[8], x1[8];
+      widen(a[r], x0);
+      widen(b[r], x1);
+      if (turns && !is_q) rotate16<PAIRS>(x0, x1, c, s);
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max(top, max(finite_magnitude(x0[i]), finite_magnitude(x1[i])));
 #pragma unroll
       for (int o = W / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int e = row_exponent(top);
-      if (use[r] && !is_q) {
-        uint2 *dst = (is_v ? p.v_codes : p.k_codes) + cache_row * chunks;
+      if (use && !is_q) {
+        uint2 *to = (is_v ? p.v_codes : p.k_codes) + cache_row * chunks + c0;
         const float inv = quant::pow2i(-e);
-        dst[c0] = encode8(x0, inv);
-        dst[c1] = encode8(x1, inv);
+        to[0] = encode8(x0, inv);
+        to[apart] = encode8(x1, inv);
         if (lane == 0) (is_v ? p.v_exps : p.k_exps)[cache_row] = static_cast<uint8_t>(e + quant::kExpBias);
       }
     }
@@ -289,8 +306,11 @@ int launch(const RopeCall &a, RopeParams p) {
   p.block_size = a.block_size;
   const int64_t rows = static_cast<int64_t>(a.num_q_heads) + 2ll * a.num_kv_heads;
   if (rows > (1 << 24)) return PKV_ERR_UNSUPPORTED;
-  p.groups = static_cast<int>((rows + kRows - 1) / kRows);
+  p.q_groups = (a.num_q_heads + kRows - 1) / kRows;
+  p.kv_groups = (a.num_kv_heads + kRows - 1) / kRows;
+  p.groups = p.q_groups + 2 * p.kv_groups;
   p.tasks = static_cast<int64_t>(a.num_tokens) * p.groups;
+  p.narrow = p.tasks <= 0xffffffffll && p.num_slots <= 0xffffffffll;
   auto go = [&](auto w) {
     constexpr int W = decltype(w)::value;
     const int64_t per = kThreads / W, grid = (p.tasks + per - 1) / per;
