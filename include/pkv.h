@@ -746,6 +746,11 @@ int pkv_write_rope_quant(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v
  *                 paged_attention_window_workspace_size(...) bytes (may be NULL
  *                 when that is 0); its contents need not be initialised and are
  *                 not preserved.  Calls that may overlap need one each
+ *                 The size is 0 or, where runs of keys may be divided, that of all
+ *                 divisions (40 MB at head_dim 128 on 152 SMs); it does not depend
+ *                 on num_seqs and total_q (which are there for their checks: sizes
+ *                 that no call has give 0) and never shrinks as max_seq_len grows,
+ *                 so that one buffer serves every batch
  *   everything else as paged_attention_prefill
  * Keys and values that a row does not see never reach its result, whatever they
  * hold (NaN and infinities included).  A row whose visible scores are all -inf

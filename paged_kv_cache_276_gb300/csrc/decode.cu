@@ -837,6 +837,10 @@ bool make_tensor_map_3d(void *map, const void *base, int dim0, int dim1, long lo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tensor_map_rows(void *map, const void *base, int head_dim, int box_rows, long long rows) {
+  return make_cache_map(static_cast<CUtensorMap *>(map), base, head_dim, box_rows, rows);
+}
+
 bool make_tensor_map_bytes(void *map, const void *base, long long rows, int box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;

@@ -17,6 +17,10 @@ bool make_tensor_map_2d(void *map, const void *base, int dim0, long long dim1, i
 bool make_tensor_map_3d(void *map, const void *base, int dim0, int dim1, long long dim2, int box0, int box1,
                         int box2);
 
+// The cache as rows of head_dim bf16, read box_rows at a time, both 64-column halves
+// of head_dim 128 in one box, [half][row][64] (decode.cu).
+bool make_tensor_map_rows(void *map, const void *base, int head_dim, int box_rows, long long rows);
+
 // Bytes as rows of 128, read box_rows at a time with the 128-byte swizzle (decode.cu).
 bool make_tensor_map_bytes(void *map, const void *base, long long rows, int box_rows);
 

@@ -36,5 +36,9 @@ struct Call {
 size_t tc_workspace_size(const Call &a);
 int tc_launch(const Call &a);
 
+// Single tokens, one per sequence (spans_step.cu).
+size_t step_workspace_size(const Call &a);
+int step_launch(const Call &a);
+
 }  // namespace spans
 }  // namespace pkv

@@ -1051,17 +1051,19 @@ Plan make_plan(const Call &a) {
   plan.span = pairs ? 2 * plan.tile_tok : plan.tile_tok;
   plan.grid = num_sms() * (3 - plan.slots);
   plan.piece_rows = pairs ? 2 * kRows : kRows;
-  // a run of fewer tiles than two least pieces is never cut
+  // A run of fewer tiles than two least pieces is never cut.  This and the sizes below
+  // go by the longest runs that any batch of these heads and lengths has, so that one
+  // workspace serves every batch: two pieces per CTA, 2 x 256 rows of them per SM.
   long long keys = a.max_seq_len;
   if (!a.mask) {
     const long long sunk = (static_cast<long long>(a.sinks) + kTK - 1) / kTK * kTK;
-    keys = std::min(keys, static_cast<long long>(a.window) + plan.span + 2 * kTK + sunk);
+    keys = std::min(keys, static_cast<long long>(a.window) + 2 * kRows + 2 * kTK + sunk);
   }
   plan.split = (keys + kTK - 1) / kTK >= 2 * kMinPiece;
-  const size_t pieces = 2 * static_cast<size_t>(plan.grid);
-  plan.o_bytes = pieces * plan.piece_rows * a.head_dim * sizeof(float);
-  plan.ml_bytes = pieces * plan.piece_rows * sizeof(float2);
-  plan.desc_bytes = static_cast<size_t>(plan.grid) * sizeof(int4);
+  const size_t rows = static_cast<size_t>(num_sms()) * 4 * kRows;
+  plan.o_bytes = rows * a.head_dim * sizeof(float);
+  plan.ml_bytes = rows * sizeof(float2);
+  plan.desc_bytes = static_cast<size_t>(num_sms()) * 2 * sizeof(int4);
   return plan;
 }
 
