@@ -139,6 +139,17 @@ constexpr int kEnds = 2;    // the run that the CTA goes on with (piece 0) ends 
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// a / b for a >= 0, b > 0 and a quotient below 2^31, in few instructions: an estimate
+// and single steps.
+__device__ __forceinline__ int divide(long long a, long long b) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+#pragma unroll 1
+  while (q * b > a) --q;
+#pragma unroll 1
+  while ((q + 1ll) * b <= a) ++q;
+  return q;
+}
+
 // Per-sequence values kept in shared memory.
 struct SeqTab {
   const long long *prefix;  // [B + 1] weight before each sequence
@@ -150,10 +161,10 @@ struct SeqTab {
 //   i < bent:  base + span (i + 1)     (its window still reaches the first token)
 //   else       flat
 struct Weights {
-  long long base, flat, bent;
-  int span, runs;
+  long long base, flat;
+  int bent, span, runs;
   __device__ Weights() {}
-  __device__ Weights(const Params &p, int L, int c) {
+  __device__ __forceinline__ Weights(const Params &p, int L, int c) {
     span = p.span;
     runs = ceil_div(c, span);
     if (p.mask) {
@@ -163,26 +174,29 @@ struct Weights {
     } else {
       const long long ctx = max(0, L - c);
       const long long reach = static_cast<long long>(p.window) - 1 + (static_cast<long long>(p.sinks) + kTK - 1) / kTK * kTK;
-      bent = ctx > reach ? 0 : min(static_cast<long long>(runs), (reach - ctx) / span + 1);
+      // at most runs, so that the division fits 32 bits
+      const long long room = min(reach - ctx, static_cast<long long>(runs) * span);
+      bent = room < 0 ? 0 : min(runs, static_cast<int>(static_cast<uint32_t>(room) / static_cast<uint32_t>(span)) + 1);
       base = kRunCost + ctx;
       flat = kRunCost + span + reach;
     }
   }
-  __device__ long long of(int i) const { return i < bent ? base + static_cast<long long>(span) * (i + 1) : flat; }
-  __device__ long long sum(long long m) const {  // of the first m runs
+  __device__ __forceinline__ long long of(int i) const { return i < bent ? base + static_cast<long long>(span) * (i + 1) : flat; }
+  __device__ __forceinline__ long long sum(int m) const {  // of the first m runs
     const long long b = min(m, bent);
     return b * base + span * (b * (b + 1) / 2) + (m - b) * flat;
   }
   // the run that holds weight x, 0 <= x < sum(runs)
-  __device__ int find(long long x) const {
+  __device__ __forceinline__ int find(long long x) const {
     const long long s = sum(bent);
-    if (x >= s) return static_cast<int>(bent + (x - s) / flat);
-    long long lo = 0, hi = bent;
+    if (x >= s) return bent + divide(x - s, flat);
+    int lo = 0, hi = bent;
+#pragma unroll 1
     while (hi - lo > 1) {
-      const long long mid = (lo + hi) >> 1;
+      const int mid = (lo + hi) >> 1;
       if (sum(mid) <= x) lo = mid; else hi = mid;
     }
-    return static_cast<int>(lo);
+    return lo;
   }
 };
 
@@ -223,112 +237,102 @@ struct Common {
 };
 
 // The runs of this CTA in order: first whole rounds (run c, c + grid, ... for CTA
-// c), then its range of the weight of the rest.
+// c), then its range of the weight of the rest.  One call site and little code: the
+// roles share the SM's instruction cache.
 struct Sched {
   long long xa, xb, s;  // the CTA's range; the current run's start
-  int seq, head, i, round, rounds, grid;
-  bool done;
+  int seq, head, i, round, rounds;
   Weights w;  // of the current sequence
   Run x;
 
-  __device__ void begin(const Params &p, const SeqTab &t) {
-    grid = gridDim.x;
-    const int runs = t.first[p.num_seqs];
+  __device__ __forceinline__ Sched(const Params &p, const SeqTab &t) {
+    const int runs = t.first[p.num_seqs], grid = gridDim.x;
     rounds = !p.mask && runs >= kRoundsFrom * grid ? runs / grid - 1 : 0;
-    round = 0;
-    done = false;
-    if (rounds > 0) whole_run(p, t);
-    else begin_range(p, t);
+    round = -1;
   }
-  __device__ void next(const Params &p, const SeqTab &t) {
-    if (round < rounds) {
-      if (++round < rounds) whole_run(p, t);
-      else begin_range(p, t);
+
+  // the next run into x; false: there is none
+  __device__ __forceinline__ bool next(const Params &p, const SeqTab &t) {
+    const int grid = gridDim.x;
+    ++round;
+    if (round <= rounds) {
+      // a whole round's run, or the first run behind the rounds
+      const int run = round * grid + (round < rounds ? blockIdx.x : 0);
+      long long lo = search(t.first, p.num_seqs, run);
+      if (rounds > 0) {
+        enter(p, t, static_cast<int>(lo));
+        const int off = run - t.first[seq];
+        head = static_cast<unsigned>(off) / static_cast<unsigned>(w.runs);
+        i = off - head * w.runs;
+      }
+      if (round == rounds) {  // this CTA's range of the rest
+        const long long start = rounds > 0 ? t.prefix[seq] + head * w.sum(w.runs) + w.sum(i) : 0;
+        const long long rest = t.prefix[p.num_seqs] - start;
+        const int c = blockIdx.x, ctas = static_cast<int>(max(1ll, min(static_cast<long long>(grid), rest / kMinRange)));
+        const long long each = rest / ctas;
+        const unsigned more = static_cast<unsigned>(rest - each * ctas);
+        xa = start + each * c + more * c / ctas;
+        xb = start + each * (c + 1) + more * (c + 1) / ctas;
+        if (c >= ctas || xa >= xb) return false;
+        enter(p, t, search(t.prefix, p.num_seqs, xa));
+        const long long per_head = w.sum(w.runs), off = xa - t.prefix[seq];
+        head = divide(off, per_head);
+        i = w.find(off - head * per_head);
+        s = t.prefix[seq] + head * per_head + w.sum(i);
+      }
     } else {
       step(p, t);
-      settle(p, t);
+    }
+#pragma unroll 1
+    for (;; step(p, t)) {  // from this run on: the first that the CTA has a piece of
+      const bool whole = round < rounds;
+      if (!whole && (s >= xb || seq >= p.num_seqs)) return false;
+      geometry(p, t.lens[seq], t.qc[seq]);
+      x.t0 = 0;
+      x.t1 = x.n;
+      if (whole) return true;
+      const long long weight = w.of(i);
+      if (xa > s) x.t0 = border(xa - s, weight);
+      if (xb < s + weight) x.t1 = border(xb - s, weight);
+      // a run without keys belongs to the CTA that holds its start; a range inside a
+      // tile is an empty piece, which the join expects
+      if (x.n == 0 ? xa <= s : x.t0 < x.t1 || (x.t0 > 0 && x.t0 < x.n)) return true;
     }
   }
 
  private:
-  __device__ void enter(const Params &p, const SeqTab &t, int sequence) {
+  // the last of the n sequences that begins at or before x
+  template <typename T>
+  static __device__ __forceinline__ int search(const T *before, int n, T x) {
+    int lo = 0, hi = n;
+#pragma unroll 1
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+  }
+  __device__ __forceinline__ void enter(const Params &p, const SeqTab &t, int sequence) {
     seq = sequence;
     w = Weights(p, t.lens[seq], t.qc[seq]);
   }
-  // run number `run` of the batch
-  __device__ void locate(const Params &p, const SeqTab &t, int run) {
-    int lo = 0, hi = p.num_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (t.first[mid] <= run) lo = mid; else hi = mid;
-    }
-    enter(p, t, lo);
-    const int off = run - t.first[seq];
-    head = off / w.runs;
-    i = off - head * w.runs;
-  }
-  __device__ void whole_run(const Params &p, const SeqTab &t) {
-    locate(p, t, round * grid + blockIdx.x);
-    geometry(p, t.lens[seq], t.qc[seq]);
-    x.t0 = 0;
-    x.t1 = x.n;
-  }
-  __device__ void begin_range(const Params &p, const SeqTab &t) {
-    long long start = 0;  // weight of the whole rounds
-    if (rounds > 0) {
-      locate(p, t, rounds * grid);
-      start = t.prefix[seq] + head * w.sum(w.runs) + w.sum(i);
-    }
-    const long long rest = t.prefix[p.num_seqs] - start;
-    const long long most = rest / kMinRange, ctas = most < 1 ? 1 : most < grid ? most : grid;
-    xa = xb = 0;
-    if (static_cast<int>(blockIdx.x) < ctas) {
-      xa = start + rest * blockIdx.x / ctas;
-      xb = start + rest * (blockIdx.x + 1) / ctas;
-    }
-    done = xa >= xb;
-    if (done) return;
-    int lo = 0, hi = p.num_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (t.prefix[mid] <= xa) lo = mid; else hi = mid;
-    }
-    enter(p, t, lo);
-    const long long per_head = w.sum(w.runs), off = xa - t.prefix[seq];
-    head = static_cast<int>(off / per_head);
-    i = w.find(off - head * per_head);
-    s = t.prefix[seq] + head * per_head + w.sum(i);
-    settle(p, t);
-  }
-  __device__ void step(const Params &p, const SeqTab &t) {
+  __device__ __forceinline__ void step(const Params &p, const SeqTab &t) {
     s += w.of(i);
     if (++i < w.runs) return;
     i = 0;
     if (++head < p.num_kv_heads) return;
     head = 0;
+#pragma unroll 1
     do ++seq;
     while (seq < p.num_seqs && t.qc[seq] == 0);
     if (seq < p.num_seqs) enter(p, t, seq);
   }
-  // from the current run on: the first that this CTA has a piece of
-  __device__ void settle(const Params &p, const SeqTab &t) {
-    for (; s < xb && seq < p.num_seqs; step(p, t)) {
-      geometry(p, t.lens[seq], t.qc[seq]);
-      const long long weight = w.of(i);
-      x.t0 = xa <= s ? 0 : border(xa - s, weight);
-      x.t1 = xb >= s + weight ? x.n : border(xb - s, weight);
-      // a run without keys belongs to the CTA that holds its start; a range
-      // inside a tile is an empty piece, which the join expects
-      const bool mine = x.n == 0 ? xa <= s : x.t0 < x.t1 || (x.t0 > 0 && x.t0 < x.n);
-      if (mine) return;
-    }
-    done = true;
-  }
-  __device__ int border(long long at, long long weight) const {
-    const int o = static_cast<int>(at * x.n / weight);
+  // the key tile that a border at this weight of the run falls on: every CTA that asks gets the same
+  __device__ __forceinline__ int border(long long at, long long weight) const {
+    const int o = static_cast<int>(__fdividef(static_cast<float>(at), static_cast<float>(weight)) * static_cast<float>(x.n));
     return o < kMinPiece ? 0 : o > x.n - kMinPiece ? x.n : o;
   }
-  __device__ void geometry(const Params &p, int L, int c) {
+  __device__ __forceinline__ void geometry(const Params &p, int L, int c) {
     x.seq = seq;
     x.head = head;
     x.r0 = i * p.span;
@@ -367,9 +371,18 @@ struct RowSight {
   }
 };
 
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+// mbar_wait (bounded by kWaitLimitNs too) in few instructions: this kernel's roles
+// share the SM's instruction cache, and a wait is in every one of their steps.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_timer_ns();
+  bool ok;
+#pragma unroll 1
+  do ok = mbar_try_wait(bar, parity);
+  while (!ok && global_timer_ns() - t0 < kWaitLimitNs);
+  return ok;
 }
+__device__ __forceinline__ bool wait_warp(uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); }
 
 // Shared-memory matrix descriptors (tc::desc_sw128, groups of 8 rows 1024 bytes
 // apart) in two words: the first holds the address (in 16 bytes), so that a product's
@@ -393,7 +406,7 @@ __device__ __forceinline__ bool any_nan2(uint32_t x) {
 // One warp: the value rows of a staged tile from key k0 on that no row of the run
 // sees become zeros, and so do values that are not finite; true: there were some.
 template <int D>
-__device__ bool clear_values(uint32_t tile, const Run &x, int k0, int lane) {
+__device__ __forceinline__ bool clear_values(uint32_t tile, const Run &x, int k0, int lane) {
   constexpr int kHalves = D / 64, kHalf = kTK * 128, kPerRow = kHalves * 8;  // 16-byte chunks of a row
   auto at = [&](int e) {
     const int row = e / kPerRow, rem = e % kPerRow;
@@ -478,6 +491,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
     const int cap = min(p.max_blocks * BS, p.max_len);
     long long sum = 0;
     int count = 0;
+#pragma unroll 1
     for (int i = lo; i < hi; ++i) {
       int L = p.seq_lens[i];
       if (L < 0 || L > cap) {
@@ -507,6 +521,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
       const int n = __shfl_up_sync(0xffffffffu, before, o);
       if (lane >= o) incl += v, before += n;
     }
+#pragma unroll 1
     for (int i = lo; i < hi; ++i) prefix[i + 1] += incl - sum, first[i + 1] += before - count;
     if (lane == 0) prefix[0] = 0, first[0] = 0;
   }
@@ -543,6 +558,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
   }
   if (p.tile_tok * p.group < kRows) {
     // the loads fill the tile's first tile_tok * G rows only: the rest stay zero
+#pragma unroll 1
     for (int i = threadIdx.x; i < S * kQTile / 16; i += kThreads)
       asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_u32(smem) + i * 16), "r"(0u) : "memory");
     fence_proxy_async_shared();
@@ -564,7 +580,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
   };
   // the CTA's j-th run, once its descriptor is there; ntq 0: there is none (or a wait gave up)
   auto run_at = [&](int j, Run &x) {
-    if (mbar_wait(bar(BI::kRunFull + j % kRunRing), (j / kRunRing) & 1)) x.get(runs + (j % kRunRing) * kRunInts);
+    if (wait(bar(BI::kRunFull + j % kRunRing), (j / kRunRing) & 1)) x.get(runs + (j % kRunRing) * kRunInts);
     else x.ntq = 0;
   };
   auto run_done = [&](int j) { mbar_arrive(bar(BI::kRunFree + j % kRunRing)); };
@@ -583,17 +599,18 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
       const uint64_t pol = p.mask && p.max_nodes <= p.span ? l2_policy_evict_first() : l2_policy_evict_normal();
       int g = 0, nq = 0;  // key tiles and query tiles so far
       int tw_seq = -1, tw_base = 0, tw_val = -1;
-      Sched sc;
+      Sched sc(p, tab);
       int4 desc = make_int4(0, 0, 0, 0);  // this CTA's pieces, for the join
-      if (!is_v) sc.begin(p, tab);
+#pragma unroll 1
       for (int j = 0; !*abort_flag; ++j) {
         Run x;
         if (is_v) {
           run_at(j, x);
           __syncwarp();
         } else {
-          if (sc.done) sc.x.ntq = 0;
+          const bool got = sc.next(p, tab);
           x = sc.x;
+          if (!got) x.ntq = 0;
           if (j >= kRunRing && !wait_warp(bar(BI::kRunFree + j % kRunRing), (j / kRunRing - 1) & 1)) {
             if (lane == 0) timed_out();
             break;
@@ -602,7 +619,6 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
             x.put(runs + (j % kRunRing) * kRunInts);
             mbar_arrive(bar(BI::kRunFull + j % kRunRing));
           }
-          if (!sc.done) sc.next(p, tab);
         }
         if (x.ntq == 0) break;
         if (!is_v && !x.whole()) {
@@ -615,6 +631,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
         }
         if (!is_v && x.t0 < x.t1) {
           bool ok = true;
+#pragma unroll 1
           for (int q = 0; q < x.ntq && ok; ++q, ++nq) {
             const int slot = slot_of(nq), use = use_of(nq);
             if (use > 0 && !wait_warp(bar(BI::kQFree + slot), (use - 1) & 1)) ok = false;
@@ -634,6 +651,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
             break;
           }
         }
+#pragma unroll 1
         for (int t = x.t0; t < x.t1; ++t, ++g) {
           const int s = g % kStages;
           if (g >= kStages && !wait_warp(bar(empty0 + s), ((g / kStages) - 1) & 1)) {
@@ -664,9 +682,11 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
       }
       // never leave a copy in flight into this CTA's shared memory
       if (lane == 0) {
+#pragma unroll 1
         for (int y = g > kStages ? g - kStages : 0; y < g; ++y)
           mbar_wait_sleep(bar(full0 + (y % kStages)), (y / kStages) & 1);
         if (!is_v) {
+#pragma unroll 1
           for (int y = nq > S ? nq - S : 0; y < nq; ++y) mbar_wait_sleep(bar(BI::kQFull + slot_of(y)), use_of(y) & 1);
           if (p.ws_desc) p.ws_desc[blockIdx.x] = desc;
         }
@@ -681,21 +701,24 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
         const uint32_t kIdS = tc::idesc_bf16(kRows, kTK, false, false) | (p.negate ? 1u << 13 : 0u);
         int g = 0, nq = 0, n[2] = {0, 0};  // key tiles, query tiles, each slot's products so far
         bool ok = true;
+#pragma unroll 1
         for (int j = 0; ok; ++j) {
           Run x;
           run_at(j, x);
           if (x.ntq == 0) break;
           run_done(j);
           if (x.t0 >= x.t1) continue;
+#pragma unroll 1
           for (int t = x.t0; t < x.t1 && ok; ++t, ++g) {
             const int s = g % kStages;
-            if (!mbar_wait(bar(BI::kKFull + s), (g / kStages) & 1)) { ok = false; break; }
+            if (!wait(bar(BI::kKFull + s), (g / kStages) & 1)) { ok = false; break; }
             const uint32_t kb = sK + s * kTile;
+#pragma unroll 1
             for (int q = 0; q < x.ntq; ++q) {
               const int slot = slot_of(nq + q);
               int &done = slot ? n[1] : n[0];
-              if (t == x.t0 && !mbar_wait(bar(BI::kQFull + slot), use_of(nq + q) & 1)) { ok = false; break; }
-              if (done > 0 && !mbar_wait(bar(BI::kSFree + slot), (done - 1) & 1)) { ok = false; break; }
+              if (t == x.t0 && !wait(bar(BI::kQFull + slot), use_of(nq + q) & 1)) { ok = false; break; }
+              if (done > 0 && !wait(bar(BI::kSFree + slot), (done - 1) & 1)) { ok = false; break; }
               tc::fence_after();
               const uint32_t qd = desc_word(sQ + slot * kQTile), kd = desc_word(kb);
 #pragma unroll
@@ -720,6 +743,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
       constexpr int kSteps = kTK / 16;  // 16 keys = 8 packed columns of P
       int g = 0, nq = 0, n[2] = {0, 0};  // key tiles, query tiles, each slot's products
       bool ok = true;
+#pragma unroll 1
       for (int j = 0;; ++j) {
         Run x;
         run_at(j, x);
@@ -728,6 +752,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
         if (x.ntq == 0) break;
         if (x.t0 >= x.t1) continue;
         const Common seen(p, x, lens[x.seq], qc[x.seq]);
+#pragma unroll 1
         for (int t = x.t0; t < x.t1; ++t, ++g) {
           const int vs = g % kStages;
           if (!wait_warp(bar(BI::kVFull + vs), (g / kStages) & 1)) { ok = false; break; }
@@ -735,13 +760,14 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
           const int k0 = x.key0(t);
           if (!seen.has(k0) && clear_values<D>(vb, x, k0, lane) && lane == 0) *odd_tile = g + 1;
           if (tc::elect_one()) {
+#pragma unroll 1
             for (int q = 0; q < x.ntq && ok; ++q) {
               const int slot = slot_of(nq + q), use = use_of(nq + q);
               int &done = slot ? n[1] : n[0];
               // the first product overwrites the accumulator: its last run must have been read
-              if (t == x.t0 && use > 0 && !mbar_wait(bar(BI::kOFree + slot), (use - 1) & 1)) { ok = false; break; }
+              if (t == x.t0 && use > 0 && !wait(bar(BI::kOFree + slot), (use - 1) & 1)) { ok = false; break; }
               const int buf = 2 * slot + (done & 1);
-              if (!mbar_wait(bar(BI::kPFull + buf), (done >> 1) & 1)) { ok = false; break; }
+              if (!wait(bar(BI::kPFull + buf), (done >> 1) & 1)) { ok = false; break; }
               tc::fence_after();
               const uint32_t pa = tP + buf * (kTK / 2), vd = desc_word(vb) | (Lay::kHalf >> 4) << 16;
 #pragma unroll
@@ -771,6 +797,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
       const uint32_t tO = tmem + slot * D + lane_off, tSr = tS + slot * kTK + lane_off, tPr = tP + slot * kTK + lane_off;
       int g = 0, nq = 0, n = 0;  // key tiles and query tiles of the CTA, key tiles of this slot
       bool ok = true;
+#pragma unroll 1
       for (int j = 0; ok; ++j) {
         Run x;
         run_at(j, x);
@@ -929,9 +956,11 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
             tc::wait_ld();
             if (!row_valid) continue;
             // add the values that were cleared because they are not finite, where this row sees them
+#pragma unroll 1
             for (int t = x.t0; odd && t < x.t1; ++t) {
               const int k0 = x.key0(t);
               if (seen.has(k0)) continue;
+#pragma unroll 1
               for (int k = 0; k < kTK; ++k) {
                 if (!((sight.of(k0) >> k) & 1)) continue;
                 const int b = p.block_tables[static_cast<size_t>(x.seq) * p.max_blocks + (k0 + k) / BS];
