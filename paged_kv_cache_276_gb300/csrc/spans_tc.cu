@@ -834,16 +834,21 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
           sight.sinks = min(p.sinks, sight.hi);
         }
         const Common seen(p, x, lens[x.seq], c);
+        const bool idle = __all_sync(0xffffffffu, !row_valid);  // spare rows only
         float m = -INFINITY, l = 0.f;
         const int g0 = g;
         g += x.t1 - x.t0;
 #pragma unroll 1
-        for (int t = x.t0; t < x.t1; ++t, ++n) {
-          const int k0 = x.key0(t), buf = n & 1;
-          // spare rows see nothing
+        for (int t = x.t0, k0 = x.key0(t); t < x.t1; ++n) {
+          const int buf = n & 1;
           const bool full = seen.has(k0);
-          const uint64_t see = full ? (row_valid ? ~0ull : 0ull) : sight.of(k0);
-          const bool none = __all_sync(0xffffffffu, see == 0);  // no row of the warp sees any of them
+          uint64_t see = ~0ull;
+          bool none = idle;  // no row of the warp sees any of the tile
+          if (!full) {
+            see = sight.of(k0);
+            none = __all_sync(0xffffffffu, see == 0);
+          }
+          k0 = ++t == x.ns ? x.t_lo * kTK : k0 + kTK;
           if (!wait_warp(bar(BI::kSFull + slot), n & 1)) { ok = false; break; }
           tc::fence_after();
           uint32_t pk[32];
