@@ -67,7 +67,12 @@ namespace {
 
 constexpr int kRows = 128;       // query rows per tile
 constexpr int kTK = 64;          // keys per tile
-constexpr float kSlack = 8.f;    // lazy rescale threshold (log2 units)
+// The reference of the weights moves when a score passes it by more than this (log2
+// units): weights stay below 2^20, which fp32 sums and bf16 hold with the same
+// relative rounding (sums overflow for values above 2^107 / keys).  With 8, a warp
+// of 32 rows rescaled its accumulator at every third tile of a window that starts
+// with the sinks' four keys (571 us for the four prompts of 8192 tokens).
+constexpr float kSlack = 20.f;
 constexpr int kRunCost = 256;    // a run's start and end, in keys
 constexpr int kMinRange = 512;   // least weight of a CTA's range, in keys
 constexpr int kRoundsFrom = 4;   // runs per CTA from which most go round the CTAs whole
