@@ -383,7 +383,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = global_timer_ns();
   bool ok;
 #pragma unroll 1
-  do ok = mbar_try_wait(bar, parity);
+  do ok = mbar_try_wait_sleep(bar, parity);
   while (!ok && global_timer_ns() - t0 < kWaitLimitNs);
   return ok;
 }
@@ -700,12 +700,28 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
       // ------------------------------------------------- S = Q K^T issuer
       // A product goes out once the slot's softmax has read the one before it (its
       // weights have their own columns), so the next product of a slot runs while
-      // the weights of this one are computed.
+      // the weights of this one are computed.  One thread issues, and the softmax warps
+      // keep its code out of the nearest instruction cache: few instructions per tile.
+      // (A wait for the phase before a barrier's first, parity 1, returns at once.)
       if (tc::elect_one()) {
         // a negative scale is taken as the negated queries' product (bit 13: negate A)
         const uint32_t kIdS = tc::idesc_bf16(kRows, kTK, false, false) | (p.negate ? 1u << 13 : 0u);
-        int g = 0, nq = 0, n[2] = {0, 0};  // key tiles, query tiles, each slot's products so far
+        const uint32_t kd0 = desc_word(sK);
+        uint32_t k_phase = 0, free_phase = 3;  // of the stage; bit per slot: of its scores
+        int s = 0, nq = 0;  // stage; query tiles so far
         bool ok = true;
+        auto product = [&](int slot) {
+          if (!wait(bar(BI::kSFree + slot), (free_phase >> slot) & 1)) return false;
+          free_phase ^= 1u << slot;
+          tc::fence_after();
+          const uint32_t qd = desc_word(sQ + slot * kQTile), kd = kd0 + s * (kTile >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            tc::mma(tS + slot * kTK, desc_of(qd + (((ks >> 2) * Lay::kQHalf + (ks & 3) * 32) >> 4), kSpanHi),
+                    desc_of(kd + (((ks >> 2) * Lay::kHalf + (ks & 3) * 32) >> 4), kSpanHi), kIdS, ks > 0);
+          tc::commit(bar(BI::kSFull + slot));
+          return true;
+        };
 #pragma unroll 1
         for (int j = 0; ok; ++j) {
           Run x;
@@ -713,29 +729,17 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
           if (x.ntq == 0) break;
           run_done(j);
           if (x.t0 >= x.t1) continue;
+          const int a = slot_of(nq), b = slot_of(nq + 1);
+          const bool two = S == 2 && x.ntq == 2;
+          ok = wait(bar(BI::kQFull + a), use_of(nq) & 1) && (!two || wait(bar(BI::kQFull + b), use_of(nq + 1) & 1));
 #pragma unroll 1
-          for (int t = x.t0; t < x.t1 && ok; ++t, ++g) {
-            const int s = g % kStages;
-            if (!wait(bar(BI::kKFull + s), (g / kStages) & 1)) { ok = false; break; }
-            const uint32_t kb = sK + s * kTile;
-#pragma unroll 1
-            for (int q = 0; q < x.ntq; ++q) {
-              const int slot = slot_of(nq + q);
-              int &done = slot ? n[1] : n[0];
-              if (t == x.t0 && !wait(bar(BI::kQFull + slot), use_of(nq + q) & 1)) { ok = false; break; }
-              if (done > 0 && !wait(bar(BI::kSFree + slot), (done - 1) & 1)) { ok = false; break; }
-              tc::fence_after();
-              const uint32_t qd = desc_word(sQ + slot * kQTile), kd = desc_word(kb);
-#pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks)
-                tc::mma(tS + slot * kTK, desc_of(qd + (((ks >> 2) * Lay::kQHalf + (ks & 3) * 32) >> 4), kSpanHi),
-                        desc_of(kd + (((ks >> 2) * Lay::kHalf + (ks & 3) * 32) >> 4), kSpanHi), kIdS, ks > 0);
-              tc::commit(bar(BI::kSFull + slot));
-              if (t == x.t1 - 1) tc::commit(bar(BI::kQFree + slot));
-              ++done;
-            }
-            if (ok) tc::commit(bar(BI::kKEmpty + s));  // the keys are read by these products only
+          for (int left = x.t1 - x.t0; left > 0 && ok; --left) {
+            ok = wait(bar(BI::kKFull) + 8 * s, k_phase) && product(a) && (!two || product(b));
+            tc::commit(bar(BI::kKEmpty) + 8 * s);  // the keys are read by these products only
+            if (++s == kStages) s = 0, k_phase ^= 1;
           }
+          tc::commit(bar(BI::kQFree + a));
+          if (two) tc::commit(bar(BI::kQFree + b));
           nq += x.ntq;
         }
         if (!ok) timed_out();
@@ -746,8 +750,25 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
       // one lane issues.
       constexpr uint32_t kIdO = tc::idesc_bf16(kRows, D, false, true);
       constexpr int kSteps = kTK / 16;  // 16 keys = 8 packed columns of P
-      int g = 0, nq = 0, n[2] = {0, 0};  // key tiles, query tiles, each slot's products
+      const uint32_t vd0 = desc_word(sV) | (Lay::kHalf >> 4) << 16;
+      uint32_t v_phase = 0, p_phase = 0, free_phase = 3, buf = 0;  // bits: [slot][buffer]; [slot]; [slot]
+      int s = 0, g = 0, nq = 0;  // stage, key tiles, query tiles
       bool ok = true;
+      const bool leader = tc::elect_one();
+      auto product = [&](int slot, bool first, bool last) {
+        const uint32_t b = 2 * slot + ((buf >> slot) & 1);
+        if (!wait(bar(BI::kPFull) + 8 * b, (p_phase >> b) & 1)) return false;
+        p_phase ^= 1u << b;
+        buf ^= 1u << slot;
+        tc::fence_after();
+        const uint32_t pa = tP + b * (kTK / 2), vd = vd0 + s * (kTile >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks)
+          tc::mma_ta(tmem + slot * D, pa + ks * 8, desc_of(vd + (ks * 2048 >> 4), kSpanHi), kIdO, !(first && ks == 0));
+        tc::commit(bar(BI::kPvDone) + 8 * b);
+        if (last) tc::commit(bar(BI::kOFull + slot));
+        return true;
+      };
 #pragma unroll 1
       for (int j = 0;; ++j) {
         Run x;
@@ -757,37 +778,25 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
         if (x.ntq == 0) break;
         if (x.t0 >= x.t1) continue;
         const Common seen(p, x, lens[x.seq], qc[x.seq]);
+        const int a = slot_of(nq), b = slot_of(nq + 1);
+        const bool two = S == 2 && x.ntq == 2;
+        // the first product overwrites the accumulator: its last run must have been read
+        ok = wait(bar(BI::kOFree + a), (free_phase >> a) & 1) && (!two || wait(bar(BI::kOFree + b), (free_phase >> b) & 1));
+        free_phase ^= (1u << a) | (two ? 1u << b : 0u);
 #pragma unroll 1
-        for (int t = x.t0; t < x.t1; ++t, ++g) {
-          const int vs = g % kStages;
-          if (!wait_warp(bar(BI::kVFull + vs), (g / kStages) & 1)) { ok = false; break; }
-          const uint32_t vb = sV + vs * kTile;
-          const int k0 = x.key0(t);
-          if (!seen.has(k0) && clear_values<D>(vb, x, k0, lane) && lane == 0) *odd_tile = g + 1;
-          if (tc::elect_one()) {
-#pragma unroll 1
-            for (int q = 0; q < x.ntq && ok; ++q) {
-              const int slot = slot_of(nq + q), use = use_of(nq + q);
-              int &done = slot ? n[1] : n[0];
-              // the first product overwrites the accumulator: its last run must have been read
-              if (t == x.t0 && use > 0 && !wait(bar(BI::kOFree + slot), (use - 1) & 1)) { ok = false; break; }
-              const int buf = 2 * slot + (done & 1);
-              if (!wait(bar(BI::kPFull + buf), (done >> 1) & 1)) { ok = false; break; }
-              tc::fence_after();
-              const uint32_t pa = tP + buf * (kTK / 2), vd = desc_word(vb) | (Lay::kHalf >> 4) << 16;
-#pragma unroll
-              for (int ks = 0; ks < kSteps; ++ks)
-                tc::mma_ta(tmem + slot * D, pa + ks * 8, desc_of(vd + (ks * 2048 >> 4), kSpanHi), kIdO,
-                           !(t == x.t0 && ks == 0));
-              tc::commit(bar(BI::kPvDone + buf));
-              if (t == x.t1 - 1) tc::commit(bar(BI::kOFull + slot));
-              ++done;
-            }
-            if (ok) tc::commit(bar(BI::kVEmpty + vs));
-          }
+        for (int t = x.t0, k0 = x.key0(t); t < x.t1; ++g) {
+          ok = ok && wait(bar(BI::kVFull) + 8 * s, v_phase);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }  // the other lanes wait for the issues here
+          if (!seen.has(k0) && clear_values<D>(sV + s * kTile, x, k0, lane) && lane == 0) *odd_tile = g + 1;
+          const bool first = t == x.t0;
+          k0 = ++t == x.ns ? x.t_lo * kTK : k0 + kTK;
+          if (leader) {
+            ok = product(a, first, t == x.t1) && (!two || product(b, first, t == x.t1));
+            tc::commit(bar(BI::kVEmpty) + 8 * s);
+          }
+          if (++s == kStages) s = 0, v_phase ^= 1;
         }
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         nq += x.ntq;
       }
       if (!ok && lane == 0) timed_out();
