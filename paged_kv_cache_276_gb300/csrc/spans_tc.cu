@@ -707,12 +707,18 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
         // a negative scale is taken as the negated queries' product (bit 13: negate A)
         const uint32_t kIdS = tc::idesc_bf16(kRows, kTK, false, false) | (p.negate ? 1u << 13 : 0u);
         const uint32_t kd0 = desc_word(sK);
-        uint32_t k_phase = 0, free_phase = 3;  // of the stage; bit per slot: of its scores
+        uint32_t k_phase = 0, free_phase = 3, pv_phase = 15, buf = 0;  // of the stage; bits: [slot]; [slot][buffer]; [slot]
         int s = 0, nq = 0;  // stage; query tiles so far
         bool ok = true;
         auto product = [&](int slot) {
           if (!wait(bar(BI::kSFree + slot), (free_phase >> slot) & 1)) return false;
           free_phase ^= 1u << slot;
+          // the weights that the softmax makes of this product go where those of the slot's
+          // tile before the last were: their product must be complete
+          const uint32_t b = 2 * slot + ((buf >> slot) & 1);
+          if (!wait(bar(BI::kPvDone) + 8 * b, (pv_phase >> b) & 1)) return false;
+          pv_phase ^= 1u << b;
+          buf ^= 1u << slot;
           tc::fence_after();
           const uint32_t qd = desc_word(sQ + slot * kQTile), kd = kd0 + s * (kTile >> 4);
 #pragma unroll
@@ -901,9 +907,8 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
             const uint64_t nm2 = f32x2_bits(__float_as_uint(-msub), __float_as_uint(-msub));
             l += weights64(sv, ks2, nm2, pk);
           }
-          // the last product from this buffer must be complete before it is written, and
-          // every product before the accumulator is
-          if (n > 1 && !wait_warp(bar(BI::kPvDone + 2 * slot + buf), ((n >> 1) - 1) & 1)) { ok = false; break; }
+          // the last product from this buffer is complete (the score product waited for it);
+          // all must be before the accumulator is written
           if (__any_sync(0xffffffffu, scale_o)) {  // warp-uniform: tcgen05.ld/st are warp-wide
             if (!wait_warp(bar(BI::kPvDone + 2 * slot + (buf ^ 1)), ((n - 1) >> 1) & 1)) { ok = false; break; }
             tc::fence_after();
