@@ -497,25 +497,46 @@ __global__ void __launch_bounds__(D / 16 * 32) step_join_kernel(const StepParams
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int col = nt * 8 + 2 * c4;
-    float M[2] = {-INFINITY, -INFINITY};
-    for (int i = 0; i < pieces; ++i) {
-      const float4 ml = *reinterpret_cast<const float4 *>(p.ws_ml + slot(i) * NT * 8 + col);
-      M[0] = fmaxf(M[0], ml.x);
-      M[1] = fmaxf(M[1], ml.z);
-    }
-    float den[2] = {0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int i = 0; i < pieces; ++i) {
-      const float4 ml = *reinterpret_cast<const float4 *>(p.ws_ml + slot(i) * NT * 8 + col);
-      const float4 x = p.ws_o[((slot(i) * (D / 16) + md) * NT + nt) * 32 + lane];
-      // a piece without keys (max -inf) holds zeros and weighs nothing
-      const float f0 = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M[0]), f1 = ml.z == -INFINITY ? 0.f : exp2f(ml.z - M[1]);
-      den[0] += ml.y * f0;
-      den[1] += ml.w * f1;
-      o[0] += f0 * x.x;
-      o[1] += f1 * x.y;
-      o[2] += f0 * x.z;
-      o[3] += f1 * x.w;
+    constexpr int kAhead = 8;  // pieces whose loads are in flight together
+    float M[2] = {-INFINITY, -INFINITY}, den[2] = {0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int b = 0; b < pieces; b += kAhead) {
+      float4 ml[kAhead], x[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        ml[i] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (b + i < pieces) {
+          ml[i] = *reinterpret_cast<const float4 *>(p.ws_ml + slot(b + i) * NT * 8 + col);
+          x[i] = p.ws_o[((slot(b + i) * (D / 16) + md) * NT + nt) * 32 + lane];
+        }
+      }
+      float top[2] = {M[0], M[1]};
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        top[0] = fmaxf(top[0], ml[i].x);
+        top[1] = fmaxf(top[1], ml[i].z);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float keep = M[e] == -INFINITY ? 0.f : exp2f(M[e] - top[e]);
+        M[e] = top[e];
+        den[e] *= keep;
+        o[e] *= keep;
+        o[e + 2] *= keep;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        // a piece without keys (max -inf) holds zeros and weighs nothing
+        const float f0 = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - M[0]);
+        const float f1 = ml[i].z == -INFINITY ? 0.f : exp2f(ml[i].z - M[1]);
+        den[0] += ml[i].y * f0;
+        den[1] += ml[i].w * f1;
+        o[0] += f0 * x[i].x;
+        o[1] += f1 * x[i].y;
+        o[2] += f0 * x[i].z;
+        o[3] += f1 * x[i].w;
+      }
     }
     const float i0 = den[0] > 0.f ? 1.f / den[0] : 0.f, i1 = den[1] > 0.f ? 1.f / den[1] : 0.f;
 #pragma unroll

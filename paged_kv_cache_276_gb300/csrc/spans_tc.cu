@@ -77,7 +77,7 @@ constexpr int kRunCost = 256;    // a run's start and end, in keys
 constexpr int kMinRange = 512;   // least weight of a CTA's range, in keys
 constexpr int kRoundsFrom = 4;   // runs per CTA from which most go round the CTAs whole
 constexpr int kMinPiece = 4;     // key tiles that a border leaves on either side
-constexpr int kJoinThreads = 256;
+constexpr int kJoinShares = 8;   // blocks of the join that share a run's head dim
 constexpr int kPairedSeqs = 512;  // sequences up to which two CTAs of one slot fit an SM
 constexpr int kRunRing = 4;      // descriptors of runs ahead
 
@@ -129,7 +129,7 @@ struct Params {
   __nv_bfloat16 *out;
   float4 *ws_o;                // [2 grid][D / 4][piece_rows]
   float2 *ws_ml;               // [2 grid][piece_rows]
-  int4 *ws_desc;               // [grid]: {sequence | KV head << 16, first token, flags, -} of each CTA's pieces
+  int4 *ws_desc;               // [grid]: {first query row, KV head, flags, tokens} of each CTA's pieces; NULL: no run is cut
   int32_t *status;
   int num_seqs, max_blocks, num_q_heads, num_kv_heads, num_blocks, total_q, max_len, oob_row;
   int group, tile_tok, span;   // tokens of a query tile (floor(128 / G) or the tree's) and of a run
@@ -252,7 +252,8 @@ struct Sched {
 
   __device__ __forceinline__ Sched(const Params &p, const SeqTab &t) {
     const int runs = t.first[p.num_seqs], grid = gridDim.x;
-    rounds = !p.mask && runs >= kRoundsFrom * grid ? runs / grid - 1 : 0;
+    // where no run is cut, they all go round whole
+    rounds = !p.ws_desc ? (runs + grid - 1) / grid : !p.mask && runs >= kRoundsFrom * grid ? runs / grid - 1 : 0;
     round = -1;
   }
 
@@ -260,6 +261,7 @@ struct Sched {
   __device__ __forceinline__ bool next(const Params &p, const SeqTab &t) {
     const int grid = gridDim.x;
     ++round;
+    if (!p.ws_desc && round * static_cast<long long>(grid) + blockIdx.x >= t.first[p.num_seqs]) return false;
     if (round <= rounds) {
       // a whole round's run, or the first run behind the rounds
       const int run = round * grid + (round < rounds ? blockIdx.x : 0);
@@ -488,8 +490,52 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
   auto bar = [&](int i) { return smem_u32(bars + i); };
 
   grid_launch_dependents();
+  // what the kernel before does not touch
+  if (threadIdx.x == 32 * kKWarp) {
+    for (int i = 0; i < S; ++i) {  // one per slot
+      mbar_init(bar(BI::kQFull + i), 1);
+      mbar_init(bar(BI::kQFree + i), 1);
+      mbar_init(bar(BI::kOFull + i), 1);
+      mbar_init(bar(BI::kOFree + i), kRows);
+      mbar_init(bar(BI::kSFull + i), 1);
+      mbar_init(bar(BI::kSFree + i), kRows);
+      for (int h = 2 * i; h < 2 * i + 2; ++h) {  // one per slot and buffer of P
+        mbar_init(bar(BI::kPFull + h), kRows);
+        mbar_init(bar(BI::kPvDone + h), 1);
+      }
+    }
+    for (int i = 0; i < kRunRing; ++i) {
+      mbar_init(bar(BI::kRunFull + i), 1);
+      mbar_init(bar(BI::kRunFree + i), 4 * S + 3);  // the softmax warps, two issuers, the value producer
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(BI::kKFull + s), 1);
+      mbar_init(bar(BI::kKEmpty + s), 1);
+      mbar_init(bar(BI::kVFull + s), 1);
+      mbar_init(bar(BI::kVEmpty + s), 1);
+    }
+    *abort_flag = 0;
+    *odd_tile = 0;
+    mbar_init_fence();
+  }
+  if (p.tile_tok * p.group < kRows) {
+    // the loads fill the tile's first tile_tok * G rows only: the rest stay zero
+#pragma unroll 1
+    for (int i = threadIdx.x; i < S * kQTile / 16; i += kThreads)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_u32(smem) + i * 16), "r"(0u) : "memory");
+    fence_proxy_async_shared();
+  }
+  if (threadIdx.x == 32 * kKWarp + 1) {
+    tma_prefetch_desc(&tmq);
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
+  }
   grid_dependency_wait();
-
+  // (tensor memory after the wait: a CTA of that kernel may not have taken its own yet)
+  if (warp == kMmaWarp) {
+    tc::alloc(smem_u32(tmem_slot), kTmemCols);
+    tc::relinquish();
+  }
   if (warp == 0) {  // weight and runs per sequence -> exclusive prefixes
     const int per = (B + 31) / 32;
     const int lo = min(B, lane * per), hi = min(B, lo + per);
@@ -529,49 +575,6 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
 #pragma unroll 1
     for (int i = lo; i < hi; ++i) prefix[i + 1] += incl - sum, first[i + 1] += before - count;
     if (lane == 0) prefix[0] = 0, first[0] = 0;
-  }
-  if (threadIdx.x == 32 * kKWarp) {
-    for (int i = 0; i < S; ++i) {  // one per slot
-      mbar_init(bar(BI::kQFull + i), 1);
-      mbar_init(bar(BI::kQFree + i), 1);
-      mbar_init(bar(BI::kOFull + i), 1);
-      mbar_init(bar(BI::kOFree + i), kRows);
-      mbar_init(bar(BI::kSFull + i), 1);
-      mbar_init(bar(BI::kSFree + i), kRows);
-      for (int h = 2 * i; h < 2 * i + 2; ++h) {  // one per slot and buffer of P
-        mbar_init(bar(BI::kPFull + h), kRows);
-        mbar_init(bar(BI::kPvDone + h), 1);
-      }
-    }
-    for (int i = 0; i < kRunRing; ++i) {
-      mbar_init(bar(BI::kRunFull + i), 1);
-      mbar_init(bar(BI::kRunFree + i), 4 * S + 3);  // the softmax warps, two issuers, the value producer
-    }
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(BI::kKFull + s), 1);
-      mbar_init(bar(BI::kKEmpty + s), 1);
-      mbar_init(bar(BI::kVFull + s), 1);
-      mbar_init(bar(BI::kVEmpty + s), 1);
-    }
-    *abort_flag = 0;
-    *odd_tile = 0;
-    mbar_init_fence();
-  }
-  if (warp == kMmaWarp) {
-    tc::alloc(smem_u32(tmem_slot), kTmemCols);
-    tc::relinquish();
-  }
-  if (p.tile_tok * p.group < kRows) {
-    // the loads fill the tile's first tile_tok * G rows only: the rest stay zero
-#pragma unroll 1
-    for (int i = threadIdx.x; i < S * kQTile / 16; i += kThreads)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_u32(smem) + i * 16), "r"(0u) : "memory");
-    fence_proxy_async_shared();
-  }
-  if (threadIdx.x == 32 * kKWarp + 1) {
-    tma_prefetch_desc(&tmq);
-    tma_prefetch_desc(&tmk);
-    tma_prefetch_desc(&tmv);
   }
   tc::fence_before();
   __syncthreads();
@@ -629,8 +632,9 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
         if (!is_v && !x.whole()) {
           if (x.t0 > 0 && x.t1 == x.n) desc.z |= kEnds;
           if (x.t0 == 0) {
-            desc.x = x.seq | (x.head << 16);
-            desc.y = x.r0;
+            desc.x = qs[x.seq] + x.r0;
+            desc.y = x.head;
+            desc.w = min(p.span, qc[x.seq] - x.r0);
             desc.z |= kLeaves;
           }
         }
@@ -1025,62 +1029,73 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
 // exact merge of the run's pieces, a thread per query row.
 //   out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M),  M = max_p m_p
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) spans_join_kernel(const Params p, int grid) {
+__global__ void __launch_bounds__(2 * kRows) spans_join_kernel(const Params p, int grid) {
   grid_launch_dependents();
   grid_dependency_wait();  // the pieces come from the grid launched just before
   const int4 d = p.ws_desc[blockIdx.x];
   if (!(d.z & kLeaves)) return;
-  __shared__ int last_cta;
-  if (threadIdx.x < 32) {  // the first CTA after this one in which the run ends
-    int found = -1;
-    for (int base = blockIdx.x + 1; base < grid && found < 0; base += 32) {
-      const int c = base + threadIdx.x;
-      const unsigned ends = __ballot_sync(0xffffffffu, c < grid && (p.ws_desc[c].z & kEnds));
-      if (ends) found = base + __ffs(ends) - 1;
-    }
-    if (threadIdx.x == 0) last_cta = found;
+  int last = -1;  // the first CTA after this one in which the run ends
+  for (int base = blockIdx.x + 1; base < grid && last < 0; base += 32) {
+    const int c = base + (threadIdx.x & 31);
+    const unsigned ends = __ballot_sync(0xffffffffu, c < grid && (p.ws_desc[c].z & kEnds));
+    if (ends) last = base + __ffs(ends) - 1;
   }
-  __syncthreads();
-  if (last_cta < 0) return;  // only where a bounded wait gave up
-  const int seq = d.x & 0xffff, head = d.x >> 16;
-  const int a = p.q_start[seq], c = p.q_start[seq + 1] - a;
-  const int pieces = last_cta - static_cast<int>(blockIdx.x) + 1;
-  for (int prow = threadIdx.x; prow < p.piece_rows; prow += blockDim.x) {
-    const int q = prow / kRows, r = prow % kRows, tok = r / p.group, gh = r - tok * p.group;
-    const int token = d.y + q * p.tile_tok + tok;
-    if (tok >= p.tile_tok || token >= c || token >= d.y + p.span) continue;
-    // piece 1 of the first CTA, piece 0 of the others
-    auto slot = [&](int i) { return 2 * (static_cast<size_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
-    float M = -INFINITY;
-    for (int i = 0; i < pieces; ++i) M = fmaxf(M, p.ws_ml[slot(i) * p.piece_rows + prow].x);
-    constexpr int kCols = D / 4 / 8;  // float4 columns of this block (8 blocks share the head dim)
-    float4 acc[kCols];
+  if (last < 0) return;  // only where a bounded wait gave up
+  const int pieces = last - static_cast<int>(blockIdx.x) + 1;
+  const int prow = threadIdx.x, q = prow / kRows, r = prow % kRows, tok = r / p.group, gh = r - tok * p.group;
+  const int token = q * p.tile_tok + tok;
+  if (tok >= p.tile_tok || token >= d.w) return;
+  constexpr int kCols = D / 4 / kJoinShares;  // float4 columns of this block
+  constexpr int kAhead = 4;                   // pieces whose loads are in flight together
+  float4 acc[kCols];
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-      const float2 ml = p.ws_ml[slot(i) * p.piece_rows + prow];
-      // an empty piece (max -inf) weighs nothing, and its O was not written
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      den += ml.y * f;
+  for (int k = 0; k < kCols; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, den = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < pieces; i0 += kAhead) {
+    float2 ml[kAhead];
+    float4 o[kAhead][kCols];
 #pragma unroll
-      for (int k = 0; k < kCols; ++k) {
-        const float4 o = f != 0.f ? p.ws_o[(slot(i) * (D / 4) + blockIdx.y * kCols + k) * p.piece_rows + prow]
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-        acc[k].x += f * o.x;
-        acc[k].y += f * o.y;
-        acc[k].z += f * o.z;
-        acc[k].w += f * o.w;
+    for (int i = 0; i < kAhead; ++i) {
+      // piece 1 of the first CTA, piece 0 of the others
+      const int c = i0 + i;
+      const size_t at = 2 * (static_cast<size_t>(blockIdx.x) + c) + (c == 0 ? 1 : 0);
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (c < pieces) {
+        ml[i] = p.ws_ml[at * p.piece_rows + prow];
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) o[i][k] = p.ws_o[(at * (D / 4) + blockIdx.y * kCols + k) * p.piece_rows + prow];
       }
     }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
-    uint2 *dst = reinterpret_cast<uint2 *>(p.out + ((static_cast<size_t>(a) + token) * p.num_q_heads + head * p.group + gh) * D) +
-                 blockIdx.y * kCols;
+    float top = M;
 #pragma unroll
-    for (int k = 0; k < kCols; ++k)
-      dst[k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    for (int i = 0; i < kAhead; ++i) top = fmaxf(top, ml[i].x);
+    const float keep = M == -INFINITY ? 0.f : exp2f(M - top);
+    M = top;
+    den *= keep;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k].x *= keep, acc[k].y *= keep, acc[k].z *= keep, acc[k].w *= keep;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      // an empty piece (max -inf) weighs nothing, and its O was not written
+      const float f = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - M);
+      if (f == 0.f) continue;
+      den += ml[i].y * f;
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) {
+        acc[k].x += f * o[i][k].x;
+        acc[k].y += f * o[i][k].y;
+        acc[k].z += f * o[i][k].z;
+        acc[k].w += f * o[i][k].w;
+      }
+    }
   }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  uint2 *dst = reinterpret_cast<uint2 *>(p.out + ((static_cast<size_t>(d.x) + token) * p.num_q_heads + d.y * p.group + gh) * D) +
+               blockIdx.y * kCols;
+#pragma unroll
+  for (int k = 0; k < kCols; ++k)
+    dst[k] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
 }
 
 // ------------------------------------------------------------------ host
@@ -1142,7 +1157,7 @@ int launch(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tm
   const unsigned grid = static_cast<unsigned>(plan.grid);
   if (e == cudaSuccess) e = launch_overlapped(kernel, grid, Layout<D, S>::kThreads, smem, stream, tmq, tmk, tmv, p);
   if (e == cudaSuccess && plan.split)
-    e = launch_overlapped(spans_join_kernel<D>, dim3(grid, 8), kJoinThreads, 0, stream, p, plan.grid);
+    e = launch_overlapped(spans_join_kernel<D>, dim3(grid, kJoinShares), plan.piece_rows, 0, stream, p, plan.grid);
   return e == cudaSuccess ? PKV_OK : (set_cuda_error(e), PKV_ERR_CUDA);
 }
 
