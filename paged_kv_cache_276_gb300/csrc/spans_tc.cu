@@ -131,7 +131,7 @@ struct Params {
   float2 *ws_ml;               // [2 grid][piece_rows]
   int4 *ws_desc;               // [grid]: {first query row, KV head, flags, tokens} of each CTA's pieces; NULL: no run is cut
   int32_t *status;
-  int num_seqs, max_blocks, num_q_heads, num_kv_heads, num_blocks, total_q, max_len, oob_row;
+  int bs_log2, num_seqs, max_blocks, num_q_heads, num_kv_heads, num_blocks, total_q, max_len, oob_row;
   int group, tile_tok, span;   // tokens of a query tile (floor(128 / G) or the tree's) and of a run
   int window, sinks, max_nodes, piece_rows;
   float scale_log2;            // of the scale's magnitude; negate: it is negative
@@ -225,10 +225,11 @@ struct Run {
 
 // The keys that every one of some rows sees, tokens first .. last of a sequence's
 // chunk (of a tree: any tokens): [lo, hi) and [0, sinks).
+template <bool Tree>
 struct Common {
   int lo, hi, sinks;
   __device__ __forceinline__ Common(const Params &p, int ctx, int first, int last) {
-    if (p.mask) {
+    if (Tree) {
       lo = sinks = 0;
       hi = ctx;
     } else {
@@ -366,14 +367,14 @@ struct Sched {
 __device__ __forceinline__ uint64_t below(int x) { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1; }
 
 // What a row sees of 64 keys from h0 on.
+template <bool Tree>
 struct RowSight {
   int lo, hi, sinks;   // window: [lo, hi) and [0, sinks)
   int ctx;             // tree: [0, ctx) and bit j of word for key ctx + j
   uint64_t word;       // (bits of the tree only: keep)
   uint64_t keep;
-  bool tree;
   __device__ __forceinline__ uint64_t of(int h0) const {
-    if (!tree) return (below(hi - h0) & ~below(lo - h0)) | below(sinks - h0);
+    if (!Tree) return (below(hi - h0) & ~below(lo - h0)) | below(sinks - h0);
     const int sh = ctx - h0;
     const uint64_t w = word & keep, own = sh >= 64 || sh <= -64 ? 0ull : sh >= 0 ? w << sh : w >> -sh;
     return below(sh) | own;
@@ -467,7 +468,7 @@ __device__ __forceinline__ bool clear_values(uint32_t tile, const Run &x, int k0
   return odd;
 }
 
-template <int BS, int D, int S>
+template <bool Tree, int D, int S>
 __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPerSm)
     spans_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv, const Params p) {
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
   auto slot_of = [](int n) { return S == 2 ? n & 1 : 0; };
   auto use_of = [](int n) { return S == 2 ? n >> 1 : n; };
   // one TMA box per block of the tile (a block longer than the tile: the tile's piece of it)
-  constexpr int kBoxRows = BS < kTK ? BS : kTK, kBoxes = kTK / kBoxRows;
+  const int box_rows = min(1 << p.bs_log2, kTK), boxes = kTK / box_rows;  // a key tile comes in boxes of one page each
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kSmemBars);
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
   if (warp == 0) {  // weight and runs per sequence -> exclusive prefixes
     const int per = (B + 31) / 32;
     const int lo = min(B, lane * per), hi = min(B, lo + per);
-    const int cap = min(p.max_blocks * BS, p.max_len);
+    const int cap = min(p.max_blocks << p.bs_log2, p.max_len);
     long long sum = 0;
     int count = 0;
 #pragma unroll 1
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
       }
       const int a = p.q_start[i], b = p.q_start[i + 1];
       int c = b - a;
-      if (a < 0 || b < a || b > p.total_q || (p.mask && c > p.max_nodes)) {
+      if (a < 0 || b < a || b > p.total_q || (Tree && c > p.max_nodes)) {
         if (blockIdx.x == 0 && p.status) atomicOr(p.status, PKV_STATUS_BAD_QSTART);
         c = 0;
       }
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
       const uint32_t ring = is_v ? sV : sK;
       const int full0 = is_v ? BI::kVFull : BI::kKFull, empty0 = is_v ? BI::kVEmpty : BI::kKEmpty;
       // a tree of one run per KV head reads every key once; other runs share theirs
-      const uint64_t pol = p.mask && p.max_nodes <= p.span ? l2_policy_evict_first() : l2_policy_evict_normal();
+      const uint64_t pol = Tree && p.max_nodes <= p.span ? l2_policy_evict_first() : l2_policy_evict_normal();
       int g = 0, nq = 0;  // key tiles and query tiles so far
       int tw_seq = -1, tw_base = 0, tw_val = -1;
       Sched sc(p, tab);
@@ -675,8 +676,8 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
             if (lane == 0) timed_out();
             break;
           }
-          const int k0 = x.key0(t), blk = k0 / BS;
-          if (x.seq != tw_seq || blk < tw_base || blk + kBoxes > tw_base + 32) {
+          const int k0 = x.key0(t), blk = k0 >> p.bs_log2;
+          if (x.seq != tw_seq || blk < tw_base || blk + boxes > tw_base + 32) {
             tw_seq = x.seq;
             tw_base = blk;
             const int e = blk + lane;
@@ -685,14 +686,14 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
           if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), kTile);
           // one lane per (box, half): the box copies go out in parallel
           const int jb = lane / kHalves, hf = lane % kHalves;
-          const int b = __shfl_sync(0xffffffffu, tw_val, (blk + min(jb, kBoxes - 1) - tw_base) & 31);
-          if (jb < kBoxes) {
-            const int kb = k0 + jb * kBoxRows;  // the box's first key
-            const bool seen = kb < x.hi && (kb + kBoxRows > x.lo || kb < x.sink_end);
+          const int b = __shfl_sync(0xffffffffu, tw_val, (blk + min(jb, boxes - 1) - tw_base) & 31);
+          if (jb < boxes) {
+            const int kb = k0 + jb * box_rows;  // the box's first key
+            const bool seen = kb < x.hi && (kb + box_rows > x.lo || kb < x.sink_end);
             int row = p.oob_row;  // no row of the run sees any of it, or a bad id: zeros
-            if (seen && b >= 0 && b < p.num_blocks) row = (b * hkv + x.head) * BS + kb % BS;
+            if (seen && b >= 0 && b < p.num_blocks) row = ((b * hkv + x.head) << p.bs_log2) + (kb & ((1 << p.bs_log2) - 1));
             else if (seen && p.status && !is_v && hf == 0) atomicOr(p.status, PKV_STATUS_BAD_BLOCK);
-            tma_load_2d(ring + s * kTile + hf * Lay::kHalf + jb * kBoxRows * 128, tm, hf * 64, row, bar(full0 + s), pol);
+            tma_load_2d(ring + s * kTile + hf * Lay::kHalf + jb * box_rows * 128, tm, hf * 64, row, bar(full0 + s), pol);
           }
         }
         if (is_v && lane == 0) run_done(j);
@@ -795,7 +796,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
         if (lane == 0) run_done(j);
         if (x.ntq == 0) break;
         if (x.t0 >= x.t1) continue;
-        const Common seen(p, x, lens[x.seq], qc[x.seq]);
+        const Common<Tree> seen(p, x, lens[x.seq], qc[x.seq]);
         const int a = slot_of(nq), b = slot_of(nq + 1);
         const bool two = S == 2 && x.ntq == 2;
         // the first product overwrites the accumulator: its last run must have been read
@@ -848,12 +849,11 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
         const int c = qc[x.seq], ctx = lens[x.seq] - c;
         const int tok = r / p.group, token = x.r0 + q * p.tile_tok + tok;
         const bool row_valid = tok < p.tile_tok && token < c;
-        RowSight sight;
-        sight.tree = p.mask != nullptr;
+        RowSight<Tree> sight;
         sight.ctx = ctx;
         sight.word = sight.keep = 0;
         sight.lo = sight.hi = sight.sinks = 0;
-        if (sight.tree) {
+        if (Tree) {
           if (row_valid) {
             sight.word = p.mask[qs[x.seq] + token];
             sight.keep = below(c);
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
         }
         // of the warp's rows, so that few of its tiles need a mask
         const int tile0 = x.r0 + q * p.tile_tok, row0 = (warp & 3) * 32;
-        const Common seen(p, ctx, tile0 + row0 / p.group, min(min(c, tile0 + p.tile_tok) - 1, tile0 + (row0 + 31) / p.group));
+        const Common<Tree> seen(p, ctx, tile0 + row0 / p.group, min(min(c, tile0 + p.tile_tok) - 1, tile0 + (row0 + 31) / p.group));
         const bool idle = __all_sync(0xffffffffu, !row_valid);  // spare rows only
         float m = -INFINITY, l = 0.f;
         const int g0 = g;
@@ -997,14 +997,14 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
 #pragma unroll 1
             for (int t = x.t0; odd && t < x.t1; ++t) {
               const int k0 = x.key0(t);
-              if (Common(p, x, lens[x.seq], c).has(k0)) continue;  // (was not cleared)
+              if (Common<Tree>(p, x, lens[x.seq], c).has(k0)) continue;  // (was not cleared)
 #pragma unroll 1
               for (int k = 0; k < kTK; ++k) {
                 if (!((sight.of(k0) >> k) & 1)) continue;
-                const int b = p.block_tables[static_cast<size_t>(x.seq) * p.max_blocks + (k0 + k) / BS];
+                const int b = p.block_tables[static_cast<size_t>(x.seq) * p.max_blocks + ((k0 + k) >> p.bs_log2)];
                 if (b < 0 || b >= p.num_blocks) continue;
                 const uint32_t *row = reinterpret_cast<const uint32_t *>(
-                    p.v_cache + ((static_cast<size_t>(b) * hkv + x.head) * BS + (k0 + k) % BS) * D + ch * 32);
+                    p.v_cache + (((static_cast<size_t>(b) * hkv + x.head) << p.bs_log2) + ((k0 + k) & ((1 << p.bs_log2) - 1))) * D + ch * 32);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   const uint32_t w = row[i];
@@ -1122,9 +1122,17 @@ Plan make_plan(const Call &a) {
   plan.tile_tok = kRows / plan.group;
   const int longest = a.mask ? a.max_nodes : a.total_q;  // tokens of a chunk or tree, at most
   plan.tile_tok = std::min(plan.tile_tok, std::max(1, longest));
-  // pairs of query tiles where the trees may have two, or the chunks have on average
-  const bool pairs = a.mask ? a.max_nodes > plan.tile_tok
-                            : a.total_q > static_cast<long long>(plan.tile_tok) * a.num_seqs;
+  // Pairs of query tiles where the trees may have two, or the chunks have on average.
+  // At head_dim 64 a pair's products are too short to hide two slots' softmax behind
+  // one issuer, and longer chunks read their keys again in any case (through L2): one
+  // slot, twice per SM, takes 410 us instead of 449 for four prompts of 8192 tokens
+  // with 32 / 8 heads, and 337 instead of 371 for 4096 tokens of 64 / 8 heads.  Chunks
+  // of one pair stay with pairs, which read their keys once: 191 us instead of 200 for
+  // 64 chunks of 64 tokens with windows of 4096; trees too, 106 instead of 116 for 32
+  // trees of 64 nodes on 4096 keys.
+  const long long tile = static_cast<long long>(plan.tile_tok) * a.num_seqs;
+  const bool one = a.head_dim == 64 && a.num_seqs <= kPairedSeqs && a.total_q > 2 * tile;
+  const bool pairs = a.mask ? a.max_nodes > plan.tile_tok : a.total_q > tile && !one;
   plan.slots = pairs || a.num_seqs > kPairedSeqs ? 2 : 1;
   plan.span = pairs ? 2 * plan.tile_tok : plan.tile_tok;
   plan.grid = num_sms() * (3 - plan.slots);
@@ -1148,19 +1156,9 @@ Plan make_plan(const Call &a) {
 using KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Params);
 
 template <int D, int S>
-KernelFn pick_kernel(int block_size) {
-  switch (block_size) {
-    case 16: return spans_tc_kernel<16, D, S>;
-    case 32: return spans_tc_kernel<32, D, S>;
-    case 64: return spans_tc_kernel<64, D, S>;
-    default: return spans_tc_kernel<128, D, S>;
-  }
-}
-
-template <int D, int S>
-int launch(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const Params &p, int block_size,
-           const Plan &plan, cudaStream_t stream) {
-  const KernelFn kernel = pick_kernel<D, S>(block_size);
+int launch(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const Params &p, const Plan &plan,
+           cudaStream_t stream) {
+  const KernelFn kernel = p.mask ? spans_tc_kernel<true, D, S> : spans_tc_kernel<false, D, S>;
   const size_t smem = smem_bytes<D, S>(p.num_seqs);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem_bytes<D, S>(S == 2 ? kMaxSeqs : kPairedSeqs)));
@@ -1203,6 +1201,7 @@ int tc_launch(const Call &a) {
     p.ws_desc = reinterpret_cast<int4 *>(ws + plan.o_bytes + plan.ml_bytes);
   }
   p.status = a.status;
+  while ((1 << p.bs_log2) < a.block_size) ++p.bs_log2;
   p.num_seqs = a.num_seqs;
   p.max_blocks = a.max_blocks;
   p.num_q_heads = a.num_q_heads;
@@ -1222,10 +1221,10 @@ int tc_launch(const Call &a) {
   p.negate = a.scale < 0.f;
   const cudaStream_t st = as_stream(a.stream);
   if (plan.slots == 1)
-    return a.head_dim == 64 ? launch<64, 1>(tmq, tmk, tmv, p, a.block_size, plan, st)
-                            : launch<128, 1>(tmq, tmk, tmv, p, a.block_size, plan, st);
-  return a.head_dim == 64 ? launch<64, 2>(tmq, tmk, tmv, p, a.block_size, plan, st)
-                          : launch<128, 2>(tmq, tmk, tmv, p, a.block_size, plan, st);
+    return a.head_dim == 64 ? launch<64, 1>(tmq, tmk, tmv, p, plan, st)
+                            : launch<128, 1>(tmq, tmk, tmv, p, plan, st);
+  return a.head_dim == 64 ? launch<64, 2>(tmq, tmk, tmv, p, plan, st)
+                          : launch<128, 2>(tmq, tmk, tmv, p, plan, st);
 }
 
 }  // namespace spans
