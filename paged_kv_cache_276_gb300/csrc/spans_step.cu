@@ -606,6 +606,9 @@ int step_launch(const Call &a) {
   const StepPlan plan = make_step_plan(a);
   if (plan.bytes() > 0 && (!a.workspace || a.workspace_bytes < plan.bytes() || !aligned16(a.workspace)))
     return PKV_ERR_WORKSPACE;
+  // a warp's range is found with products of all units and the warps in 64 bits
+  if (static_cast<double>(a.num_seqs) * a.num_kv_heads * (a.max_seq_len / kUnit + 4) * plan.warps > 4e18)
+    return PKV_ERR_UNSUPPORTED;
   const long long rows = static_cast<long long>(a.num_blocks) * a.num_kv_heads * a.block_size;
   CUtensorMap tmk, tmv;
   const int box = std::min(a.block_size, kUnit);

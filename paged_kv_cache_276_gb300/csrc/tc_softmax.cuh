@@ -50,22 +50,9 @@ __device__ __forceinline__ float extreme64(const uint32_t (&v)[64], bool neg) {
   return fmin3(fmin3(e[0], e[1], e[2]), fmin3(e[3], e[4], e[5]), fminf(e[6], e[7]));
 }
 
-// The largest of N raw scores (a multiple of 16).
-template <int N>
-__device__ __forceinline__ float extreme(const uint32_t (&v)[N]) {
-  float e[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) e[q] = fmaxf(__uint_as_float(v[q]), __uint_as_float(v[q + 8]));
-#pragma unroll
-  for (int k = 16; k < N; k += 16)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) e[q] = fmax3(e[q], __uint_as_float(v[k + q]), __uint_as_float(v[k + q + 8]));
-  return fmax3(fmax3(e[0], e[1], e[2]), fmax3(e[3], e[4], e[5]), fmaxf(e[6], e[7]));
-}
-
 // Weights of N raw scores, p = 2^(s * scale * log2e - m), two at a time with a
 // packed fp32 FMA, packed to bf16 pairs; returns the sum of the weights before
-// their rounding to bf16 (the rounding errors, at most 2^-9 of each weight and
+// their rounding to bf16 (the rounding errors, at most 2^-8 of each weight and
 // of either sign, leave the sum's relative error far below the output's bf16
 // step).  Masked keys hold -inf (or +inf for a negative scale): their weight
 // is 2^-inf = 0.

@@ -226,6 +226,52 @@ def test_window_long_prompt():
     b.check(b.sees_window(700, 4))
 
 
+@pytest.mark.parametrize("window,sinks", [(1, 2 ** 31 - 1), (2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (50, 2 ** 31 - 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_window_chunks_largest_windows_and_sinks(d, window, sinks):
+    b = Batch([700, 64, 1], [300, 64, 1], 8, 2, d, 16, seed=3 + d).upload()
+    b.window(window, sinks)
+    b.check(b.sees_window(window, sinks))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("longest,window", [(3, 40), (90, 200)])
+def test_window_chunks_many_sequences(d, longest, window):
+    """More sequences than two CTAs of an SM have room for."""
+    rng = np.random.default_rng(11)
+    chunks = rng.integers(0, longest + 1, 700)
+    lens = chunks + rng.integers(0, 120, 700)
+    b = Batch(lens, chunks, 4, 1, d, 16, seed=12).upload()
+    b.window(window, 3)
+    b.check(b.sees_window(window, 3))
+
+
+@pytest.mark.parametrize("d,chunk", [(64, 600), (128, 600), (64, 16), (128, 16)])
+def test_window_chunks_many_runs(d, chunk):
+    """Several runs per CTA, of tiles of 8 tokens, with and without ones that are cut."""
+    lens = [700, 640, 600, 655]
+    b = Batch(lens, [chunk] * 4, 64, 4, d, 32, seed=13).upload()
+    for window, sinks in ((90, 5), (640, 0)):
+        b.window(window, sinks)
+        b.check(b.sees_window(window, sinks))
+
+
+@pytest.mark.parametrize("single", [False, True])
+def test_blocks_in_several_tables_and_twice_in_one(single):
+    """Shared prefixes, and a block that stands at two places of one sequence."""
+    b = Batch([200, 200, 333], [1] * 3 if single else [40, 7, 90], 8, 2, 128, 16, seed=14)
+    b.tables[1][:10] = b.tables[0][:10]
+    b.tables[2][5] = b.tables[2][3]
+    b.upload()
+    b.window(150, 4, single=single)
+    b.check(b.sees_window(150, 4))
+    if not single:
+        return
+    words = tree_words([1] * 3, b.rng)
+    b.tree(words)
+    b.check(b.sees_tree(words))
+
+
 # ----------------------------------------------------------------------- trees
 @pytest.mark.parametrize("nodes", [1, 2, 7, 8, 26, 33, 63, 64])
 @pytest.mark.parametrize("d,bs", [(64, 16), (64, 64), (128, 16), (128, 32), (128, 128)])
