@@ -745,7 +745,7 @@ int pkv_write_rope_quant(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v
  *   workspace     device, 16-byte aligned, at least
  *                 paged_attention_window_workspace_size(...) bytes (may be NULL
  *                 when that is 0); its contents need not be initialised and are
- *                 not preserved.  Calls that may overlap need one each
+ *                 not preserved.  Calls that may overlap need one each.
  *                 The size is 0 or, where runs of keys may be divided, that of all
  *                 divisions (40 MB at head_dim 128 on 152 SMs); it does not depend
  *                 on num_seqs and total_q (which are there for their checks: sizes
@@ -754,7 +754,7 @@ int pkv_write_rope_quant(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v
  *   everything else as paged_attention_prefill
  * Keys and values that a row does not see never reach its result, whatever they
  * hold (NaN and infinities included).  A row whose visible scores are all -inf
- * gives zeros, as paged_attention_decode.
+ * gives zeros, as paged_attention_decode (where the values it sees are finite).
  * Supported: head_dim in {64, 128}; num_q_heads / num_kv_heads <= 16;
  *   block_size in {16, 32, 64, 128}; num_seqs <= 1024 (65535 with q_start NULL);
  *   max_blocks_per_seq * block_size and num_blocks * num_kv_heads * block_size

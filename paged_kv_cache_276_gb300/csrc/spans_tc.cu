@@ -34,8 +34,8 @@
 // with two slots in a CTA, one CTA per SM: both query tiles of a pair are multiplied
 // against each key and value tile, half the traffic per product (a query tile
 // without a partner goes to the slots in turn).  Batches of one query tile per
-// sequence run with one slot in a CTA, two CTAs per SM, each over runs of its own:
-// while one starts or ends a run the other streams.
+// sequence, and long chunks at head_dim 64, run with one slot in a CTA, two CTAs per
+// SM, each over runs of its own: while one starts or ends a run the other streams.
 //
 // Values that a row does not see must not reach it, and 0 times NaN or infinity is
 // NaN: in a tile that is not seen whole, the P V issuer's warp clears the values no
