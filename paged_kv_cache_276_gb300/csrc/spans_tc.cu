@@ -160,6 +160,8 @@ struct Params {
 // flags of a descriptor
 constexpr int kLeaves = 1;  // the CTA's last run goes on in the next CTA (piece 1 holds its start)
 constexpr int kEnds = 2;    // the run that the CTA goes on with (piece 0) ends here
+// in the place of a piece's sum: it holds no key tile, and its O was not written
+constexpr float kNoTile = -1.f;
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -1048,7 +1050,7 @@ __global__ void __launch_bounds__(Layout<D, S>::kThreads, Layout<D, S>::kCtasPer
           tc::fence_before();
           mbar_arrive(bar(BI::kOFree + slot));
         }
-        if (!whole && row_valid) p.ws_ml[piece * p.piece_rows + prow] = make_float2(m, l);
+        if (!whole && row_valid) p.ws_ml[piece * p.piece_rows + prow] = make_float2(m, any ? l : kNoTile);
         __syncwarp();
         if (lane == 0) run_done(j);
       }
@@ -1098,7 +1100,7 @@ __global__ void __launch_bounds__(2 * kRows) spans_join_kernel(const Params p, i
       // piece 1 of the first CTA, piece 0 of the others
       const int c = i0 + i;
       const size_t at = 2 * (static_cast<size_t>(blockIdx.x) + c) + (c == 0 ? 1 : 0);
-      ml[i] = make_float2(-INFINITY, 0.f);
+      ml[i] = make_float2(-INFINITY, kNoTile);
       if (c < pieces) {
         ml[i] = p.ws_ml[at * p.piece_rows + prow];
 #pragma unroll
@@ -1115,9 +1117,11 @@ __global__ void __launch_bounds__(2 * kRows) spans_join_kernel(const Params p, i
     for (int k = 0; k < kCols; ++k) acc[k].x *= keep, acc[k].y *= keep, acc[k].z *= keep, acc[k].w *= keep;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      // an empty piece (max -inf) weighs nothing, and its O was not written
+      // Every piece with a tile takes part, also at a factor of 0: one whose scores are all
+      // NaN has the maximum -inf too, and its sum and O (NaN) must reach the row, as must
+      // what is not finite in a piece far below the maximum.
+      if (ml[i].y == kNoTile) continue;
       const float f = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - M);
-      if (f == 0.f) continue;
       den += ml[i].y * f;
 #pragma unroll
       for (int k = 0; k < kCols; ++k) {
