@@ -255,7 +255,7 @@ struct Common {
       hi = ctx;
     } else {
       hi = ctx + first + 1;
-      lo = max(0, ctx + last - p.window + 1);
+      lo = max(0, max(0, ctx + last + 1) - p.window);  // (a row may stand before the first token)
       sinks = min(p.sinks, hi);
     }
   }

@@ -1,6 +1,8 @@
-"""Windowed and tree attention at the ends of their integers: block ids as large as their type holds."""
+"""Windowed and tree attention at the ends of their integers: block ids and windows as large as their types hold."""
+import numpy as np
 import pytest
 
+from oracle import spans as OS
 from test_gpu_spans import Batch, bits, built, check  # noqa: F401 (built: the module's fixture)
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +33,17 @@ def test_bad_block_ids_are_reported_and_not_read(d, bs, form, bad):
     b.k[b.tables[0, e]] = b.v[b.tables[0, e]] = 0
     ref, mag, dot = b.expect(sees)
     check(bits(b.out)[:c], ref[:c], mag[:c], dot[:c], 900, d)
+
+
+@pytest.mark.parametrize("window,sinks", [(LARGEST, 0), (LARGEST, LARGEST), (LARGEST - 1, 5), (1, LARGEST)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_largest_windows_of_chunks_longer_than_their_sequence(d, window, sinks):
+    """Rows that stand before the first token, further from it than the window's type has room for."""
+    lens, chunks = [10, 0, 130, 64], [300, 40, 500, 65]
+    b = Batch(lens, chunks, 4, 2, d, 16, seed=52).upload()
+    b.window(window, sinks)
+    sees = [np.zeros((c, L), bool) for c, L in zip(chunks, lens)]
+    for s, c, L in zip(sees, chunks, lens):
+        s[c - min(c, L):] = OS.window_sees(L, min(c, L), window, sinks)
+    b.check(sees)
+    assert not bits(b.out)[:290].any() and not bits(b.out)[300:340].any()
