@@ -1,4 +1,5 @@
-// Launch with programmatic stream serialisation, for the 8-bit cache's kernels.
+// Launch with programmatic stream serialisation, for the kernels of the 8-bit cache,
+// the rotary append, and the windowed and tree attention.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -50,17 +50,18 @@ __device__ __forceinline__ float extreme64(const uint32_t (&v)[64], bool neg) {
   return fmin3(fmin3(e[0], e[1], e[2]), fmin3(e[3], e[4], e[5]), fminf(e[6], e[7]));
 }
 
-// Weights of N raw scores, p = 2^(s * scale * log2e - m), two at a time with a
+// Weights of 64 raw scores, p = 2^(s * scale * log2e - m), two at a time with a
 // packed fp32 FMA, packed to bf16 pairs; returns the sum of the weights before
-// their rounding to bf16 (the rounding errors, at most 2^-8 of each weight and
-// of either sign, leave the sum's relative error far below the output's bf16
-// step).  Masked keys hold -inf (or +inf for a negative scale): their weight
-// is 2^-inf = 0.
-template <int N>
-__device__ __forceinline__ float weights(const uint32_t *v, uint64_t ks2, uint64_t nm2, uint32_t *pk) {
+// their rounding to bf16.  They are rounded because a matrix instruction takes
+// both operands in one 16-bit type and the values are bf16 (fp16 does not hold
+// their range); weights as two bf16 terms would double the P V products.  The
+// rounding errors, at most 2^-8 of each weight and of either sign, leave the sum's
+// relative error far below the output's bf16 step.  Masked keys hold -inf (or
+// +inf for a negative scale): their weight is 2^-inf = 0.
+__device__ __forceinline__ float weights64(const uint32_t (&v)[64], uint64_t ks2, uint64_t nm2, uint32_t (&pk)[32]) {
   uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};  // four packed partial sums (0 bits = +0.0)
 #pragma unroll
-  for (int c = 0; c < N / 2; ++c) {
+  for (int c = 0; c < 32; ++c) {
     float x0, x1;
     f32x2_split(ffma2(f32x2_bits(v[2 * c], v[2 * c + 1]), ks2, nm2), x0, x1);
     const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
@@ -79,10 +80,6 @@ __device__ __forceinline__ float weights(const uint32_t *v, uint64_t ks2, uint64
 // parks the warp until the phase completes (or a short hardware window ends).
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-}
-
-__device__ __forceinline__ float weights64(const uint32_t (&v)[64], uint64_t ks2, uint64_t nm2, uint32_t (&pk)[32]) {
-  return weights<64>(v, ks2, nm2, pk);
 }
 
 }  // namespace pkv
