@@ -754,9 +754,11 @@ int pkv_write_rope_quant(const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v
  *   everything else as paged_attention_prefill
  * Keys and values that a row does not see never reach its result, whatever they
  * hold (NaN and infinities included).  A row whose visible scores are all -inf
- * gives zeros, as paged_attention_decode (where the values it sees are finite).
+ * gives zeros, as paged_attention_decode (where the values it sees are finite);
+ * one with a visible score that is NaN gives NaN, however its keys are divided.
  * Weighted values are summed in fp32 before they are normalised, with weights of
- * up to 2^20: values above 2^107 / (keys seen) in magnitude may give infinities.
+ * up to 2^20 (q_start NULL: 2^8): values above 2^107 (2^119) / (keys seen) in
+ * magnitude may give infinities.
  * Supported: head_dim in {64, 128}; num_q_heads / num_kv_heads <= 16;
  *   block_size in {16, 32, 64, 128}; num_seqs <= 1024 (65535 with q_start NULL);
  *   max_blocks_per_seq * block_size and num_blocks * num_kv_heads * block_size

@@ -18,9 +18,10 @@
 // The lane's cosines and sines are read once for its kRows rows, whose loads are
 // all in flight together.
 // Measured at 32768 tokens, 32 query and 8 KV heads of 128, rows of a fused
-// projection: 119.6 us (6.9 TB/s, a plain copy 6.79); 8192 tokens, 64 and 8 heads,
-// into the 8-bit cache: 53.4 us (6.1 TB/s; the conversions leave the loads of a warp
-// waiting); the 256 tokens of a decode step 3.3 us, a launch and two dependent loads.
+// projection: 119.6 us (6.9 TB/s of what is read and written, a plain copy 6.78; an eighth
+// of the writes is still in L2 at the end); 8192 tokens, 64 and 8 heads, into the 8-bit
+// cache: 53.4 us (6.05 TB/s; the conversions leave the loads of a warp waiting); the 256
+// tokens of a decode step 3.4 us, a launch and two dependent loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

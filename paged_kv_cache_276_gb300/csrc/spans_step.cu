@@ -23,7 +23,7 @@
 //
 // Measured (clocks at 2070 MHz, of a copy's 6.78 TB/s): 256 sequences of mixed lengths,
 // window 1024 and 4 sinks, 32 / 8 heads of 128: 103 to 105 us, 5.8 TB/s; 16 sequences of
-// 32768 tokens, window 4096, 64 / 8 heads: 48 us, 5.6 TB/s.  On the tensor cores' kernel
+// 32768 tokens, window 4096, 64 / 8 heads: 48 to 49 us, 5.5 TB/s.  On the tensor cores' kernel
 // (spans_tc.cu with tiles of one token) they take 142 and 60 us: a tile of 128 rows holds
 // G that are used, and one CTA keeps fewer copies in flight than these warps' rings.
 // What is left is the start (dependent loads of lengths and tables, about 3 us) and the
@@ -224,7 +224,8 @@ __device__ __forceinline__ void attend_unit(Acc<D, NT> &acc, const uint32_t (&qf
         }
       }
   }
-  // weights: summed in fp32 as they are, rounded to bf16 for the product with the values
+  // weights: summed in fp32 as they are, rounded to bf16 for the product with the values (both
+  // operands of a matrix instruction have one 16-bit type, and fp16 does not hold bf16 values)
   uint32_t pb[MT][NT][2];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
