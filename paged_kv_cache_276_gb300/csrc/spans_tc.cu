@@ -55,10 +55,10 @@
 // overlap, and what they wait for each other is the rest.  A run's end takes a slot about
 // 7000 clocks (the last product, the rows' output, the next descriptor).
 // Measured (clocks at 2070 MHz): four prompts of 8192 tokens, 32 / 8 heads of 128, window
-// 1024: 492 to 502 us by the card, 1.03 to 1.05 PFLOP/s of the visible products; a tree of 64 nodes on 32768 tokens,
-// 64 / 8 heads: 66 to 67 us, 1.02 PFLOP/s; 256 trees of 8 nodes on 215 k tokens, 32 / 8 heads:
-// 157 to 158 us, 5.7 TB/s.  In a tree's batch the products fit beside the copies while a node's
-// G heads fill few rows, and HBM is the bound.
+// 1024: 492 to 502 us by the card, 1.03 to 1.05 PFLOP/s of the visible products; a tree of
+// 64 nodes on 32768 tokens, 64 / 8 heads: 66 to 67 us, 1.02 PFLOP/s; 256 trees of 8 nodes on
+// 215 k tokens, 32 / 8 heads: 157 to 158 us, 5.7 TB/s.  In a tree's batch the products fit
+// beside the copies while a node's G heads fill few rows, and HBM is the bound.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
